@@ -517,6 +517,153 @@ int moe_mxfp4_grouped(const uint8_t* x_q, const uint8_t* x_scale, const int32_t*
                       uint16_t* out_bf16, uint8_t* out_q, uint8_t* out_scale, int64_t T, int64_t H, int64_t I,
                       int64_t E, int64_t topk, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * NVFP4, and products with 4-bit weights in the default maths
+ *
+ * The 4-bit model page's own format (Lernex/Metis-1.6-Praxis-NVFP4, "What is
+ * in NVFP4"): E2M1 values, an E4M3 scale per 16 consecutive inputs and a
+ * float32 scale per expert. Codes are packed as for MXFP4 above (element 2i
+ * in the low nibble of byte i); a row of K values is K/2 code bytes and K/16
+ * scale bytes. The value of a code is dec(code) * dec(block scale) * gscale.
+ * Without fast-math the page's runtime widens 4-bit weights to 16 bits as it
+ * multiplies and keeps the activations in BF16 (same page, "What --fast-math
+ * does"); these calls do that for NVFP4 and MXFP4 weights.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of scratch nvfp4_quantize needs when it finds the group scales
+ * itself (0 for invalid sizes). */
+size_t nvfp4_quantize_workspace_bytes(int64_t G, int64_t R, int64_t K);
+
+/*
+ * nvfp4_quantize — G groups (matrices, experts) of R rows of K BF16 values ->
+ * codes, block scales and one float32 scale per group. With every quotient
+ * and product rounded once to float32:
+ *   gscale[g]  = max(max|x_g| / 2688, 2^-96), 1 for an all-zero group
+ *                (2688 = 6 * 448), or the caller's value
+ *   scale[b]   = E4M3(min((max|x_b| / 6) / gscale, 448))    nearest even
+ *   d          = dec(scale[b]) * gscale
+ *   q          = E2M1(x / d), nearest, ties to even, saturating at 6;
+ *                0 with the sign of x where d == 0
+ * Bit-exact and deterministic.
+ *   x_bf16  [G, R, K]    q_fp4 [G, R, K/2]    scale_e4m3 [G, R, K/16]
+ *   gscale  [G]; written, or read where gscale_given != 0 (values between
+ *           2^-96 and 2^112; a block whose scale would pass 448 saturates)
+ *   workspace  nvfp4_quantize_workspace_bytes bytes; may be NULL where
+ *           gscale_given != 0
+ *   K a positive multiple of 16, R * K at most 2^40, at most 2^31 - 1 chunks
+ *   of 32768 values in all.
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, WORKSPACE, DEVICE,
+ *         LAUNCH.
+ */
+int nvfp4_quantize(const uint16_t* x_bf16, int64_t G, int64_t R, int64_t K, uint8_t* q_fp4, uint8_t* scale_e4m3,
+                   float* gscale, int gscale_given, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * nvfp4_dequantize — the values back: y = bf16(fl32(dec(q) * d)), d as above.
+ *   Shapes, limits and errors as nvfp4_quantize (no workspace).
+ */
+int nvfp4_dequantize(const uint8_t* q_fp4, const uint8_t* scale_e4m3, const float* gscale, int64_t G, int64_t R,
+                     int64_t K, uint16_t* y_bf16, hipStream_t stream);
+
+/*
+ * nvfp4_gemm, mxfp4_gemm — BF16 activations times 4-bit weights:
+ *   nvfp4: y[m,n] = bf16( gscale * sum_k x[m,k] * dec(w_scale[n,k/16]) * dec(w_q[n,k]) )
+ *   mxfp4: y[m,n] = bf16( sum_k x[m,k] * 2^(w_scale[n,k/32] - 127) * dec(w_q[n,k]) )
+ * A code times its block scale is exact in BF16, products are exact in
+ * float32, sums are float32, gscale is applied in float32 and the result is
+ * rounded to nearest even. M <= 32 runs a weight-streaming kernel, larger M a
+ * tiled one.
+ *   x_bf16 [M, K]; w_q [N, K/2]; w_scale [N, K/16] or [N, K/32]
+ *   w_gscale  [1] float32, on the device, 4-byte aligned (it may be an element
+ *             of a vector)
+ *   y_bf16 [M, N] (must not overlap the inputs)
+ *   K a positive multiple of 32, N of 16; K, N <= 2^20, M <= 2^24
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, DEVICE, LAUNCH.
+ */
+int nvfp4_gemm(const uint16_t* x_bf16, const uint8_t* w_q, const uint8_t* w_scale, const float* w_gscale,
+               uint16_t* y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+int mxfp4_gemm(const uint16_t* x_bf16, const uint8_t* w_q, const uint8_t* w_scale, uint16_t* y_bf16, int64_t M,
+               int64_t N, int64_t K, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Router, and routed experts for a few tokens in the default maths
+ *
+ * The pages' router picks the top experts of every token in float32 with a
+ * balance bias (Lernex/Metis-1.6-Praxis, "Architecture"; sglang-metis 0.1.0,
+ * "How the model maps onto SGLang"), and a step with few tokens runs in the
+ * default maths: BF16 activations, weights widened as they are multiplied
+ * (Lernex/Metis-1.6-Logos-FP8, "What --fast-math does"). Readings where the
+ * pages are silent: the bias moves the choice and not the weights; weights
+ * may be renormalised over the chosen experts.
+ * ------------------------------------------------------------------------- */
+
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+/*
+ * moe_router — the experts of every token and their weights:
+ *   l[t,e]  = sum_k x[t,k] * w_router[e,k]     exact products, float64 sums
+ *   s       = softmax over e of l, or sigmoid(l)              (float64)
+ *   ids[t]  = the topk experts with the largest s + bias, in that order, the
+ *             lower index first where they are equal (a NaN comes last)
+ *   w[t,j]  = route_scale * s[ids[t,j]], divided by the sum over j of s where
+ *             renormalize != 0; rounded once to float32
+ * The choice does not depend on T.
+ *   x_bf16 [T, H]; w_router [E, H] BF16; bias [E] float32 or NULL
+ *   topk_ids [T, topk] int32; topk_w [T, topk] float32
+ *   1 <= topk <= min(E, 64), E <= 1024, H a positive multiple of 8,
+ *   E * H <= 2^29, H <= 2^20, T <= 2^24
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, DEVICE, LAUNCH.
+ */
+int moe_router(const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int32_t* topk_ids, float* topk_w,
+               int64_t T, int64_t H, int64_t E, int64_t topk, int score, int renormalize, float route_scale,
+               hipStream_t stream);
+
+/* Weight formats of the few-token calls. */
+enum { MOE_FP8 = 0, MOE_MXFP4 = 1, MOE_NVFP4 = 2 };
+
+/* Bytes of scratch the few-token calls need: T * topk * I * 4 (0 for sizes
+ * they do not take). */
+size_t moe_few_tokens_workspace_bytes(int format, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
+
+/*
+ * moe_few_tokens — one routed-expert pass for at most 64 tokens:
+ *   g, u   = gate and up halves of W13[e] . x[t]          (float32)
+ *   h      = silu(g) * u                                  (float32, carried
+ *            as the sum of two BF16 values, 16 significant bits)
+ *   out[t] = bf16( sum over j with a valid id of topk_w[t,j] * (W2[e] . h) )
+ * Sums are float32 in an order fixed by the ids; a token that names an expert
+ * twice counts it with the sum of the two weights; a token without a valid id
+ * gets zeros. Every picked expert's weights are read once.
+ *   x_bf16 [T, H]; topk_ids, topk_w [T, topk]; ids outside [0, E) are dropped
+ *   format    w13_q        w13_scale               w13_gscale
+ *   MOE_FP8   [E, 2I, H]   float32 [E, 2I]         NULL
+ *   MOE_MXFP4 [E, 2I, H/2] E8M0 [E, 2I, H/32]      NULL
+ *   MOE_NVFP4 [E, 2I, H/2] E4M3 [E, 2I, H/16]      float32 [E]
+ *   w2_q [E, H, I] or [E, H, I/2] with scales likewise (along I)
+ *   out_bf16 [T, H]
+ *   workspace  moe_few_tokens_workspace_bytes bytes; calls that may overlap
+ *              need one each
+ *   T <= 64, T * topk <= 1024, E <= 1024, H and I positive multiples of 32,
+ *   2 * I * H below 2^31, T * topk * I below 2^29
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED (also another format), MISALIGNED,
+ *         WORKSPACE, DEVICE, LAUNCH.
+ */
+int moe_few_tokens(int format, const uint16_t* x_bf16, const int32_t* topk_ids, const float* topk_w,
+                   const uint8_t* w13_q, const void* w13_scale, const float* w13_gscale, const uint8_t* w2_q,
+                   const void* w2_scale, const float* w2_gscale, uint16_t* out_bf16, int64_t T, int64_t H, int64_t I,
+                   int64_t E, int64_t topk, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_few_tokens_layer — the whole layer: moe_router, then moe_few_tokens on
+ * its choice, which is left in topk_ids / topk_w. Arguments, limits and
+ * errors of both.
+ */
+int moe_few_tokens_layer(int format, const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int score,
+                         int renormalize, float route_scale, int32_t* topk_ids, float* topk_w, const uint8_t* w13_q,
+                         const void* w13_scale, const float* w13_gscale, const uint8_t* w2_q, const void* w2_scale,
+                         const float* w2_gscale, uint16_t* out_bf16, int64_t T, int64_t H, int64_t I, int64_t E,
+                         int64_t topk, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

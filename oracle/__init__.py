@@ -27,6 +27,10 @@ What it defines, and where the pages state it:
   (Lernex/Metis-1.6-Praxis-NVFP4, "What is in NVFP4": E2M1 values with a
   scale per small block; "What --fast-math does": expert inputs rounded to
   FP4), its block quantiser, linear layer and routed-expert pass.
+* NVFP4 (``nvfp4``): the 4-bit checkpoint's own format, its quantiser and the
+  product of BF16 activations with 4-bit weights (same page).
+* The router and the default-maths routed-expert pass of a step with few
+  tokens (``few``).
 * The routed-expert chain (``moe``): routed experts in FP8 with the same
   scheme, top-k routing, the stack run twice with shared weights
   (Lernex/Metis-1.6-Praxis, "Architecture"; sglang-metis 0.1.0, "How the
@@ -46,11 +50,14 @@ from .linear import w8a8_linear, w8a8_linear_int, w8a16_linear
 from .moe import (route, grouped_gate_up, moe_pass, moe_two_pass, swiglu_f32, bf16_values, combine_copies)
 from .mxfp4 import (e2m1_decode, e2m1_encode, e8m0_value, mx_dequant, mx_quantize_rows, mx_unpack, mxfp4_linear,
                     moe_mxfp4_pass, moe_mxfp4_two_pass)
+from .nvfp4 import NVFP4_GSCALE_MIN, nvfp4_quantize, nvfp4_scaled, nvfp4_dequant_f32, w4a16_linear
+from .few import router, wide_pass
 
 __all__ = [
     "E4M3_MAX", "decode", "decode_table", "encode", "encode_bits", "finite_codes", "magnitudes",
     "bf16_bits_to_f64", "round_to_bf16_bits", "bf16_bits_to_f32", "quantize_rows",
     "w8a8_linear", "w8a8_linear_int", "w8a16_linear", "route", "grouped_gate_up", "moe_pass", "moe_two_pass",
     "swiglu_f32", "bf16_values", "combine_copies", "e2m1_decode", "e2m1_encode", "e8m0_value", "mx_dequant", "mx_quantize_rows", "mx_unpack",
-    "mxfp4_linear", "moe_mxfp4_pass", "moe_mxfp4_two_pass",
+    "mxfp4_linear", "moe_mxfp4_pass", "moe_mxfp4_two_pass", "NVFP4_GSCALE_MIN", "nvfp4_quantize", "nvfp4_scaled",
+    "nvfp4_dequant_f32", "w4a16_linear", "router", "wide_pass",
 ]

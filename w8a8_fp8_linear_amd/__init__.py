@@ -20,6 +20,8 @@ __all__ = [
     "quantize_per_token", "w8a8_gemm", "w8a8_linear", "quantize_weight",
     "moe_route", "moe_gate_up_bf16", "moe_gate_up_swiglu_quant", "moe_down_combine",
     "w8a8_grouped_gemm", "moe_w8a8_grouped", "moe_workspace", "moe_ffn",
+    "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_gemm", "mxfp4_gemm",
+    "moe_router", "moe_few_tokens", "moe_few_tokens_layer", "moe_few_tokens_workspace", "moe_few_tokens_ffn",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -68,6 +70,19 @@ _SIGNATURES = {
     "moe_mxfp4_down_combine": (ctypes.c_int, [_c_ptr] * 12 + [_c_i64] * 5 + [ctypes.c_int, _c_ptr]),
     "moe_mxfp4_workspace_bytes": (ctypes.c_size_t, [_c_i64] * 5),
     "moe_mxfp4_grouped": (ctypes.c_int, [_c_ptr] * 11 + [_c_i64] * 5 + [_c_ptr, ctypes.c_size_t, _c_ptr]),
+    "nvfp4_quantize_workspace_bytes": (ctypes.c_size_t, [_c_i64] * 3),
+    "nvfp4_quantize": (ctypes.c_int, [_c_ptr] + [_c_i64] * 3 + [_c_ptr] * 3 + [ctypes.c_int, _c_ptr, ctypes.c_size_t,
+                                                                              _c_ptr]),
+    "nvfp4_dequantize": (ctypes.c_int, [_c_ptr] * 3 + [_c_i64] * 3 + [_c_ptr] * 2),
+    "nvfp4_gemm": (ctypes.c_int, [_c_ptr] * 5 + [_c_i64] * 3 + [_c_ptr]),
+    "mxfp4_gemm": (ctypes.c_int, [_c_ptr] * 4 + [_c_i64] * 3 + [_c_ptr]),
+    "moe_router": (ctypes.c_int, [_c_ptr] * 5 + [_c_i64] * 4 + [ctypes.c_int, ctypes.c_int, ctypes.c_float, _c_ptr]),
+    "moe_few_tokens_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] + [_c_i64] * 5),
+    "moe_few_tokens": (ctypes.c_int, [ctypes.c_int] + [_c_ptr] * 10 + [_c_i64] * 5 + [_c_ptr, ctypes.c_size_t,
+                                                                                    _c_ptr]),
+    "moe_few_tokens_layer": (ctypes.c_int, [ctypes.c_int] + [_c_ptr] * 3 + [ctypes.c_int, ctypes.c_int,
+                                                                           ctypes.c_float]
+                             + [_c_ptr] * 9 + [_c_i64] * 5 + [_c_ptr, ctypes.c_size_t, _c_ptr]),
 }
 
 
@@ -755,4 +770,274 @@ def moe_mxfp4_ffn(x, routes, w13_q, w13_scale, w2_q, w2_scale, workspace=None):
         else:
             out, xq, xs = r
             outs.append(out)
+    return outs
+
+
+# ---- NVFP4, 4-bit weights in the default maths ------------------------------------
+#
+# NVFP4 codes are packed as MXFP4's; scales are uint8 E4M3 with one byte per
+# 16 values along K and one float32 per matrix: q [.., K/2], scale [.., K/16],
+# gscale [groups].
+
+
+def _same_device(x, *named):
+    """The arguments of a call, each (tensor, dtype, shape, name): checked
+    against x's device, their type and shape; all contiguous. Returns x's
+    device index."""
+    if not x.is_cuda:
+        raise ValueError("x must be on a GPU")
+    dev = x.get_device()
+    for t, dtype, shape, name in named:
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the device of x")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    return dev
+
+
+def _call(dev: int, name: str, *args):
+    """The library's call on device ``dev`` and its current stream."""
+    import torch
+
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev:
+        _check(name, getattr(lib(), name)(*args, stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(name, getattr(lib(), name)(*args, stream))
+
+
+def _nvfp4_groups(shape):
+    if len(shape) not in (2, 3):
+        raise ValueError("[M, K] or [G, R, K] expected")
+    return (shape if len(shape) == 3 else (1,) + tuple(shape))
+
+
+def nvfp4_quantize(x, gscale=None, q=None, scale=None, workspace=None):
+    """BF16 [M, K] (one group) or [G, R, K] -> (codes uint8 [.., K/2], E4M3 scales
+    uint8 [.., K/16], float32 scales [groups]). A group's float32 scale is
+    found from its largest value, or given as ``gscale``."""
+    import torch
+
+    G, R, K = _nvfp4_groups(tuple(x.shape))
+    lead = tuple(x.shape[:-1])
+    given = gscale is not None
+    if K % 16:
+        raise ValueError("K must be a multiple of 16")
+    if q is None:
+        q = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty(lead + (K // 16,), dtype=torch.uint8, device=x.device)
+    if gscale is None:
+        gscale = torch.empty((G,), dtype=torch.float32, device=x.device)
+    dev = _same_device(x, (x, torch.bfloat16, lead + (K,), "x"), (q, torch.uint8, lead + (K // 2,), "q"),
+                       (scale, torch.uint8, lead + (K // 16,), "scale"), (gscale, torch.float32, (G,), "gscale"))
+    if workspace is None and not given:
+        workspace = torch.empty(max(int(lib().nvfp4_quantize_workspace_bytes(G, R, K)), 16), dtype=torch.uint8,
+                                device=x.device)
+    _call(dev, "nvfp4_quantize", x.data_ptr(), G, R, K, q.data_ptr(), scale.data_ptr(), gscale.data_ptr(), int(given),
+          *_workspace_args(workspace, dev))
+    return q, scale, gscale
+
+
+def _workspace_args(workspace, dev):
+    """(pointer, bytes) of a caller's or an own workspace; (None, 0) without one."""
+    import torch
+
+    if workspace is None:
+        return None, 0
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the device of x")
+    return workspace.data_ptr(), workspace.numel()
+
+
+def nvfp4_dequantize(q, scale, gscale, out=None):
+    """NVFP4 codes [.., K/2], scales [.., K/16] and float32 scales [groups] -> BF16 [.., K]."""
+    import torch
+
+    G, R, Kh = _nvfp4_groups(tuple(q.shape))
+    lead, K = tuple(q.shape[:-1]), 2 * Kh
+    if K % 16:
+        raise ValueError("K must be a multiple of 16")
+    if out is None:
+        out = torch.empty(lead + (K,), dtype=torch.bfloat16, device=q.device)
+    dev = _same_device(q, (q, torch.uint8, lead + (Kh,), "q"), (scale, torch.uint8, lead + (K // 16,), "scale"),
+                       (gscale, torch.float32, (G,), "gscale"), (out, torch.bfloat16, lead + (K,), "out"))
+    _call(dev, "nvfp4_dequantize", q.data_ptr(), scale.data_ptr(), gscale.data_ptr(), G, R, K, out.data_ptr())
+    return out
+
+
+def nvfp4_gemm(x, w_q, w_scale, w_gscale, out=None):
+    """Default maths on NVFP4 weights: y[m, n] = bf16(w_gscale * sum_k x[m, k] * dec(w_scale) * dec(w_q[n, k])),
+    x BF16 [M, K], w_q [N, K/2], w_scale [N, K/16] (E4M3), w_gscale one float32 (on the GPU)."""
+    import torch
+
+    M, K = x.shape
+    N = w_q.shape[0]
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    dev = _same_device(x, (x, torch.bfloat16, (M, K), "x"), (w_q, torch.uint8, (N, K // 2), "w_q"),
+                       (w_scale, torch.uint8, (N, K // 16), "w_scale"), (out, torch.bfloat16, (M, N), "out"))
+    if w_gscale.dtype is not torch.float32 or w_gscale.numel() != 1 or w_gscale.get_device() != dev:
+        raise ValueError("w_gscale must be one float32 on the device of x")
+    _call(dev, "nvfp4_gemm", x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), w_gscale.data_ptr(), out.data_ptr(), M,
+          N, K)
+    return out
+
+
+def mxfp4_gemm(x, w_q, w_scale, out=None):
+    """Default maths on MXFP4 weights: y[m, n] = bf16(sum_k x[m, k] * 2^(w_scale - 127) * dec(w_q[n, k])),
+    x BF16 [M, K], w_q [N, K/2], w_scale [N, K/32] (E8M0)."""
+    import torch
+
+    M, K = x.shape
+    N = w_q.shape[0]
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    dev = _same_device(x, (x, torch.bfloat16, (M, K), "x"), (w_q, torch.uint8, (N, K // 2), "w_q"),
+                       (w_scale, torch.uint8, (N, K // 32), "w_scale"), (out, torch.bfloat16, (M, N), "out"))
+    _call(dev, "mxfp4_gemm", x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), out.data_ptr(), M, N, K)
+    return out
+
+
+# ---- router, and routed experts for a few tokens in the default maths --------------
+#
+# Expert weights travel as a tuple per projection: FP8 (codes [E, rows, K],
+# float32 [E, rows]); MXFP4 (codes [E, rows, K/2], E8M0 [E, rows, K/32]);
+# NVFP4 (codes [E, rows, K/2], E4M3 [E, rows, K/16], float32 [E]).
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_FP8, _MXFP4, _NVFP4 = 0, 1, 2
+
+
+def moe_router(x, w_router, topk: int, bias=None, score="softmax", renormalize=True, route_scale=1.0, ids=None,
+               weights=None):
+    """The experts of every token: (ids int32 [T, topk], weights float32 [T, topk]).
+
+    The score is softmax or sigmoid of x . w_router^T (float64 sums); the
+    choice goes by score + bias, larger first, the lower id where they are
+    equal; the weights are the scores of the chosen, renormalised to sum to
+    one if asked, times ``route_scale``."""
+    import torch
+
+    T, H = x.shape
+    E = w_router.shape[0]
+    if ids is None:
+        ids = torch.empty((T, topk), dtype=torch.int32, device=x.device)
+    if weights is None:
+        weights = torch.empty((T, topk), dtype=torch.float32, device=x.device)
+    dev = _same_device(x, (x, torch.bfloat16, (T, H), "x"), (w_router, torch.bfloat16, (E, H), "w_router"),
+                       (ids, torch.int32, (T, topk), "ids"), (weights, torch.float32, (T, topk), "weights"),
+                       *(((bias, torch.float32, (E,), "bias"),) if bias is not None else ()))
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    _call(dev, "moe_router", x.data_ptr(), w_router.data_ptr(), bias.data_ptr() if bias is not None else None,
+          ids.data_ptr(), weights.data_ptr(), T, H, E, topk, _SCORES[score], int(renormalize), route_scale)
+    return ids, weights
+
+
+def _expert_format(w13, H: int):
+    """The weight format by the tuple and its shapes."""
+    if len(w13) == 3:
+        return _NVFP4
+    return _FP8 if w13[0].shape[2] == H else _MXFP4
+
+
+def _expert_specs(fmt, w, name, E, rows, K):
+    import torch
+
+    if fmt == _FP8:
+        return ((w[0], torch.uint8, (E, rows, K), f"{name} codes"),
+                (w[1], torch.float32, (E, rows), f"{name} scales"))
+    if fmt == _MXFP4:
+        return ((w[0], torch.uint8, (E, rows, K // 2), f"{name} codes"),
+                (w[1], torch.uint8, (E, rows, K // 32), f"{name} scales"))
+    return ((w[0], torch.uint8, (E, rows, K // 2), f"{name} codes"),
+            (w[1], torch.uint8, (E, rows, K // 16), f"{name} scales"), (w[2], torch.float32, (E,), f"{name} gscale"))
+
+
+def _few_args(x, ids, weights, w13, w2, out, workspace, topk):
+    """Checked arguments of the few-token calls: (device, format, expert
+    pointers, out, sizes, workspace arguments)."""
+    import torch
+
+    T, H = x.shape
+    if len(w13) not in (2, 3) or len(w13) != len(w2):
+        raise ValueError("w13 and w2 must both be (codes, scales) or (codes, scales, gscale)")
+    if w13[0].dim() != 3 or w2[0].dim() != 3:
+        raise ValueError("expert codes must have 3 dims")
+    fmt = _expert_format(w13, H)
+    E, twoI = w13[0].shape[:2]
+    I = twoI // 2
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    dev = _same_device(x, (x, torch.bfloat16, (T, H), "x"), (ids, torch.int32, (T, topk), "topk_ids"),
+                       (weights, torch.float32, (T, topk), "topk_w"), (out, torch.bfloat16, (T, H), "out"),
+                       *_expert_specs(fmt, w13, "w13", E, 2 * I, H), *_expert_specs(fmt, w2, "w2", E, H, I))
+    if workspace is None:
+        workspace = moe_few_tokens_workspace(T, I, topk, x.device)
+    experts = (w13[0].data_ptr(), w13[1].data_ptr(), w13[2].data_ptr() if fmt == _NVFP4 else None,
+               w2[0].data_ptr(), w2[1].data_ptr(), w2[2].data_ptr() if fmt == _NVFP4 else None)
+    return dev, fmt, experts, out, (T, H, I, E, topk), _workspace_args(workspace, dev)
+
+
+def moe_few_tokens_workspace(T: int, I: int, topk: int, device="cuda"):
+    """Scratch buffer sized for moe_few_tokens and moe_few_tokens_layer."""
+    import torch
+
+    return torch.empty(max(T * topk * I * 4, 16), dtype=torch.uint8, device=device)
+
+
+def moe_few_tokens(x, topk_ids, topk_w, w13, w2, out=None, workspace=None):
+    """One routed-expert pass in the default maths for at most 64 tokens: BF16 [T, H].
+
+    x BF16 [T, H] as it is, the experts' FP8, MXFP4 or NVFP4 weights widened
+    as they are multiplied; h = silu(g) * u is not rounded below 16 bits and a
+    token's weighted sum is rounded to BF16 once."""
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be [T, k]")
+    dev, fmt, experts, out, sizes, ws = _few_args(x, topk_ids, topk_w, w13, w2, out, workspace, topk_ids.shape[1])
+    _call(dev, "moe_few_tokens", fmt, x.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(), *experts, out.data_ptr(),
+          *sizes, *ws)
+    return out
+
+
+def moe_few_tokens_layer(x, w_router, w13, w2, topk: int, bias=None, score="softmax", renormalize=True,
+                         route_scale=1.0, out=None, ids=None, weights=None, workspace=None):
+    """The whole layer for at most 64 tokens: moe_router, then moe_few_tokens on
+    its choice. Returns (out BF16 [T, H], ids [T, topk], weights [T, topk])."""
+    import torch
+
+    T, H = x.shape
+    E = w_router.shape[0]
+    if ids is None:
+        ids = torch.empty((T, topk), dtype=torch.int32, device=x.device)
+    if weights is None:
+        weights = torch.empty((T, topk), dtype=torch.float32, device=x.device)
+    dev, fmt, experts, out, sizes, ws = _few_args(x, ids, weights, w13, w2, out, workspace, topk)
+    _same_device(x, (w_router, torch.bfloat16, (sizes[3], H), "w_router"),
+                 *(((bias, torch.float32, (E,), "bias"),) if bias is not None else ()))
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    _call(dev, "moe_few_tokens_layer", fmt, x.data_ptr(), w_router.data_ptr(),
+          bias.data_ptr() if bias is not None else None, _SCORES[score], int(renormalize), route_scale,
+          ids.data_ptr(), weights.data_ptr(), *experts, out.data_ptr(), *sizes, *ws)
+    return out, ids, weights
+
+
+def moe_few_tokens_ffn(x, routers, w13, w2, topk: int, score="softmax", renormalize=True, route_scale=1.0,
+                       workspace=None):
+    """The layer run once per entry of ``routers`` ((w_router, bias or None)
+    each) on one set of expert weights, each pass fed the previous pass's
+    output, as moe_ffn does for many tokens. Returns the list of per-pass
+    (out, ids, weights)."""
+    outs = []
+    for w_router, bias in routers:
+        outs.append(moe_few_tokens_layer(x, w_router, w13, w2, topk, bias=bias, score=score, renormalize=renormalize,
+                                         route_scale=route_scale, workspace=workspace))
+        x = outs[-1][0]
     return outs

@@ -18,7 +18,8 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = ["api.hip", "quant.hip", "gemm.hip", "w8a16.hip", "moe.hip", "mx.hip"]
+SOURCES = ["api.hip", "quant.hip", "gemm.hip", "w8a16.hip", "moe.hip", "mx.hip", "nvfp4.hip", "w4a16.hip",
+           "few.hip"]
 OUT = os.path.join(HERE, "libw8a8.so")
 
 FLAGS = [

@@ -583,3 +583,171 @@ int moe_mxfp4_grouped(const uint8_t* x_q, const uint8_t* x_scale, const int32_t*
 }
 
 }  // extern "C"
+
+// ---- NVFP4 and 4-bit weights in the default maths -------------------------------
+namespace {
+
+constexpr int64_t kNvBlock = 16;
+
+int check_nvfp4_shape(int64_t G, int64_t R, int64_t K) {
+  if (G < 0 || R < 0 || K < 0 || !mul_ok(R, K) || !mul_ok(G, R * K) || !mul_ok(G * R * K, 4)) return W8A8_ERR_BAD_SHAPE;
+  if (K == 0 || K % kNvBlock != 0 || R * K > (int64_t(1) << 40)) return W8A8_ERR_UNSUPPORTED;
+  if (!mul_ok(G, w8a8::nvfp4_parts(R * K)) || G * w8a8::nvfp4_parts(R * K) > INT32_MAX ||
+      G * R * K / 2048 > INT32_MAX)
+    return W8A8_ERR_UNSUPPORTED;
+  return W8A8_OK;
+}
+
+int w4a16_checked(int format, const uint16_t* x, const uint8_t* w, const uint8_t* s, const float* g, uint16_t* y,
+                  int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  const int c = check_dense_shape(M, N, K);
+  if (c != W8A8_OK) return c;
+  if (K % 32 != 0) return W8A8_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return W8A8_OK;
+  if (any_null({x, w, s, y}) || (format == MOE_NVFP4 && !g)) return W8A8_ERR_NULL_ARG;
+  // the scale is one float, often an element of a vector with one per matrix
+  if (!all_aligned({x, w, s, y}) || (reinterpret_cast<uintptr_t>(g) & 3u)) return W8A8_ERR_MISALIGNED;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  return launch_status(w8a8::launch_w4a16_gemm(format, x, w, s, g, y, M, N, K, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nvfp4_quantize_workspace_bytes(int64_t G, int64_t R, int64_t K) {
+  if (check_nvfp4_shape(G, R, K) != W8A8_OK) return 0;
+  return (size_t)align256(G * w8a8::nvfp4_parts(R * K) * 4);
+}
+
+int nvfp4_quantize(const uint16_t* x_bf16, int64_t G, int64_t R, int64_t K, uint8_t* q_fp4, uint8_t* scale_e4m3,
+                   float* gscale, int gscale_given, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int c = check_nvfp4_shape(G, R, K);
+  if (c != W8A8_OK) return c;
+  if (G == 0 || R == 0) return W8A8_OK;
+  if (any_null({x_bf16, q_fp4, scale_e4m3, gscale}) || (!gscale_given && !workspace)) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({x_bf16, q_fp4, scale_e4m3, gscale, workspace})) return W8A8_ERR_MISALIGNED;
+  if (!gscale_given && workspace_bytes < nvfp4_quantize_workspace_bytes(G, R, K)) return W8A8_ERR_WORKSPACE;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  return launch_status(w8a8::launch_nvfp4_quantize(x_bf16, G, R * K, q_fp4, scale_e4m3, gscale, gscale_given != 0,
+                                                   static_cast<uint32_t*>(workspace), stream));
+}
+
+int nvfp4_dequantize(const uint8_t* q_fp4, const uint8_t* scale_e4m3, const float* gscale, int64_t G, int64_t R,
+                     int64_t K, uint16_t* y_bf16, hipStream_t stream) {
+  const int c = check_nvfp4_shape(G, R, K);
+  if (c != W8A8_OK) return c;
+  if (G == 0 || R == 0) return W8A8_OK;
+  if (any_null({q_fp4, scale_e4m3, gscale, y_bf16})) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({q_fp4, scale_e4m3, gscale, y_bf16})) return W8A8_ERR_MISALIGNED;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  return launch_status(w8a8::launch_nvfp4_dequantize(q_fp4, scale_e4m3, gscale, G, R * K, y_bf16, stream));
+}
+
+int nvfp4_gemm(const uint16_t* x_bf16, const uint8_t* w_q, const uint8_t* w_scale, const float* w_gscale,
+               uint16_t* y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  return w4a16_checked(MOE_NVFP4, x_bf16, w_q, w_scale, w_gscale, y_bf16, M, N, K, stream);
+}
+
+int mxfp4_gemm(const uint16_t* x_bf16, const uint8_t* w_q, const uint8_t* w_scale, uint16_t* y_bf16, int64_t M,
+               int64_t N, int64_t K, hipStream_t stream) {
+  return w4a16_checked(MOE_MXFP4, x_bf16, w_q, w_scale, nullptr, y_bf16, M, N, K, stream);
+}
+
+}  // extern "C"
+
+// ---- router and few-token experts ------------------------------------------------
+namespace {
+
+int check_router_shape(int64_t T, int64_t H, int64_t E, int64_t topk, int score) {
+  if (T < 0 || H < 0 || E < 0 || topk < 0 || !mul_ok(E, H) || !mul_ok(T, H) || !mul_ok(T * H, 2) || !mul_ok(T, topk))
+    return W8A8_ERR_BAD_SHAPE;
+  if (E < 1 || E > kMaxExperts || topk < 1 || topk > kMaxTopk || topk > E) return W8A8_ERR_UNSUPPORTED;
+  if (H == 0 || H % 8 != 0 || H > (int64_t(1) << 20) || E * H > (int64_t(1) << 29) || T > (int64_t(1) << 24))
+    return W8A8_ERR_UNSUPPORTED;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return W8A8_ERR_UNSUPPORTED;
+  return W8A8_OK;
+}
+
+int check_few_shape(int format, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
+  const int c = check_moe_shape(T, H, I, E, topk);
+  if (c != W8A8_OK) return c;
+  if (format != MOE_FP8 && format != MOE_MXFP4 && format != MOE_NVFP4) return W8A8_ERR_UNSUPPORTED;
+  if (H % 32 != 0 || I % 32 != 0) return W8A8_ERR_UNSUPPORTED;
+  if (T > w8a8::kFewMaxTokens || T * topk > w8a8::kFewMaxSlots) return W8A8_ERR_UNSUPPORTED;
+  if (T * topk * I >= int64_t(1) << 29 || E * (I / 16) > INT32_MAX) return W8A8_ERR_UNSUPPORTED;
+  return W8A8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_router(const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int32_t* topk_ids, float* topk_w,
+               int64_t T, int64_t H, int64_t E, int64_t topk, int score, int renormalize, float route_scale,
+               hipStream_t stream) {
+  const int c = check_router_shape(T, H, E, topk, score);
+  if (c != W8A8_OK) return c;
+  if (T == 0) return W8A8_OK;
+  if (any_null({x_bf16, w_router, topk_ids, topk_w})) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({x_bf16, w_router, bias, topk_ids, topk_w})) return W8A8_ERR_MISALIGNED;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  return launch_status(w8a8::launch_router(x_bf16, w_router, bias, topk_ids, topk_w, T, H, E, topk,
+                                           score == MOE_SCORE_SIGMOID, renormalize != 0, route_scale, stream));
+}
+
+size_t moe_few_tokens_workspace_bytes(int format, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
+  if (check_few_shape(format, T, H, I, E, topk) != W8A8_OK) return 0;
+  return w8a8::few_workspace_bytes(T, I, topk);
+}
+
+int moe_few_tokens(int format, const uint16_t* x_bf16, const int32_t* topk_ids, const float* topk_w,
+                   const uint8_t* w13_q, const void* w13_scale, const float* w13_gscale, const uint8_t* w2_q,
+                   const void* w2_scale, const float* w2_gscale, uint16_t* out_bf16, int64_t T, int64_t H, int64_t I,
+                   int64_t E, int64_t topk, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int c = check_few_shape(format, T, H, I, E, topk);
+  if (c != W8A8_OK) return c;
+  if (T == 0) return W8A8_OK;
+  if (any_null({x_bf16, topk_ids, topk_w, w13_q, w13_scale, w2_q, w2_scale, out_bf16, workspace}))
+    return W8A8_ERR_NULL_ARG;
+  if (format == MOE_NVFP4 && any_null({w13_gscale, w2_gscale})) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({x_bf16, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale, w2_gscale, out_bf16,
+                    workspace}))
+    return W8A8_ERR_MISALIGNED;
+  if (workspace_bytes < w8a8::few_workspace_bytes(T, I, topk)) return W8A8_ERR_WORKSPACE;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  return launch_status(w8a8::launch_few(format, x_bf16, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale,
+                                        w2_gscale, out_bf16, T, H, I, E, topk, workspace, stream));
+}
+
+int moe_few_tokens_layer(int format, const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int score,
+                         int renormalize, float route_scale, int32_t* topk_ids, float* topk_w, const uint8_t* w13_q,
+                         const void* w13_scale, const float* w13_gscale, const uint8_t* w2_q, const void* w2_scale,
+                         const float* w2_gscale, uint16_t* out_bf16, int64_t T, int64_t H, int64_t I, int64_t E,
+                         int64_t topk, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  int c = check_router_shape(T, H, E, topk, score);
+  if (c == W8A8_OK) c = check_few_shape(format, T, H, I, E, topk);
+  if (c != W8A8_OK) return c;
+  if (T == 0) return W8A8_OK;
+  if (any_null({x_bf16, w_router, topk_ids, topk_w, w13_q, w13_scale, w2_q, w2_scale, out_bf16, workspace}))
+    return W8A8_ERR_NULL_ARG;
+  if (format == MOE_NVFP4 && any_null({w13_gscale, w2_gscale})) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({x_bf16, w_router, bias, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale, w2_gscale,
+                    out_bf16, workspace}))
+    return W8A8_ERR_MISALIGNED;
+  if (workspace_bytes < w8a8::few_workspace_bytes(T, I, topk)) return W8A8_ERR_WORKSPACE;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  const hipError_t e = w8a8::launch_router(x_bf16, w_router, bias, topk_ids, topk_w, T, H, E, topk,
+                                           score == MOE_SCORE_SIGMOID, renormalize != 0, route_scale, stream);
+  if (e != hipSuccess) return launch_status(e);
+  return launch_status(w8a8::launch_few(format, x_bf16, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale,
+                                        w2_gscale, out_bf16, T, H, I, E, topk, workspace, stream));
+}
+
+}  // extern "C"

@@ -126,4 +126,28 @@ hipError_t launch_mx_moe(const uint8_t* xq, const uint8_t* xs, const int32_t* id
                          uint8_t* out_q, uint8_t* out_s, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk,
                          void* ws, hipStream_t stream);
 
+// NVFP4 (nvfp4.hip): G groups of n = R * K BF16 values -> codes [G, n/2], E4M3
+// scales [G, n/16], float32 scale [G]. given: gscale is read, part unused;
+// else gscale is written and part holds G * nvfp4_parts(n) words of scratch.
+int64_t nvfp4_parts(int64_t n);
+hipError_t launch_nvfp4_quantize(const uint16_t* x, int64_t G, int64_t n, uint8_t* q, uint8_t* s, float* gscale,
+                                 bool given, uint32_t* part, hipStream_t stream);
+hipError_t launch_nvfp4_dequantize(const uint8_t* q, const uint8_t* s, const float* gscale, int64_t G, int64_t n,
+                                   uint16_t* y, hipStream_t stream);
+
+// Weight formats of the default-maths calls below: 0 FP8 rows, 1 MXFP4, 2 NVFP4.
+// 4-bit weights times BF16 activations (w4a16.hip); g: NVFP4's float32 scale.
+hipError_t launch_w4a16_gemm(int format, const uint16_t* x, const uint8_t* w, const uint8_t* s, const float* g,
+                             uint16_t* y, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+// The few-token routed-expert layer (few.hip).
+constexpr int64_t kFewMaxTokens = 64, kFewMaxSlots = 1024;
+hipError_t launch_router(const uint16_t* x, const uint16_t* wr, const float* bias, int32_t* ids, float* tw, int64_t T,
+                         int64_t H, int64_t E, int64_t topk, int sigmoid, int renorm, float scale, hipStream_t stream);
+size_t few_workspace_bytes(int64_t T, int64_t I, int64_t topk);
+hipError_t launch_few(int format, const uint16_t* x, const int32_t* ids, const float* tw, const uint8_t* w13,
+                      const void* s13, const float* g13, const uint8_t* w2, const void* s2, const float* g2,
+                      uint16_t* out, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, void* ws,
+                      hipStream_t stream);
+
 }  // namespace w8a8

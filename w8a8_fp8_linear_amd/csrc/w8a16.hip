@@ -23,33 +23,10 @@
 //    activation values straight from global memory.
 #include "device.h"
 #include "launch.h"
+#include "widen.h"
 
 namespace w8a8 {
 namespace {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-__device__ inline v4f mfma_16x16x32_bf16(v4i a, v4i b, v4f c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                 0, 0);
-}
-
-// Two float32 values that are exact in BF16 -> their BF16 halves packed (a in the low half).
-__device__ inline uint32_t pack_bf16(float a, float b) {
-  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-}
-
-// 8 E4M3 codes (bytes of w0 then w1, value 0 in the low byte) -> 8 BF16 values.
-// The hardware conversion decodes E4M3 exactly into float32 (checked on gfx950
-// against the format's definition for all 256 codes).
-__device__ inline v4i widen8(uint32_t w0, uint32_t w1) {
-  const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w0, false);
-  const auto b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w0, true);
-  const auto c = __builtin_amdgcn_cvt_pk_f32_fp8((int)w1, false);
-  const auto d = __builtin_amdgcn_cvt_pk_f32_fp8((int)w1, true);
-  return v4i{(int)pack_bf16(a[0], a[1]), (int)pack_bf16(b[0], b[1]), (int)pack_bf16(c[0], c[1]),
-             (int)pack_bf16(d[0], d[1])};
-}
 
 // 64-byte weight rows: 16-byte chunk c of row r sits at c ^ ((r >> 1) & 3), so
 // 8 consecutive rows at one logical chunk cover 8 different 16-byte bank
