@@ -604,26 +604,29 @@ enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
  *   l[t,e]  = sum_k x[t,k] * w_router[e,k]     exact products, float64 sums
  *   s       = softmax over e of l, or sigmoid(l)              (float64)
  *   ids[t]  = the topk experts with the largest s + bias, in that order, the
- *             lower index first where they are equal (a NaN comes last)
+ *             lower index first where they are equal (-inf and NaN come last)
  *   w[t,j]  = route_scale * s[ids[t,j]], divided by the sum over j of s where
  *             renormalize != 0; rounded once to float32
- * The choice does not depend on T.
  *   x_bf16 [T, H]; w_router [E, H] BF16; bias [E] float32 or NULL
  *   topk_ids [T, topk] int32; topk_w [T, topk] float32
+ *   workspace  moe_router_workspace_bytes bytes (the logits)
  *   1 <= topk <= min(E, 64), E <= 1024, H a positive multiple of 8,
  *   E * H <= 2^29, H <= 2^20, T <= 2^24
- * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, DEVICE, LAUNCH.
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, WORKSPACE, DEVICE,
+ *         LAUNCH.
  */
+size_t moe_router_workspace_bytes(int64_t T, int64_t E);
 int moe_router(const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int32_t* topk_ids, float* topk_w,
                int64_t T, int64_t H, int64_t E, int64_t topk, int score, int renormalize, float route_scale,
-               hipStream_t stream);
+               void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Weight formats of the few-token calls. */
 enum { MOE_FP8 = 0, MOE_MXFP4 = 1, MOE_NVFP4 = 2 };
 
-/* Bytes of scratch the few-token calls need: T * topk * I * 4 (0 for sizes
- * they do not take). */
-size_t moe_few_tokens_workspace_bytes(int format, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
+/* Bytes of scratch that either few-token call needs (0 for sizes they do not
+ * take): h, and the larger of the router's logits and the float32 rows of the
+ * routed copies. */
+size_t moe_few_tokens_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
 
 /*
  * moe_few_tokens — one routed-expert pass for at most 64 tokens:
@@ -644,7 +647,7 @@ size_t moe_few_tokens_workspace_bytes(int format, int64_t T, int64_t H, int64_t 
  *   workspace  moe_few_tokens_workspace_bytes bytes; calls that may overlap
  *              need one each
  *   T <= 64, T * topk <= 1024, E <= 1024, H and I positive multiples of 32,
- *   2 * I * H below 2^31, T * topk * I below 2^29
+ *   2 * I * H below 2^31, T * topk * I and T * topk * H below 2^29
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED (also another format), MISALIGNED,
  *         WORKSPACE, DEVICE, LAUNCH.
  */

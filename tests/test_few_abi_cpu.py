@@ -50,8 +50,11 @@ def test_products():
 def test_router():
     f = w8.lib().moe_router
 
-    def call(x=P, wr=P, b=None, ids=P, tw=P, T=4, H=64, E=8, k=2, score=0):
-        return f(x, wr, b, ids, tw, T, H, E, k, score, 1, 1.0, None)
+    size = w8.lib().moe_router_workspace_bytes(4, 8)
+    assert size == 4 * 8 * 8 and w8.lib().moe_router_workspace_bytes(4, 1025) == 0
+
+    def call(x=P, wr=P, b=None, ids=P, tw=P, T=4, H=64, E=8, k=2, score=0, ws=P, n=size):
+        return f(x, wr, b, ids, tw, T, H, E, k, score, 1, 1.0, ws, n, None)
 
     assert call(T=-1) == SHAPE
     assert call(H=12) == UNSUP and call(H=0) == UNSUP and call(E=0) == UNSUP and call(E=1025) == UNSUP
@@ -60,6 +63,7 @@ def test_router():
     assert call(T=0) == OK
     assert call(x=None) == NULL and call(tw=None) == NULL
     assert call(b=P + 4) == MIS and call(ids=P + 8) == MIS
+    assert call(ws=None) == NULL and call(ws=P + 8) == MIS and call(n=size - 1) == WS
     if _no_gpu():
         assert call() == DEV
 
@@ -67,15 +71,17 @@ def test_router():
 @pytest.mark.parametrize("fmt", [0, 1, 2])
 def test_few_tokens(fmt):
     f, need = w8.lib().moe_few_tokens, w8.lib().moe_few_tokens_workspace_bytes
-    size = need(fmt, 4, 64, 32, 8, 2)
-    assert size == 4 * 2 * 32 * 4
+    size = need(4, 64, 32, 8, 2)
+    assert size == 4 * 2 * 32 * 4 + 4 * 8 * 8                      # h and the logits
+    assert need(16, 64, 32, 8, 2) == 16 * 2 * 32 * 4 + 16 * 2 * 64 * 4   # h and the float32 rows
+    size = 4 * 2 * 32 * 4                                         # without a router: h
 
     def call(fmt=fmt, T=4, H=64, I=32, E=8, k=2, x=P, g=P, ws=P, n=size, out=P):
         return f(fmt, x, P, P, P, P, g, P, P, g, out, T, H, I, E, k, ws, n, None)
 
     assert call(T=-1) == SHAPE
     assert call(fmt=3) == UNSUP and call(fmt=-1) == UNSUP
-    assert call(T=65) == UNSUP and call(T=64, k=17) == UNSUP and need(fmt, 65, 64, 32, 8, 2) == 0
+    assert call(T=65) == UNSUP and call(T=64, k=17) == UNSUP and need(65, 64, 32, 8, 2) == 0
     assert call(H=48) == UNSUP and call(I=16) == UNSUP and call(E=1025) == UNSUP and call(k=0) == UNSUP
     assert call(H=1 << 17, I=1 << 14) == UNSUP
     assert call(T=0) == OK

@@ -92,6 +92,18 @@ def test_router_nan_is_last():
     assert ids[0].tolist() == [2, 1, 0, 3]
 
 
+def test_router_barred_experts():
+    """A bias of -inf bars an expert; where fewer than k are left, the barred follow by index."""
+    rng = np.random.default_rng(4)
+    x, wr = _router_inputs(rng, 6, 64, 70)
+    bias = np.full(70, -np.inf, np.float32)
+    bias[[5, 40, 69]] = 0
+    ids, w = w8.moe_router(to_dev_bf16(x), to_dev_bf16(wr), 5, bias=to_dev(bias))
+    got = ids.cpu().numpy()
+    assert np.all(np.sort(got[:, :3], 1) == [5, 40, 69]) and np.all(got[:, 3:] == [0, 1])
+    assert torch.isfinite(w).all()
+
+
 def _experts(rng, fmt, E, I, H):
     w13, v13 = random_codes(rng, fmt, E, 2 * I, H)
     w2, v2 = random_codes(rng, fmt, E, H, I)
@@ -205,7 +217,7 @@ def test_checkpoint_to_two_passes(fmt):
 @pytest.mark.parametrize("fmt,T", [("fp8", 1), ("nvfp4", 40)])
 def test_layer_in_a_graph(fmt, T):
     x, wr, w13, w2 = _layer_state(fmt, T, 288, 96, 20, seed=3)
-    ws = w8.moe_few_tokens_workspace(T, 96, 4)
+    ws = w8.moe_few_tokens_workspace(T, 288, 96, 20, 4)
     eager = [t.clone() for t in w8.moe_few_tokens_layer(x, wr, w13, w2, 4, workspace=ws)]
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()

@@ -76,8 +76,10 @@ _SIGNATURES = {
     "nvfp4_dequantize": (ctypes.c_int, [_c_ptr] * 3 + [_c_i64] * 3 + [_c_ptr] * 2),
     "nvfp4_gemm": (ctypes.c_int, [_c_ptr] * 5 + [_c_i64] * 3 + [_c_ptr]),
     "mxfp4_gemm": (ctypes.c_int, [_c_ptr] * 4 + [_c_i64] * 3 + [_c_ptr]),
-    "moe_router": (ctypes.c_int, [_c_ptr] * 5 + [_c_i64] * 4 + [ctypes.c_int, ctypes.c_int, ctypes.c_float, _c_ptr]),
-    "moe_few_tokens_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] + [_c_i64] * 5),
+    "moe_router_workspace_bytes": (ctypes.c_size_t, [_c_i64] * 2),
+    "moe_router": (ctypes.c_int, [_c_ptr] * 5 + [_c_i64] * 4 + [ctypes.c_int, ctypes.c_int, ctypes.c_float, _c_ptr,
+                                                               ctypes.c_size_t, _c_ptr]),
+    "moe_few_tokens_workspace_bytes": (ctypes.c_size_t, [_c_i64] * 5),
     "moe_few_tokens": (ctypes.c_int, [ctypes.c_int] + [_c_ptr] * 10 + [_c_i64] * 5 + [_c_ptr, ctypes.c_size_t,
                                                                                     _c_ptr]),
     "moe_few_tokens_layer": (ctypes.c_int, [ctypes.c_int] + [_c_ptr] * 3 + [ctypes.c_int, ctypes.c_int,
@@ -915,7 +917,7 @@ _FP8, _MXFP4, _NVFP4 = 0, 1, 2
 
 
 def moe_router(x, w_router, topk: int, bias=None, score="softmax", renormalize=True, route_scale=1.0, ids=None,
-               weights=None):
+               weights=None, workspace=None):
     """The experts of every token: (ids int32 [T, topk], weights float32 [T, topk]).
 
     The score is softmax or sigmoid of x . w_router^T (float64 sums); the
@@ -935,8 +937,11 @@ def moe_router(x, w_router, topk: int, bias=None, score="softmax", renormalize=T
                        *(((bias, torch.float32, (E,), "bias"),) if bias is not None else ()))
     if score not in _SCORES:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
+    if workspace is None:
+        workspace = torch.empty(max(T * E * 8, 16), dtype=torch.uint8, device=x.device)
     _call(dev, "moe_router", x.data_ptr(), w_router.data_ptr(), bias.data_ptr() if bias is not None else None,
-          ids.data_ptr(), weights.data_ptr(), T, H, E, topk, _SCORES[score], int(renormalize), route_scale)
+          ids.data_ptr(), weights.data_ptr(), T, H, E, topk, _SCORES[score], int(renormalize), route_scale,
+          *_workspace_args(workspace, dev))
     return ids, weights
 
 
@@ -979,17 +984,18 @@ def _few_args(x, ids, weights, w13, w2, out, workspace, topk):
                        (weights, torch.float32, (T, topk), "topk_w"), (out, torch.bfloat16, (T, H), "out"),
                        *_expert_specs(fmt, w13, "w13", E, 2 * I, H), *_expert_specs(fmt, w2, "w2", E, H, I))
     if workspace is None:
-        workspace = moe_few_tokens_workspace(T, I, topk, x.device)
+        workspace = moe_few_tokens_workspace(T, H, I, E, topk, x.device)
     experts = (w13[0].data_ptr(), w13[1].data_ptr(), w13[2].data_ptr() if fmt == _NVFP4 else None,
                w2[0].data_ptr(), w2[1].data_ptr(), w2[2].data_ptr() if fmt == _NVFP4 else None)
     return dev, fmt, experts, out, (T, H, I, E, topk), _workspace_args(workspace, dev)
 
 
-def moe_few_tokens_workspace(T: int, I: int, topk: int, device="cuda"):
+def moe_few_tokens_workspace(T: int, H: int, I: int, E: int, topk: int, device="cuda"):
     """Scratch buffer sized for moe_few_tokens and moe_few_tokens_layer."""
     import torch
 
-    return torch.empty(max(T * topk * I * 4, 16), dtype=torch.uint8, device=device)
+    nbytes = int(lib().moe_few_tokens_workspace_bytes(T, H, I, E, topk))
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
 
 
 def moe_few_tokens(x, topk_ids, topk_w, w13, w2, out=None, workspace=None):

@@ -678,7 +678,7 @@ int check_few_shape(int format, int64_t T, int64_t H, int64_t I, int64_t E, int6
   if (format != MOE_FP8 && format != MOE_MXFP4 && format != MOE_NVFP4) return W8A8_ERR_UNSUPPORTED;
   if (H % 32 != 0 || I % 32 != 0) return W8A8_ERR_UNSUPPORTED;
   if (T > w8a8::kFewMaxTokens || T * topk > w8a8::kFewMaxSlots) return W8A8_ERR_UNSUPPORTED;
-  if (T * topk * I >= int64_t(1) << 29 || E * (I / 16) > INT32_MAX) return W8A8_ERR_UNSUPPORTED;
+  if (T * topk * I >= int64_t(1) << 29 || T * topk * H >= int64_t(1) << 29) return W8A8_ERR_UNSUPPORTED;
   return W8A8_OK;
 }
 
@@ -686,23 +686,30 @@ int check_few_shape(int format, int64_t T, int64_t H, int64_t I, int64_t E, int6
 
 extern "C" {
 
+size_t moe_router_workspace_bytes(int64_t T, int64_t E) {
+  if (T < 0 || E < 1 || E > kMaxExperts || T > (int64_t(1) << 24)) return 0;
+  return w8a8::router_workspace_bytes(T, E);
+}
+
 int moe_router(const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int32_t* topk_ids, float* topk_w,
                int64_t T, int64_t H, int64_t E, int64_t topk, int score, int renormalize, float route_scale,
-               hipStream_t stream) {
+               void* workspace, size_t workspace_bytes, hipStream_t stream) {
   const int c = check_router_shape(T, H, E, topk, score);
   if (c != W8A8_OK) return c;
   if (T == 0) return W8A8_OK;
-  if (any_null({x_bf16, w_router, topk_ids, topk_w})) return W8A8_ERR_NULL_ARG;
-  if (!all_aligned({x_bf16, w_router, bias, topk_ids, topk_w})) return W8A8_ERR_MISALIGNED;
+  if (any_null({x_bf16, w_router, topk_ids, topk_w, workspace})) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({x_bf16, w_router, bias, topk_ids, topk_w, workspace})) return W8A8_ERR_MISALIGNED;
+  if (workspace_bytes < w8a8::router_workspace_bytes(T, E)) return W8A8_ERR_WORKSPACE;
   const int d = check_device();
   if (d != W8A8_OK) return d;
   return launch_status(w8a8::launch_router(x_bf16, w_router, bias, topk_ids, topk_w, T, H, E, topk,
-                                           score == MOE_SCORE_SIGMOID, renormalize != 0, route_scale, stream));
+                                           score == MOE_SCORE_SIGMOID, renormalize != 0, route_scale, workspace,
+                                           stream));
 }
 
-size_t moe_few_tokens_workspace_bytes(int format, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
-  if (check_few_shape(format, T, H, I, E, topk) != W8A8_OK) return 0;
-  return w8a8::few_workspace_bytes(T, I, topk);
+size_t moe_few_tokens_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
+  if (check_few_shape(MOE_FP8, T, H, I, E, topk) != W8A8_OK) return 0;
+  return w8a8::few_layer_workspace_bytes(T, H, I, E, topk);
 }
 
 int moe_few_tokens(int format, const uint16_t* x_bf16, const int32_t* topk_ids, const float* topk_w,
@@ -718,7 +725,7 @@ int moe_few_tokens(int format, const uint16_t* x_bf16, const int32_t* topk_ids, 
   if (!all_aligned({x_bf16, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale, w2_gscale, out_bf16,
                     workspace}))
     return W8A8_ERR_MISALIGNED;
-  if (workspace_bytes < w8a8::few_workspace_bytes(T, I, topk)) return W8A8_ERR_WORKSPACE;
+  if (workspace_bytes < w8a8::few_workspace_bytes(T, H, I, topk)) return W8A8_ERR_WORKSPACE;
   const int d = check_device();
   if (d != W8A8_OK) return d;
   return launch_status(w8a8::launch_few(format, x_bf16, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale,
@@ -740,11 +747,12 @@ int moe_few_tokens_layer(int format, const uint16_t* x_bf16, const uint16_t* w_r
   if (!all_aligned({x_bf16, w_router, bias, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale, w2_gscale,
                     out_bf16, workspace}))
     return W8A8_ERR_MISALIGNED;
-  if (workspace_bytes < w8a8::few_workspace_bytes(T, I, topk)) return W8A8_ERR_WORKSPACE;
+  if (workspace_bytes < w8a8::few_layer_workspace_bytes(T, H, I, E, topk)) return W8A8_ERR_WORKSPACE;
   const int d = check_device();
   if (d != W8A8_OK) return d;
   const hipError_t e = w8a8::launch_router(x_bf16, w_router, bias, topk_ids, topk_w, T, H, E, topk,
-                                           score == MOE_SCORE_SIGMOID, renormalize != 0, route_scale, stream);
+                                           score == MOE_SCORE_SIGMOID, renormalize != 0, route_scale,
+                                           w8a8::few_layer_logits(workspace, T, I, topk), stream);
   if (e != hipSuccess) return launch_status(e);
   return launch_status(w8a8::launch_few(format, x_bf16, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale,
                                         w2_gscale, out_bf16, T, H, I, E, topk, workspace, stream));

@@ -1,44 +1,76 @@
-// A whole routed-expert layer for a few tokens in the default maths: router,
-// gate/up + SwiGLU, down + weighted sum, three launches.
+// A whole routed-expert layer for a few tokens in the default maths: router
+// (logits, choice), gate/up + SwiGLU, down, weighted sum.
 //
 // A step with few tokens is set by how fast the expert weights are read, and
 // the pages' runtime uses the default maths there: BF16 activations, weights
 // widened to 16 bits as they are multiplied (Lernex/Metis-1.6-Logos-FP8,
 // "What --fast-math does"). So each picked expert's weights are read once,
-// whatever the number of tokens that picked it, and nothing is sorted,
-// quantised or written in between but h:
+// whatever the number of tokens that picked it, and nothing is sorted or
+// quantised in between:
 //
-//  * router: l[t, e] = sum_k x[t, k] wr[e, k] in float64, the score
-//    softmax(l) or sigmoid(l), the top-k experts by score + bias, and their
-//    weights. The products of two BF16 values are exact in float32 and the
-//    sums are float64, so the experts a token gets do not depend on how many
-//    tokens run with it or on how the sum is split.
-//  * few_gate_up: one workgroup per (expert, 16 columns of h): the 16 gate
-//    and 16 up rows of that expert, K split over the waves, for every token
-//    that picked it (the MFMA's column side). h = silu(g) * u is written as a
+//  * router_logits_*: l[t, e] = sum_k x[t, k] wr[e, k] in float64. The
+//    products of two BF16 values are exact in float32, the sums are float64:
+//    two experts change places only where their logits agree to 2^-45 or so.
+//  * router_select: the score softmax(l) or sigmoid(l), the top-k experts by
+//    score + bias, and their weights.
+//  * few_rows (gate/up): tiles of 16 columns of h: the 16 gate and 16 up rows
+//    of an expert, for every token that picked it (the MFMA's column side).
+//    h = silu(g) * u is written as a
 //    pair of BF16 values, h = hi + lo: 16 significant bits, so that the down
 //    product of an h kept in float32 (the reading of the grouped calls) is
 //    met to 2^-17 while it runs on the BF16 matrix cores.
-//  * few_down: one workgroup per 16 output columns: it walks all picked
-//    experts, each wave taking its share of (expert, part of K) units, adds
-//    the router-weighted results per token in float32 and rounds once to
-//    BF16. No partial result leaves the workgroup, and the order of the sum
-//    is fixed by the ids alone.
+//  * few_down_small (at most 8 tokens and 64 routed copies): one workgroup per 4 or
+//    8 output columns walks all picked experts, a wave an expert, and adds
+//    the router-weighted results per token in registers.
+//  * few_rows (down) + few_combine (more): tiles of 32 rows of an expert's W2
+//    leave its tokens' weighted float32 rows, and the rows of a token are
+//    added in the order of its slots.
+// The output is rounded to BF16 once. Every sum's order is fixed by the ids
+// and the sizes alone.
 //
 // A token that names an expert twice is one column whose router weights add.
 #include "device.h"
 #include "launch.h"
 #include "widen.h"
 
+#include <float.h>
+
 namespace w8a8 {
 namespace {
 
 // ---- router ------------------------------------------------------------------
 
-constexpr int kRouterThreads = 1024;
-constexpr int kRouterMaxE = 1024;
+typedef double v4d __attribute__((ext_vector_type(4)));
 
 __device__ inline double shfl_xor_f64(double v, int m) { return __shfl_xor(v, m, 64); }
+
+// v of the lane that a DPP control names, `v` itself where there is none.
+template <int CTRL>
+__device__ inline double dpp_f64(double v) {
+  const uint2 u = __builtin_bit_cast(uint2, v);
+  return __builtin_bit_cast(
+      double, make_uint2((uint32_t)__builtin_amdgcn_update_dpp((int)u.x, (int)u.x, CTRL, 0xF, 0xF, false),
+                         (uint32_t)__builtin_amdgcn_update_dpp((int)u.y, (int)u.y, CTRL, 0xF, 0xF, false)));
+}
+
+__device__ inline double readlane_f64(double v, int lane) {
+  const uint2 u = __builtin_bit_cast(uint2, v);
+  return __builtin_bit_cast(double, make_uint2((uint32_t)__builtin_amdgcn_readlane((int)u.x, lane),
+                                               (uint32_t)__builtin_amdgcn_readlane((int)u.y, lane)));
+}
+
+// The wave's largest value, in every lane: row shifts by 1, 2, 4, 8, then the
+// row broadcasts leave it in lane 63. DPP moves take a few cycles where a
+// shuffle through LDS takes a hundred.
+__device__ inline double wave_max_f64(double v) {
+  v = fmax(v, dpp_f64<0x111>(v));
+  v = fmax(v, dpp_f64<0x112>(v));
+  v = fmax(v, dpp_f64<0x114>(v));
+  v = fmax(v, dpp_f64<0x118>(v));
+  v = fmax(v, dpp_f64<0x142>(v));
+  v = fmax(v, dpp_f64<0x143>(v));
+  return readlane_f64(v, 63);
+}
 
 // 8 BF16 values -> float64 (exact).
 __device__ inline void bf16x8_to_f64(v4i v, double* d) {
@@ -54,119 +86,178 @@ struct RouterArgs {
   const uint16_t* x;   // [T, H]
   const uint16_t* wr;  // [E, H]
   const float* bias;   // [E] or NULL
+  double* logits;      // [T, E]
   int32_t* ids;        // [T, k]
   float* tw;           // [T, k]
   int T, H, E, k, sigmoid, renorm;
   float scale;
 };
 
+// Few tokens: a wave per expert, lanes along K, TT tokens.
 template <int TT>
-__global__ __launch_bounds__(kRouterThreads) void router(const RouterArgs p) {
-  __shared__ double val[TT][kRouterMaxE];  // logits, then scores
-  __shared__ double sel[TT][kRouterMaxE];  // what the experts are ordered by
-  __shared__ double picked[TT][64];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int t0 = blockIdx.x * TT;
-  const int nt = min(TT, p.T - t0);
-  const auto rX = make_rsrc(p.x + (int64_t)t0 * p.H, (int64_t)nt * p.H * 2);
-  const auto rW = make_rsrc(p.wr, (int64_t)p.E * p.H * 2);
-
-  constexpr int NE = 4;  // experts a wave takes together
-  for (int e0 = wave * NE; e0 < p.E; e0 += (kRouterThreads / 64) * NE) {
-    double acc[NE][TT];
+__global__ __launch_bounds__(256) void router_logits_few(const RouterArgs p) {
+  constexpr int U = TT <= 2 ? 4 : 2;  // 512-value pieces of the rows loaded together
+  const int lane = threadIdx.x & 63;
+  const int e = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t0 = blockIdx.y * TT;
+  if (e >= p.E) return;
+  const auto rX = make_rsrc(p.x + (int64_t)t0 * p.H, (int64_t)min(TT, p.T - t0) * p.H * 2);
+  const auto rW = make_rsrc(p.wr + (int64_t)e * p.H, (int64_t)p.H * 2);
+  double acc[TT];
 #pragma unroll
-    for (int e = 0; e < NE; ++e)
+  for (int t = 0; t < TT; ++t) acc[t] = 0.0;
+  for (int k0 = lane * 8; k0 < p.H; k0 += 512 * U) {
+    v4i wv[U], xv[U][TT];
 #pragma unroll
-      for (int t = 0; t < TT; ++t) acc[e][t] = 0.0;
-    for (int k = lane * 8; k < p.H; k += 512) {
-      v4i xv[TT], wv[NE];
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + 512 * u;
+      wv[u] = buffer_load16(rW, k < p.H ? (uint32_t)k * 2u : kOutOfRange);
 #pragma unroll
-      for (int t = 0; t < TT; ++t) xv[t] = buffer_load16(rX, (uint32_t)(t * p.H + k) * 2u);
-#pragma unroll
-      for (int e = 0; e < NE; ++e) wv[e] = buffer_load16(rW, (uint32_t)((e0 + e) * p.H + k) * 2u);
-      double x[TT][8];
-#pragma unroll
-      for (int t = 0; t < TT; ++t) bf16x8_to_f64(xv[t], x[t]);
-#pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        double w[8];
-        bf16x8_to_f64(wv[e], w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int t = 0; t < TT; ++t) acc[e][t] = __builtin_fma(w[i], x[t][i], acc[e][t]);
-      }
+      for (int t = 0; t < TT; ++t) xv[u][t] = buffer_load16(rX, k < p.H ? (uint32_t)(t * p.H + k) * 2u : kOutOfRange);
     }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int e = 0; e < NE; ++e)
+    for (int u = 0; u < U; ++u) {
+      double w[8], x[8];
+      bf16x8_to_f64(wv[u], w);
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        double a = acc[e][t];
+        bf16x8_to_f64(xv[u][t], x);
 #pragma unroll
-        for (int m = 32; m > 0; m >>= 1) a += shfl_xor_f64(a, m);
-        if (lane == 0 && e0 + e < p.E) val[t][e0 + e] = a;
+        for (int i = 0; i < 8; ++i) acc[t] = __builtin_fma(w[i], x[i], acc[t]);
       }
+    }
   }
-  __syncthreads();
-
-  // Scores. The threads are split over the tokens; each wave finds its
-  // token's maximum and sum by itself.
-  constexpr int G = kRouterThreads / TT;  // threads per token
-  const int t = tid / G, i = tid % G;
-  double mx = -INFINITY;
-  for (int e = lane; e < p.E; e += 64) mx = fmax(mx, val[t][e]);
 #pragma unroll
-  for (int m = 32; m > 0; m >>= 1) mx = fmax(mx, shfl_xor_f64(mx, m));
-  __syncthreads();
-  for (int e = i; e < p.E; e += G) {
-    const double l = val[t][e];
-    val[t][e] = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - mx);
+  for (int t = 0; t < TT; ++t) {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) acc[t] += shfl_xor_f64(acc[t], m);
+    if (lane == 0 && t0 + t < p.T) p.logits[(int64_t)(t0 + t) * p.E + e] = acc[t];
   }
+}
+
+// More tokens: 16 tokens x 16 experts a workgroup on the float64 matrix
+// cores, K split over the 8 waves in 32-deep steps. A lane loads 8
+// consecutive values of its token's and of its expert's row (K 8 g .. of the
+// step); MFMA i takes value i of each, so the step's K order is permuted alike
+// on both sides.
+__global__ __launch_bounds__(512) void router_logits_mfma(const RouterArgs p) {
+  __shared__ double red[8][256];
+  constexpr int U = 4;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int tiles_e = (p.E + 15) / 16;
+  const int t0 = blockIdx.x / tiles_e * 16, e0 = blockIdx.x % tiles_e * 16;
+  const auto rX = make_rsrc(p.x + (int64_t)t0 * p.H, (int64_t)(p.T - t0) * p.H * 2);
+  const auto rW = make_rsrc(p.wr + (int64_t)e0 * p.H, (int64_t)(p.E - e0) * p.H * 2);
+  const uint32_t row = (uint32_t)r16 * (uint32_t)p.H * 2u;
+  v4d acc[2] = {v4d{0, 0, 0, 0}, v4d{0, 0, 0, 0}};
+  const int nk = (p.H + 31) >> 5;
+  for (int kt = wave; kt < nk; kt += 8 * U) {
+    v4i xv[U], wv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = ((kt + 8 * u) << 5) + 8 * g;
+      const uint32_t off = kt + 8 * u < nk && k < p.H ? row + (uint32_t)k * 2u : kOutOfRange;
+      xv[u] = buffer_load16(rX, off);
+      wv[u] = buffer_load16(rW, off);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      double x[8], w[8];
+      bf16x8_to_f64(xv[u], x);
+      bf16x8_to_f64(wv[u], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        acc[i & 1] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[i], w[i], acc[i & 1], 0, 0, 0);
+    }
+  }
+  // acc[r] of lane (r16, g): token 4 r + g, expert r16
+#pragma unroll
+  for (int r = 0; r < 4; ++r) red[wave][(4 * r + g) * 16 + r16] = acc[0][r] + acc[1][r];
   __syncthreads();
-  if (!p.sigmoid) {
+  const int i = threadIdx.x;
+  if (i < 256) {
+    double s = red[0][i];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) s += red[w][i];
+    const int t = t0 + (i >> 4), e = e0 + (i & 15);
+    if (t < p.T && e < p.E) p.logits[(int64_t)t * p.E + e] = s;
+  }
+}
+
+// The choice: a wave per token, lane l holding the NV experts from NV * l on.
+// k times the largest of what is left: the lanes' largest, the wave's, and
+// the first lane that has it, so that equal scores go by index.
+template <int NV>
+__global__ __launch_bounds__(64) void router_select(const RouterArgs p) {
+  const int lane = threadIdx.x;
+  const int t = blockIdx.x;
+  const double* l = p.logits + (int64_t)t * p.E;
+  double val[NV], sel[NV];
+  float bias[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane * NV + i;
+    val[i] = e < p.E ? l[e] : -INFINITY;
+    bias[i] = p.bias && e < p.E ? p.bias[e] : 0.f;
+  }
+  double inv = 1.0;
+  if (p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) val[i] = 1.0 / (1.0 + exp(-val[i]));
+  } else {
+    double mx = val[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) mx = fmax(mx, val[i]);
+    mx = wave_max_f64(mx);
     double sum = 0.0;
-    for (int e = lane; e < p.E; e += 64) sum += val[t][e];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      val[i] = exp(val[i] - mx);
+      sum += val[i];
+    }
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) sum += shfl_xor_f64(sum, m);
-    __syncthreads();
-    for (int e = i; e < p.E; e += G) val[t][e] /= sum;
-    __syncthreads();
+    inv = 1.0 / sum;
   }
-  for (int e = i; e < p.E; e += G) {
-    const double s = val[t][e] + (p.bias ? (double)p.bias[e] : 0.0);
-    sel[t][e] = s == s ? s : -INFINITY;  // a NaN score comes last: every rank below is taken once
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    // -infinity (a bias that bars an expert) and NaN come after every number,
+    // what is no expert or already chosen after all
+    const double s = val[i] * inv + (double)bias[i];
+    sel[i] = lane * NV + i >= p.E ? -INFINITY : s > -DBL_MAX ? s : -DBL_MAX;
   }
-  __syncthreads();
-  // rank[e] = how many experts go before e: a larger score, or the same and a
-  // lower index. The experts with rank < k are the choice, in order.
-  int parts = 1;
-  while (parts < 64 && 2 * parts * p.E <= G) parts *= 2;
-  for (int e0 = 0; e0 < p.E; e0 += G / parts) {
-    const int e = e0 + i / parts;
-    int rank = 0;
-    if (e < p.E) {
-      const double s = sel[t][e];
-      for (int o = i % parts; o < p.E; o += parts) {
-        const double v = sel[t][o];
-        rank += (v > s || (v == s && o < e)) ? 1 : 0;
-      }
+  double mine = 0.0, all = 0.0;  // lane j: the j-th chosen score; the sum of the chosen
+  int mine_e = 0;
+  for (int j = 0; j < p.k; ++j) {
+    double best = sel[0], v = val[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < NV; ++i) {
+      const bool up = sel[i] > best;
+      best = up ? sel[i] : best;
+      v = up ? val[i] : v;
+      at = up ? i : at;
     }
-    for (int m = 1; m < parts; m <<= 1) rank += __shfl_xor(rank, m, 64);
-    if (e < p.E && i % parts == 0 && rank < p.k) {
-      picked[t][rank] = val[t][e];
-      if (t < nt) p.ids[(int64_t)(t0 + t) * p.k + rank] = e;
+    const double mx = wave_max_f64(best);
+    const int from = __builtin_ctzll(__ballot(best == mx));
+    const double score = readlane_f64(v, from) * inv;
+    const int e = from * NV + __builtin_amdgcn_readlane(at, from);
+    all += score;
+    if (lane == j) {
+      mine = score;
+      mine_e = e;
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lane == from && i == at) sel[i] = -INFINITY;
   }
-  __syncthreads();
-  if (i < p.k && t < nt) {
-    double w = picked[t][i];
-    if (p.renorm) {
-      double sum = 0.0;
-      for (int j = 0; j < p.k; ++j) sum += picked[t][j];
-      w /= sum;
-    }
-    p.tw[(int64_t)(t0 + t) * p.k + i] = (float)(w * (double)p.scale);
+  if (lane < p.k) {
+    p.ids[(int64_t)t * p.k + lane] = mine_e;
+    p.tw[(int64_t)t * p.k + lane] = (float)((p.renorm ? mine / all : mine) * (double)p.scale);
   }
 }
 
@@ -183,284 +274,511 @@ struct FewArgs {
   const void* s2;
   const float* g2;
   uint16_t* h;            // [T * k, 2, I]: hi and lo of every routed copy's h
+  float* y;               // [T * k, H]: weighted float32 rows (few_down_rows)
   uint16_t* out;          // [T, H]
-  int T, H, I, E, k;
+  int T, H, I, E, k, by_slot;
 };
-
-constexpr int kFewMaxE = 1024;
-
-// Which tokens picked expert e: lane t < T looks through its token's ids.
-// Returns the mask over tokens; *slot (of lane t) is the first of the token's
-// slots that names e.
-__device__ inline uint64_t tokens_of(const FewArgs& p, int e, int lane, int* slot) {
-  int first = -1;
-  if (lane < p.T) {
-    for (int j = p.k - 1; j >= 0; --j)
-      if (p.ids[lane * p.k + j] == e) first = lane * p.k + j;
-  }
-  *slot = first;
-  return __ballot(first >= 0);
-}
 
 __device__ inline int rank_in(uint64_t mask, int lane) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
 }
 
-template <int F, int NT, int U>
-__device__ inline void gate_up_tile(const FewArgs& p, int e, int row0, int n, const int* cols, v4f* red, int wave,
-                                    int lane) {
-  using W = WideFmt<F>;
-  const int r16 = lane & 15, g = lane >> 4;
-  const int64_t rb = W::row_bytes(p.H), rs = W::row_scales(p.H);
-  const auto rW = make_rsrc(p.w13 + (int64_t)e * 2 * p.I * rb, 2 * (int64_t)p.I * rb);
-  const auto rS = make_rsrc(static_cast<const uint8_t*>(p.s13) + (int64_t)e * 2 * p.I * rs, 2 * (int64_t)p.I * rs);
-  const auto rX = make_rsrc(p.x, (int64_t)p.T * p.H * 2);
-  const uint32_t wrow[2] = {(uint32_t)((row0 + r16) * rb), (uint32_t)((p.I + row0 + r16) * rb)};
-  const uint32_t srow[2] = {(uint32_t)((row0 + r16) * rs), (uint32_t)((p.I + row0 + r16) * rs)};
-  uint32_t xrow[NT];
+// The work of a group: an expert and the tokens that picked it.
+struct Group {
+  int e;   // -1: nothing to do
+  int n;   // tokens
+};
+
+// With no more routed copies than experts a group is a copy (slot), and the
+// first copy of an expert works for all of them; otherwise a group is an
+// expert. Lane t < T looks through its token's ids, eight loads at a time.
+// cols[c] and (if asked) colw[c]: the first slot and the summed router weight
+// of the group's c-th token, written by wave 0; the caller's barrier follows.
+template <bool WEIGHTS>
+__device__ inline Group find_group(const FewArgs& p, int group, int* cols, float* colw) {
+  const int lane = threadIdx.x & 63;
+  const int e = p.by_slot ? p.ids[group] : group;
+  int slot = -1;
+  float w = 0.f;
+  for (int j0 = 0; j0 < p.k; j0 += 8) {
+    int id[8];
+    float tw[8];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int c = t * 16 + r16;
-    xrow[t] = c < n ? (uint32_t)(cols[c] / p.k) * (uint32_t)p.H * 2u : kOutOfRange;
+    for (int j = 0; j < 8; ++j) {
+      const bool in = lane < p.T && j0 + j < p.k;
+      const int s = lane * p.k + j0 + j;
+      id[j] = in ? p.ids[s] : -1;
+      tw[j] = WEIGHTS && in ? p.tw[s] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (id[j] == e) {
+        slot = slot < 0 ? lane * p.k + j0 + j : slot;
+        w += tw[j];
+      }
+    }
   }
+  if (e < 0 || e >= p.E) return {-1, 0};  // a group's own id may be none; then nothing above matters
+  const uint64_t mask = __ballot(slot >= 0);
+  if (mask == 0) return {-1, 0};
+  if (p.by_slot && __builtin_amdgcn_readlane(slot, __builtin_ctzll(mask)) != group) return {-1, 0};
+  if (slot >= 0 && threadIdx.x < 64) {
+    const int c = rank_in(mask, lane);
+    cols[c] = slot;
+    if (WEIGHTS) colw[c] = w;
+  }
+  return {e, __builtin_popcountll(mask)};
+}
+
+constexpr int kFewWaves = 4;
+
+template <int F>
+__device__ inline v4f row_scales(const void* s, const float* g, int64_t row, int e) {
+  if constexpr (F == kFmtFp8) {
+    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(s) + row);
+    return v4f{f.x, f.y, f.z, f.w};
+  } else if constexpr (F == kFmtNvfp4) {
+    const float f = g[e];
+    return v4f{f, f, f, f};
+  } else {
+    return v4f{1.f, 1.f, 1.f, 1.f};
+  }
+}
+
+// One projection of one group of tokens. A tile is two sets of 16 weight rows
+// (gate/up: 16 gate rows and their up rows; down: 32 rows); KS waves split a
+// tile's K, so a workgroup holds kFewWaves / KS tiles at a time and takes
+// `rounds` such sets of tiles one after another.
+//
+// The group's input rows (gate/up: x; down: hi and lo of h) are staged in LDS
+// once, in pieces of KC inputs if they do not fit whole, and every wave reads
+// its MFMA columns from there. The weights go straight to registers, U steps
+// of 2 x 16 rows x 64 bytes at a time, with the next U steps' loads issued
+// before the current ones are used: nothing but the start waits for the
+// weight stream, and with two workgroups per CU 128 KB of it are in flight.
+template <int F, bool DOWN, int NT, int KS>
+constexpr int kRowsU = F == kFmtFp8 || (KS == 1 && !DOWN) ? 4 : 2;  // 2: a round fits 64 tokens' h, or a short split K
+
+template <int F, bool DOWN, int NT, int KS>
+__global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int wgs_per_group, int rounds,
+                                                           int lds_bytes) {
+  using W = WideFmt<F>;
+  constexpr int U = kRowsU<F, DOWN, NT, KS>;
+  using S = BlockScales<F, 2, U>;
+  constexpr int P = DOWN ? 2 : 1;                 // parts of the input: h = hi + lo
+  constexpr int kRound = U * KS * W::kStepK;      // K values a round of loads covers
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  __shared__ int cols[64];
+  __shared__ float colw[64];
+  __shared__ v4f red[KS > 1 ? kFewWaves * 2 * NT * 64 : 1];
+  __shared__ __attribute__((aligned(16))) uint8_t slds[kFewWaves][S::kLds];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int ks = wave % KS;
+  const int K = DOWN ? p.I : p.H, rows = DOWN ? p.H : 2 * p.I;
+  const int tile_rows = DOWN ? 32 : 16;           // output rows (down) or h columns (gate/up) of a tile
+  const int out_rows = DOWN ? p.H : p.I;
+  const int set_rows = DOWN ? 16 : p.I;           // distance of the two row sets
+  const int64_t rb = W::row_bytes(K), rs = W::row_scales(K);
+  const Group grp = find_group<DOWN>(p, blockIdx.x / wgs_per_group, cols, colw);
+  if (grp.e < 0) return;
+  const int e = grp.e, n = grp.n;
+  const auto rW = make_rsrc((DOWN ? p.w2 : p.w13) + (int64_t)e * rows * rb, (int64_t)rows * rb);
+  uint32_t skew;
+  const auto rS = scale_rsrc(static_cast<const uint8_t*>(DOWN ? p.s2 : p.s13) + (int64_t)e * rows * rs, (int64_t)rows * rs,
+                             &skew);
+  const auto rX = DOWN ? make_rsrc(p.h, (int64_t)p.T * p.k * p.I * 4) : make_rsrc(p.x, (int64_t)p.T * p.H * 2);
+
+  // KC: whole rounds, all of K if the n rows fit
+  const int k_all = (K + kRound - 1) / kRound * kRound;
+  const int fit = lds_bytes / (n * 2 * P) / kRound * kRound;
+  const int KC = fit < k_all ? fit : k_all;
+  const int k_pad = (k_all + KC - 1) / KC * KC;
+  const int cpr = KC >> 3;                        // 16-byte chunks of a staged row
+
+  // this wave's tiles: row0, row0 + tile_step, ...
+  const int tile_step = tile_rows * (kFewWaves / KS);
+  int row0 = (blockIdx.x % wgs_per_group) * rounds * tile_step + (wave / KS) * tile_rows;
+  const int k_wave = ks * U * W::kStepK;          // this wave's part of a round
+  struct Buf {
+    v4i w[U][2];
+    S sc;
+  } buf[2];
+  int load_k = 0, load_row = row0;
+  auto load = [&](Buf& b) {
+    const int row = load_row + r16;
+    const bool in = load_row < out_rows;
+    const uint32_t w0 = (uint32_t)(row * rb), w1 = (uint32_t)((row + set_rows) * rb);
+    const int kw = load_k + k_wave;
+    b.sc.load(rS, [&](int a) {
+      return in && kw < K ? skew + (uint32_t)((row + a * set_rows) * rs) + (uint32_t)(kw / W::kBlock) : kOutOfRange;
+    });
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = kw + u * W::kStepK + W::kLaneK * g;
+      const bool live = in && k < K;
+      b.w[u][0] = buffer_load16(rW, live ? w0 + (uint32_t)W::row_bytes(k) : kOutOfRange);
+      b.w[u][1] = buffer_load16(rW, live ? w1 + (uint32_t)W::row_bytes(k) : kOutOfRange);
+    }
+    load_k += kRound;
+    if (load_k >= k_pad) {
+      load_k = 0;
+      load_row += tile_step;
+    }
+  };
+  load(buf[0]);
+  lds_barrier();  // cols, colw
+
+  // Rows go to LDS in 1 KB pieces of 64 chunks; the 16-byte chunks of row r
+  // are stored with their index XORed with r % 8, so that the 8 rows that 8
+  // lanes read at one K lie in different banks.
+  auto stage = [&](int k0) {
+    for (int row = wave; row < P * n; row += kFewWaves) {
+      const int part = row >= n ? 1 : 0;
+      const int slot = cols[row - part * n];
+      const uint32_t base = DOWN ? (uint32_t)slot * (uint32_t)p.I * 4u + (uint32_t)part * (uint32_t)p.I * 2u
+                                 : (uint32_t)(slot / p.k) * (uint32_t)p.H * 2u;
+      uint8_t* dst = smem + row * (KC * 2);
+      for (int c0 = 0; c0 < cpr; c0 += 64) {
+        const int k = k0 + 8 * ((c0 + lane) ^ (row & 7));
+        if (c0 + lane < cpr) buffer_load16_lds(rX, dst + c0 * 16, k < K ? base + 2u * (uint32_t)k : kOutOfRange);
+      }
+    }
+  };
+  const int nt = (n + 15) >> 4;
+  uint32_t xrow[P][NT], xswz[P][NT];  // this lane's staged rows (columns past the last one read it again)
+#pragma unroll
+  for (int q = 0; q < P; ++q)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint32_t row = (uint32_t)(q * n + min(t * 16 + r16, n - 1));
+      xrow[q][t] = row * (uint32_t)(KC * 2);
+      xswz[q][t] = (row & 7u) << 4;
+    }
+  v4f scale[2];  // the current tile's row scales
+  auto load_scales = [&]() {
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+      scale[a] = row0 < out_rows ? row_scales<F>(DOWN ? p.s2 : p.s13, DOWN ? p.g2 : p.g13,
+                                                 (int64_t)e * rows + row0 + a * set_rows + 4 * g, e)
+                                 : v4f{0.f, 0.f, 0.f, 0.f};
+  };
+  load_scales();
+
   v4f acc[2][NT];
 #pragma unroll
   for (int a = 0; a < 2; ++a)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[a][t] = v4f{0.f, 0.f, 0.f, 0.f};
-  stream_dot<F, 2, NT, U>(rW, rS, wrow, srow, rX, xrow, p.H, wave, 4, acc);
+
+  auto compute = [&](const Buf& b, int kk) {  // kk: first K of the round inside the staged piece
+    b.sc.spread(slds[wave]);
 #pragma unroll
-  for (int a = 0; a < 2; ++a)
+    for (int u = 0; u < U; ++u) {
+      const uint32_t at = 2u * (uint32_t)(kk + k_wave + u * W::kStepK + W::kLaneK * g);
+      const uint32_t s0 = S::get(slds[wave], u, 0), s1 = S::get(slds[wave], u, 1);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) red[((wave * 2 + a) * NT + t) * 64 + lane] = acc[a][t];
-  __syncthreads();
-  // wave t finishes column tile t: lane (r16, g) holds column r16, h columns row0 + 4 g ..
-  const int t = wave;
-  const int c = t * 16 + r16;
-  if (t >= NT || c >= n) return;
-  v4f gu[2];
+      for (int i = 0; i < W::kMfma; ++i) {
+        const v4i w0 = widen_part<F>(b.w[u][0], s0, i), w1 = widen_part<F>(b.w[u][1], s1, i);
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    gu[a] = red[(a * NT + t) * 64 + lane];
+        for (int t = 0; t < NT; ++t) {
+          if (NT > 1 && t >= nt) break;
 #pragma unroll
-    for (int w = 1; w < 4; ++w) gu[a] += red[((w * 2 + a) * NT + t) * 64 + lane];
-    if constexpr (F == kFmtFp8) {
-      const float4 s = *reinterpret_cast<const float4*>(static_cast<const float*>(p.s13) + (int64_t)e * 2 * p.I +
-                                                        a * p.I + row0 + 4 * g);
-      gu[a] *= v4f{s.x, s.y, s.z, s.w};
-    } else if constexpr (F == kFmtNvfp4) {
-      const float s = p.g13[e];
-      gu[a] *= v4f{s, s, s, s};
+          for (int q = 0; q < P; ++q) {
+            const v4i x = *reinterpret_cast<const v4i*>(smem + xrow[q][t] + ((at + 16u * i) ^ xswz[q][t]));
+            acc[0][t] = mfma_16x16x32_bf16(w0, x, acc[0][t]);
+            acc[1][t] = mfma_16x16x32_bf16(w1, x, acc[1][t]);
+          }
+        }
+      }
     }
-  }
-  float h[4], lo[4];
+  };
+
+  auto finish = [&]() {  // the sums of tile row0: lane (r16, g) holds rows 4 g .. of both sets, column 16 t + r16
+    if constexpr (KS > 1) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) h[r] = silu_f32(gu[0][r]) * gu[1][r];
-  const uint32_t h0 = bf16x2_rne(h[0], h[1]), h1 = bf16x2_rne(h[2], h[3]);
-  lo[0] = h[0] - bf16_lo(h0);
-  lo[1] = h[1] - bf16_hi(h0);
-  lo[2] = h[2] - bf16_lo(h1);
-  lo[3] = h[3] - bf16_hi(h1);
-  uint16_t* dst = p.h + (int64_t)cols[c] * 2 * p.I + row0 + 4 * g;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(h0, h1);
-  *reinterpret_cast<uint2*>(dst + p.I) = make_uint2(bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]));
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) red[((wave * 2 + a) * NT + t) * 64 + lane] = acc[a][t];
+      lds_barrier();
+      if (ks == 0) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int w = 1; w < KS; ++w) acc[a][t] += red[(((wave + w) * 2 + a) * NT + t) * 64 + lane];
+      }
+      lds_barrier();
+    }
+    if (ks == 0 && row0 < out_rows) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int c = t * 16 + r16;
+        if (c < n) {
+          const v4f v0 = acc[0][t] * scale[0], v1 = acc[1][t] * scale[1];
+          if constexpr (DOWN) {
+            const float w = colw[c];
+            float* dst = p.y + (int64_t)cols[c] * p.H + row0 + 4 * g;
+            *reinterpret_cast<v4f*>(dst) = v0 * v4f{w, w, w, w};
+            *reinterpret_cast<v4f*>(dst + 16) = v1 * v4f{w, w, w, w};
+          } else {
+            float h[4], lo[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) h[r] = silu_f32(v0[r]) * v1[r];
+            const uint32_t h0 = bf16x2_rne(h[0], h[1]), h1 = bf16x2_rne(h[2], h[3]);
+            lo[0] = h[0] - bf16_lo(h0);
+            lo[1] = h[1] - bf16_hi(h0);
+            lo[2] = h[2] - bf16_lo(h1);
+            lo[3] = h[3] - bf16_hi(h1);
+            uint16_t* dst = p.h + (int64_t)cols[c] * 2 * p.I + row0 + 4 * g;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(h0, h1);
+            *reinterpret_cast<uint2*>(dst + p.I) = make_uint2(bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[a][t] = v4f{0.f, 0.f, 0.f, 0.f};
+    row0 += tile_step;
+  };
+
+  const int total = rounds * (k_pad / kRound);
+  int k0 = 0, kk = 0;  // first K of the current round inside its tile, inside the staged piece
+  auto step = [&](int r, const Buf& cur, Buf& next) {
+    const bool fresh = kk == 0 && (KC < k_pad || r == 0);  // a new piece of the input rows
+    if (fresh) {
+      if (r) lds_barrier();  // every wave is done with the piece before
+      stage(k0);
+    }
+    if (r + 1 < total) load(next);
+    if (fresh) {
+      wait_vmem_all();
+      lds_barrier();
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    compute(cur, kk);
+    k0 += kRound;
+    kk = kk + kRound < KC ? kk + kRound : 0;
+    if (k0 >= k_pad) {
+      k0 = 0;
+      finish();
+      if (r + 1 < total) load_scales();
+    }
+  };
+  for (int r = 0; r < total; r += 2) {
+    step(r, buf[0], buf[1]);
+    if (r + 1 < total) step(r + 1, buf[1], buf[0]);
+  }
 }
 
-// Workgroups (group, tile of 16 h columns). With no more routed copies than
-// experts a group is a copy (slot), and the first copy of an expert works for
-// all of them; otherwise a group is an expert. Either way a group that has
-// nothing to do leaves after reading the ids.
-template <int F, int NTMAX>
-__global__ __launch_bounds__(256) void few_gate_up(const FewArgs p, int tiles, int by_slot) {
-  __shared__ int cols[16 * NTMAX];
-  __shared__ v4f red[4 * 2 * NTMAX * 64];
+// out[t] = bf16(sum of the token's rows, in the order of its slots). A slot
+// counts if its id is valid and no earlier slot of the token names it.
+__global__ __launch_bounds__(256) void few_combine(const FewArgs p) {
+  const int t = blockIdx.y, lane = threadIdx.x & 63;
+  const int c = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
+  uint64_t rows = 0;
+  for (int j = 0; j < p.k; ++j) {
+    const int e = __builtin_amdgcn_readlane(id, j);
+    if (e >= 0 && e < p.E && __builtin_ctzll(__ballot(id == e)) == j) rows |= 1ull << j;
+  }
+  if (c >= p.H) return;
+  const float* y = p.y + (int64_t)t * p.k * p.H + c;
+  v4f s = v4f{0.f, 0.f, 0.f, 0.f};
+  while (rows) {
+    v4f v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = v4f{0.f, 0.f, 0.f, 0.f};
+      if (rows) v[i] = *reinterpret_cast<const v4f*>(y + (int64_t)__builtin_ctzll(rows) * p.H);
+      rows &= rows - 1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s += v[i];
+  }
+  *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.H + c) = make_uint2(bf16x2_rne(s[0], s[1]), bf16x2_rne(s[2], s[3]));
+}
+
+// At most R tokens (R = 4 or 8) and 64 slots: R output columns a workgroup,
+// so that a narrow output still fills the GPU. The 16 rows of an MFMA's
+// weight operand are R weight rows at 16 / R places of K, its 16 columns R
+// tokens at the same places: of the 16 x 16 results those count whose row and
+// column are at the same place of K, and the places are added at the end. A
+// wave takes every WAVES-th expert, in the order of their first slots; lane s
+// holds slot s's id and weight, so a ballot finds the expert's tokens.
+template <int F, int R, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void few_down_small(const FewArgs p) {
+  using W = WideFmt<F>;
+  constexpr int C = 16 / R;   // places of K
+  constexpr int U = F == kFmtFp8 ? 4 : 2;
+  __shared__ v4f red[WAVES][64];
+  __shared__ __attribute__((aligned(16))) uint8_t slds[WAVES][BlockScales<F, 1, U>::kLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = blockIdx.x / tiles, row0 = (blockIdx.x % tiles) * 16;
-  const int e = by_slot ? p.ids[group] : group;
-  if (e < 0 || e >= p.E) return;
-  int slot;
-  const uint64_t mask = tokens_of(p, e, lane, &slot);
-  if (mask == 0) return;
-  if (by_slot && __shfl(slot, __builtin_ctzll(mask), 64) != group) return;
-  const int n = __builtin_popcountll(mask);
-  if (slot >= 0 && wave == 0) cols[rank_in(mask, lane)] = slot;
-  __syncthreads();
-  if (NTMAX == 1 || n <= 16)
-    gate_up_tile<F, 1, 4>(p, e, row0, n, cols, red, wave, lane);
-  else if (NTMAX == 2 || n <= 32)
-    gate_up_tile<F, (NTMAX >= 2 ? 2 : 1), 2>(p, e, row0, n, cols, red, wave, lane);
-  else
-    gate_up_tile<F, (NTMAX >= 4 ? 4 : 1), 1>(p, e, row0, n, cols, red, wave, lane);
-}
-
-constexpr int kDownWaves = 16;
-
-// LDS written and read by the lanes of one wave: the hardware keeps a wave's
-// LDS accesses in order, this keeps the compiler to it.
-__device__ inline void wave_lds_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
-// One unit of the down projection: part `part` of `parts` of expert e's K
-// range, for all its tokens, added into this wave's accumulators.
-template <int F, int NT, int U>
-__device__ inline void down_unit(const FewArgs& p, int e, int part, int parts, int row0, int n, const int* col_slot,
-                                 const float* col_w, float* acc_w, int lane) {
-  using W = WideFmt<F>;
   const int r16 = lane & 15, g = lane >> 4;
+  const int row0 = blockIdx.x * R;
+  const int slots = p.T * p.k;
+  const int id = lane < slots ? p.ids[lane] : -1;
+  const float tw = lane < slots ? p.tw[lane] : 0.f;
+  const int tok = r16 % R;
   const int64_t rb = W::row_bytes(p.I), rs = W::row_scales(p.I);
-  const auto rW = make_rsrc(p.w2 + ((int64_t)e * p.H + row0) * rb, 16 * rb);
-  const auto rS = make_rsrc(static_cast<const uint8_t*>(p.s2) + ((int64_t)e * p.H + row0) * rs, 16 * rs);
-  const auto rX = make_rsrc(p.h, (int64_t)p.T * p.k * p.I * 4);
-  const uint32_t wrow[1] = {(uint32_t)(r16 * rb)}, srow[1] = {(uint32_t)(r16 * rs)};
-  uint32_t xrow[2 * NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int c = t * 16 + r16;
-    xrow[t] = c < n ? (uint32_t)col_slot[c] * (uint32_t)p.I * 4u : kOutOfRange;
-    xrow[NT + t] = c < n ? xrow[t] + (uint32_t)p.I * 2u : kOutOfRange;
-  }
-  v4f s = v4f{1.f, 1.f, 1.f, 1.f};
-  if constexpr (F == kFmtFp8) {
-    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p.s2) + (int64_t)e * p.H + row0 + 4 * g);
-    s = v4f{f.x, f.y, f.z, f.w};
-  } else if constexpr (F == kFmtNvfp4) {
-    const float f = p.g2[e];
-    s = v4f{f, f, f, f};
-  }
-  v4f acc[1][2 * NT];
-#pragma unroll
-  for (int t = 0; t < 2 * NT; ++t) acc[0][t] = v4f{0.f, 0.f, 0.f, 0.f};
-  stream_dot<F, 1, 2 * NT, U>(rW, rS, wrow, srow, rX, xrow, p.I, part, parts, acc);
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int c = t * 16 + r16;
-    if (c < n) {
-      const float w = col_w[c];
-      v4f* a = reinterpret_cast<v4f*>(acc_w + (col_slot[c] / p.k) * 16 + 4 * g);
-      *a += (acc[0][t] + acc[0][NT + t]) * s * v4f{w, w, w, w};
+  const int steps = ((p.I + W::kStepK - 1) / W::kStepK + C - 1) / C;  // of one place
+  const auto rX = make_rsrc(p.h, (int64_t)slots * p.I * 4);
+  const uint32_t wrow[1] = {(uint32_t)((r16 % R) * rb)};
+  v4f y = v4f{0.f, 0.f, 0.f, 0.f};
+  int turn = wave;  // experts until this wave's next one
+  for (int s = 0; s < slots; ++s) {
+    const int e = __builtin_amdgcn_readlane(id, s);
+    if (e < 0 || e >= p.E) continue;
+    const uint64_t same = __ballot(id == e);
+    if (__builtin_ctzll(same) != s || turn-- != 0) continue;
+    turn = WAVES - 1;
+    const auto rW = make_rsrc(p.w2 + ((int64_t)e * p.H + row0) * rb, R * rb);
+    uint32_t skew;
+    const auto rS = scale_rsrc(static_cast<const uint8_t*>(p.s2) + ((int64_t)e * p.H + row0) * rs, R * rs, &skew);
+    const uint32_t srow[1] = {skew + (uint32_t)((r16 % R) * rs)};
+    const uint64_t kmask = p.k == 64 ? ~0ull : (1ull << p.k) - 1;
+    uint64_t mine = tok < p.T ? (same >> (tok * p.k)) & kmask : 0;
+    const int slot = mine ? tok * p.k + __builtin_ctzll(mine) : 0;
+    const uint32_t at = (uint32_t)slot * (uint32_t)p.I * 4u;
+    const uint32_t xrow[2] = {mine ? at : kOutOfRange, mine ? at + (uint32_t)p.I * 2u : kOutOfRange};
+    float w = 0.f;
+    while (__ballot(mine != 0)) {  // once, or again for a token that names the expert again
+      const float v = __shfl(tw, mine ? tok * p.k + __builtin_ctzll(mine) : 0, 64);
+      w += mine ? v : 0.f;
+      mine &= mine - 1;
     }
+    v4f acc[1][2] = {{v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}}};
+    stream_dot<F, 1, 2, U>(rW, rS, wrow, srow, rX, xrow, p.I, (r16 / R) * steps * W::kStepK, steps, slds[wave], acc);
+    y += (acc[0][0] + acc[0][1]) * row_scales<F>(p.s2, p.g2, (int64_t)e * p.H + row0 + (4 * g) % R, e) *
+         v4f{w, w, w, w};
   }
-}
-
-template <int F, int NTMAX>
-__global__ __launch_bounds__(64 * kDownWaves) void few_down(const FewArgs p) {
-  constexpr int TMAX = 16 * NTMAX;
-  __shared__ unsigned long long mask[kFewMaxE];      // tokens of each expert
-  __shared__ uint16_t active[kFewMaxE];              // experts with tokens, ascending
-  __shared__ int s_ids[kFewMaxSlots];
-  __shared__ float s_tw[kFewMaxSlots];
-  __shared__ int s_active;
-  __shared__ int col_slot[kDownWaves][TMAX];
-  __shared__ float col_w[kDownWaves][TMAX];
-  __shared__ v4f acc[kDownWaves][TMAX * 4];          // [wave][token][16 output columns]
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int row0 = blockIdx.x * 16;
-  for (int i = tid; i < p.E; i += 64 * kDownWaves) mask[i] = 0;
-  for (int i = lane; i < p.T * 4; i += 64) acc[wave][i] = v4f{0.f, 0.f, 0.f, 0.f};
+  // lane (r16, g): rows 4 g .. 4 g + 3 of the operand, that is output columns
+  // row0 + (4 g) % R .. at place 4 g / R; column r16: token r16 % R at place r16 / R
+  red[wave][lane] = y;
   __syncthreads();
-  for (int i = tid; i < p.T * p.k; i += 64 * kDownWaves) {
-    const int e = p.ids[i];
-    s_ids[i] = e;
-    s_tw[i] = p.tw[i];
-    if (e >= 0 && e < p.E) atomicOr(&mask[e], 1ull << (i / p.k));
-  }
-  __syncthreads();
-  if (wave == 0) {
-    int n = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 64) {
-      const bool on = e0 + lane < p.E && mask[e0 + lane] != 0;
-      const uint64_t m = __ballot(on);
-      if (on) active[n + rank_in(m, lane)] = (uint16_t)(e0 + lane);
-      n += __builtin_popcountll(m);
-    }
-    if (lane == 0) s_active = n;
-  }
-  __syncthreads();
-  const int na = s_active;
-  // Few experts are cut into parts of K, so that every wave has a unit.
-  const int nk = (p.I + WideFmt<F>::kStepK - 1) / WideFmt<F>::kStepK;
-  int parts = 1;
-  while (parts < nk && parts * na < kDownWaves) parts *= 2;
-  for (int u = wave; u < na * parts; u += kDownWaves) {
-    const int e = active[u / parts];
-    const uint64_t m = mask[e];
-    const int n = __builtin_popcountll(m);
-    if ((m >> lane) & 1) {
-      float w = 0.f;
-      int first = -1;
-      for (int j = p.k - 1; j >= 0; --j)
-        if (s_ids[lane * p.k + j] == e) {
-          first = lane * p.k + j;
-          w += s_tw[first];
-        }
-      const int c = rank_in(m, lane);
-      col_slot[wave][c] = first;
-      col_w[wave][c] = w;
-    }
-    wave_lds_order();
-    const int part = u % parts;
-    if (NTMAX == 1 || n <= 16)
-      down_unit<F, 1, 4>(p, e, part, parts, row0, n, col_slot[wave], col_w[wave], (float*)acc[wave], lane);
-    else if (NTMAX == 2 || n <= 32)
-      down_unit<F, (NTMAX >= 2 ? 2 : 1), 1>(p, e, part, parts, row0, n, col_slot[wave], col_w[wave], (float*)acc[wave], lane);
-    else
-      down_unit<F, (NTMAX >= 4 ? 4 : 1), 1>(p, e, part, parts, row0, n, col_slot[wave], col_w[wave], (float*)acc[wave], lane);
-    wave_lds_order();
-  }
-  __syncthreads();
-  for (int i = tid; i < p.T * 4; i += 64 * kDownWaves) {
-    v4f s = acc[0][i];
+  if (threadIdx.x < R * R / 4) {
+    const int t = threadIdx.x % R, q = threadIdx.x / R;  // token, quarter of the columns
+    if (t >= p.T) return;
+    v4f s = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int w = 0; w < WAVES; ++w)
 #pragma unroll
-    for (int w = 1; w < kDownWaves; ++w) s += acc[w][i];
-    *reinterpret_cast<uint2*>(p.out + (int64_t)(i >> 2) * p.H + row0 + 4 * (i & 3)) =
+      for (int c = 0; c < C; ++c) s += red[w][(c * (R / 4) + q) * 16 + c * R + t];
+    *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.H + row0 + 4 * q) =
         make_uint2(bf16x2_rne(s[0], s[1]), bf16x2_rne(s[2], s[3]));
   }
 }
 
-template <int F, int NTMAX>
-hipError_t launch_few_nt(const FewArgs& a, hipStream_t stream) {
-  const int tiles = a.I / 16;
-  const int by_slot = a.T * a.k <= a.E ? 1 : 0;
-  const int groups = by_slot ? a.T * a.k : a.E;
-  hipLaunchKernelGGL((few_gate_up<F, NTMAX>), dim3(groups * tiles), dim3(256), 0, stream, a, tiles, by_slot);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((few_down<F, NTMAX>), dim3(a.H / 16), dim3(64 * kDownWaves), 0, stream, a);
+// The small form takes the step's slots into one wave's lanes and its tokens
+// into one operand.
+bool few_small(int64_t T, int64_t topk) { return T <= 8 && T * topk <= 64; }
+
+template <int F, bool DOWN, int NT, int KS>
+void launch_rows_ks(const FewArgs& a, int groups, hipStream_t stream) {
+  const int K = DOWN ? a.I : a.H, P = DOWN ? 2 : 1;
+  const int tiles = (DOWN ? a.H : a.I) / (DOWN ? 32 : 16), per_wg = kFewWaves / KS;
+  const int sets = (tiles + per_wg - 1) / per_wg;  // sets of tiles a group has
+  const int rounds = 1;
+  const int wgs = (sets + rounds - 1) / rounds;
+  const int round_k = kRowsU<F, DOWN, NT, KS> * KS * WideFmt<F>::kStepK;
+  const int k_all = (K + round_k - 1) / round_k * round_k;
+  const int rows = (int)(a.T < 64 ? a.T : 64);
+  const int64_t want = (int64_t)rows * k_all * 2 * P;
+  const int lds = (int)(want < 65536 ? (want + 1023) / 1024 * 1024 : 65536);  // a load writes 1 KB
+  hipLaunchKernelGGL((few_rows<F, DOWN, NT, KS>), dim3((unsigned)(groups * wgs)), dim3(64 * kFewWaves), lds, stream, a, wgs,
+                     rounds, lds);
+}
+
+template <int F, bool DOWN>
+hipError_t launch_rows(const FewArgs& a, hipStream_t stream) {
+  const int groups = a.by_slot ? a.T * a.k : a.E;
+  const int tiles = groups * ((DOWN ? a.H : a.I) / (DOWN ? 32 : 16));
+  if (a.T > 16)
+    launch_rows_ks<F, DOWN, 4, 1>(a, groups, stream);
+  else if (tiles <= 768)
+    launch_rows_ks<F, DOWN, 1, 4>(a, groups, stream);
+  else if (tiles <= 1536)
+    launch_rows_ks<F, DOWN, 1, 2>(a, groups, stream);
+  else
+    launch_rows_ks<F, DOWN, 1, 1>(a, groups, stream);
   return hipGetLastError();
 }
 
 template <int F>
 hipError_t launch_few_fmt(const FewArgs& a, hipStream_t stream) {
-  if (a.T <= 16) return launch_few_nt<F, 1>(a, stream);
-  if (a.T <= 32) return launch_few_nt<F, 2>(a, stream);
-  return launch_few_nt<F, 4>(a, stream);
-}
-
-}  // namespace
-
-hipError_t launch_router(const uint16_t* x, const uint16_t* wr, const float* bias, int32_t* ids, float* tw, int64_t T,
-                         int64_t H, int64_t E, int64_t topk, int sigmoid, int renorm, float scale,
-                         hipStream_t stream) {
-  const RouterArgs a{x, wr, bias, ids, tw, (int)T, (int)H, (int)E, (int)topk, sigmoid, renorm, scale};
-  if (T <= 256)
-    hipLaunchKernelGGL(router<1>, dim3((unsigned)T), dim3(kRouterThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL(router<4>, dim3((unsigned)((T + 3) / 4)), dim3(kRouterThreads), 0, stream, a);
+  hipError_t e = launch_rows<F, false>(a, stream);
+  if (e != hipSuccess) return e;
+  if (few_small(a.T, a.k)) {
+    if (a.T <= 4)
+      hipLaunchKernelGGL((few_down_small<F, 4, 8>), dim3(a.H / 4), dim3(64 * 8), 0, stream, a);
+    else
+      hipLaunchKernelGGL((few_down_small<F, 8, 16>), dim3(a.H / 8), dim3(64 * 16), 0, stream, a);
+    return hipGetLastError();
+  }
+  e = launch_rows<F, true>(a, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(few_combine, dim3((a.H + 1023) / 1024, a.T), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
-size_t few_workspace_bytes(int64_t T, int64_t I, int64_t topk) { return (size_t)(T * topk * I * 4); }
+size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t router_workspace_bytes(int64_t T, int64_t E) { return (size_t)(T * E * 8); }
+
+hipError_t launch_router(const uint16_t* x, const uint16_t* wr, const float* bias, int32_t* ids, float* tw, int64_t T,
+                         int64_t H, int64_t E, int64_t topk, int sigmoid, int renorm, float scale, void* ws,
+                         hipStream_t stream) {
+  const RouterArgs a{x, wr, bias, static_cast<double*>(ws), ids, tw, (int)T, (int)H, (int)E, (int)topk, sigmoid, renorm,
+                     scale};
+  const unsigned e4 = (unsigned)((E + 3) / 4);
+  if (T <= 2)
+    hipLaunchKernelGGL(router_logits_few<1>, dim3(e4, (unsigned)T), dim3(256), 0, stream, a);
+  else if (T <= 64)
+    hipLaunchKernelGGL(router_logits_few<4>, dim3(e4, (unsigned)((T + 3) / 4)), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL(router_logits_mfma, dim3((unsigned)((T + 15) / 16 * ((E + 15) / 16))), dim3(512), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (E <= 64)
+    hipLaunchKernelGGL(router_select<1>, dim3((unsigned)T), dim3(64), 0, stream, a);
+  else if (E <= 256)
+    hipLaunchKernelGGL(router_select<4>, dim3((unsigned)T), dim3(64), 0, stream, a);
+  else
+    hipLaunchKernelGGL(router_select<16>, dim3((unsigned)T), dim3(64), 0, stream, a);
+  return hipGetLastError();
+}
+
+// h, then the y rows; the router's logits, which are read before y is
+// written, share the y rows' place.
+static size_t few_h_bytes(int64_t T, int64_t I, int64_t topk) { return align256((size_t)(T * topk * I * 4)); }
+
+size_t few_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t topk) {
+  return few_h_bytes(T, I, topk) + (few_small(T, topk) ? 0 : (size_t)(T * topk * H * 4));
+}
+
+size_t few_layer_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
+  const size_t y = few_workspace_bytes(T, H, I, topk) - few_h_bytes(T, I, topk), l = router_workspace_bytes(T, E);
+  return few_h_bytes(T, I, topk) + (y > l ? y : l);
+}
+
+void* few_layer_logits(void* ws, int64_t T, int64_t I, int64_t topk) {
+  return static_cast<uint8_t*>(ws) + few_h_bytes(T, I, topk);
+}
 
 hipError_t launch_few(int format, const uint16_t* x, const int32_t* ids, const float* tw, const uint8_t* w13,
                       const void* s13, const float* g13, const uint8_t* w2, const void* s2, const float* g2,
                       uint16_t* out, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, void* ws,
                       hipStream_t stream) {
-  const FewArgs a{x,   ids, tw,     w13,    s13,    g13,    w2,        s2, g2, static_cast<uint16_t*>(ws),
-                  out, (int)T, (int)H, (int)I, (int)E, (int)topk};
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  const FewArgs a{x,  ids, tw, w13, s13, g13, w2, s2, g2, reinterpret_cast<uint16_t*>(b),
+                  reinterpret_cast<float*>(b + few_h_bytes(T, I, topk)), out, (int)T, (int)H, (int)I, (int)E, (int)topk,
+                  T * topk <= E ? 1 : 0};
   if (format == kFmtFp8) return launch_few_fmt<kFmtFp8>(a, stream);
   if (format == kFmtMxfp4) return launch_few_fmt<kFmtMxfp4>(a, stream);
   return launch_few_fmt<kFmtNvfp4>(a, stream);

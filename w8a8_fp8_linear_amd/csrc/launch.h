@@ -143,8 +143,12 @@ hipError_t launch_w4a16_gemm(int format, const uint16_t* x, const uint8_t* w, co
 // The few-token routed-expert layer (few.hip).
 constexpr int64_t kFewMaxTokens = 64, kFewMaxSlots = 1024;
 hipError_t launch_router(const uint16_t* x, const uint16_t* wr, const float* bias, int32_t* ids, float* tw, int64_t T,
-                         int64_t H, int64_t E, int64_t topk, int sigmoid, int renorm, float scale, hipStream_t stream);
-size_t few_workspace_bytes(int64_t T, int64_t I, int64_t topk);
+                         int64_t H, int64_t E, int64_t topk, int sigmoid, int renorm, float scale, void* ws,
+                         hipStream_t stream);
+size_t router_workspace_bytes(int64_t T, int64_t E);
+size_t few_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t topk);
+size_t few_layer_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
+void* few_layer_logits(void* ws, int64_t T, int64_t I, int64_t topk);  // the router's part of the layer's workspace
 hipError_t launch_few(int format, const uint16_t* x, const int32_t* ids, const float* tw, const uint8_t* w13,
                       const void* s13, const float* g13, const uint8_t* w2, const void* s2, const float* g2,
                       uint16_t* out, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, void* ws,

@@ -43,15 +43,17 @@ template <int F, int MT, int U>
 __global__ __launch_bounds__(256) void w4a16_skinny(const W4Args p) {
   using W = WideFmt<F>;
   __shared__ v4f red[3][MT][64];
+  __shared__ __attribute__((aligned(16))) uint8_t slds[4][BlockScales<F, 1, U>::kLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = blockIdx.x * 16;
   const int64_t rb = W::row_bytes(p.K), rs = W::row_scales(p.K);
   const auto rW = make_rsrc(p.w + n0 * rb, (p.N - n0) * rb);
-  const auto rS = make_rsrc(p.s + n0 * rs, (p.N - n0) * rs);
+  uint32_t skew;
+  const auto rS = scale_rsrc(p.s + n0 * rs, (p.N - n0) * rs, &skew);
   const auto rX = make_rsrc(p.x, (int64_t)p.M * p.K * 2);
   const int r16 = lane & 15, g = lane >> 4;
-  const uint32_t wrow[1] = {(uint32_t)(r16 * rb)}, srow[1] = {(uint32_t)(r16 * rs)};
+  const uint32_t wrow[1] = {(uint32_t)(r16 * rb)}, srow[1] = {skew + (uint32_t)(r16 * rs)};
   uint32_t xrow[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) xrow[t] = t * 16 + r16 < p.M ? (uint32_t)(t * 16 + r16) * (uint32_t)p.K * 2u : kOutOfRange;
@@ -59,7 +61,8 @@ __global__ __launch_bounds__(256) void w4a16_skinny(const W4Args p) {
   v4f acc[1][MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) acc[0][t] = v4f{0.f, 0.f, 0.f, 0.f};
-  stream_dot<F, 1, MT, U>(rW, rS, wrow, srow, rX, xrow, p.K, wave, 4, acc);
+  const int steps = ((p.K + W::kStepK - 1) / W::kStepK + 3) / 4;  // of a wave's quarter of K
+  stream_dot<F, 1, MT, U>(rW, rS, wrow, srow, rX, xrow, p.K, wave * steps * W::kStepK, steps, slds[wave], acc);
   if (wave > 0) {
 #pragma unroll
     for (int t = 0; t < MT; ++t) red[wave - 1][t][lane] = acc[0][t];

@@ -85,16 +85,79 @@ struct WideFmt {
   __host__ __device__ static constexpr int64_t row_scales(int64_t K) { return F == kFmtFp8 ? 0 : K / kBlock; }
 };
 
-// The lane's block scales of one step (K values k .. k + 31 of a row whose
-// scale bytes start at srow): one E8M0 byte or two E4M3 bytes.
-template <int F>
-__device__ inline uint32_t load_block_scales(__amdgpu_buffer_rsrc_t r, uint32_t srow, int k, bool live) {
-  if constexpr (F == kFmtMxfp4)
-    return __builtin_amdgcn_raw_buffer_load_b8(r, live ? srow + (uint32_t)(k >> 5) : kOutOfRange, 0, 0);
-  else if constexpr (F == kFmtNvfp4)
-    return __builtin_amdgcn_raw_buffer_load_b16(r, live ? srow + (uint32_t)(k >> 4) : kOutOfRange, 0, 0);
-  else
+// LDS written and read by the lanes of one wave: the hardware keeps a wave's
+// LDS accesses in order, this keeps the compiler to it.
+__device__ inline void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// The block scales of U consecutive steps of NR sets of 16 weight rows. Read
+// where they are used they would be one or two bytes a lane, 16 cache lines
+// per load for 64 or 128 bytes; instead lane 16 g + r loads 16 bytes of row r
+// of set g / kPieces at once, and hands them out through 1 KB of LDS that the
+// wave keeps for itself. Scale rows start at any byte: the dwords around the
+// piece are loaded and shifted (a dword that holds a byte of the tensor can
+// always be read).
+template <int F, int NR, int U>
+struct BlockScales {
+  static constexpr bool kAny = F != kFmtFp8;
+  static constexpr int kStepBytes = kAny ? WideFmt<F>::kStepK / WideFmt<F>::kBlock : 0;
+  static constexpr int kPieces = U * kStepBytes > 16 ? U * kStepBytes / 16 : 1;
+  static constexpr int kLds = kAny ? 1024 : 16;  // bytes of LDS a wave needs
+  static_assert(NR * kPieces <= 4, "a wave's 64 lanes load all pieces at once");
+  v4i q;
+  uint32_t top, shift;
+
+  // off(a): byte offset in r of set a's first scale of these steps, for this
+  // lane's row; r begins at a multiple of 16.
+  template <class OFF>
+  __device__ inline void load(__amdgpu_buffer_rsrc_t r, const OFF& off) {
+    if constexpr (kAny) {
+      const int g = (threadIdx.x & 63) >> 4;
+      uint32_t at = kOutOfRange;
+#pragma unroll
+      for (int a = 0; a < NR; ++a)
+        if (g / kPieces == a) at = off(a) + (uint32_t)(g % kPieces) * 16u;
+      shift = at & 3u;
+      q = buffer_load16(r, at & ~3u);
+      top = __builtin_amdgcn_raw_buffer_load_b32(r, (at & ~3u) + 16u, 0, 0);
+    }
+  }
+
+  // To the wave's LDS; the scales of step u, set a are then at get().
+  __device__ inline void spread(uint8_t* lds) const {
+    if constexpr (kAny) {
+      const uint32_t d[5] = {(uint32_t)q.x, (uint32_t)q.y, (uint32_t)q.z, (uint32_t)q.w, top};
+      v4i o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = (int)__builtin_amdgcn_alignbyte(d[i + 1], d[i], shift);
+      wave_lds_order();
+      *reinterpret_cast<v4i*>(lds + (threadIdx.x & 63) * 16) = o;
+      wave_lds_order();
+    }
+  }
+
+  static __device__ inline uint32_t get(const uint8_t* lds, int u, int a) {
+    if constexpr (kAny) {
+      const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+      const int at = u * kStepBytes;  // g's bytes follow: never past a 16-byte piece
+      const uint8_t* s = lds + (r16 + 16 * (a * kPieces + at / 16)) * 16 + at % 16;
+      if constexpr (F == kFmtMxfp4)
+        return s[g];
+      else
+        return reinterpret_cast<const uint16_t*>(s)[g];
+    }
     return 0;
+  }
+};
+
+// A resource over the scale rows of one matrix that begins at any byte:
+// `skew` is where the matrix begins in it.
+__device__ inline __amdgpu_buffer_rsrc_t scale_rsrc(const void* base, int64_t bytes, uint32_t* skew) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(base);
+  *skew = (uint32_t)(b & 15u);
+  return make_rsrc(reinterpret_cast<const void*>(b & ~(uintptr_t)15), (bytes + *skew + 3) & ~(int64_t)3);
 }
 
 // The MFMA operand i (8 BF16 values) of a lane's 16 code bytes.
@@ -111,31 +174,30 @@ __device__ inline v4i widen_part(v4i w, uint32_t sc, int i) {
   }
 }
 
-// acc[a][t] += W[16 rows of set a][K] . X[16 rows of tile t][K]^T over the K
-// steps first, first + stride, ... of ceil(K / kStepK). wrow / srow: byte
-// offsets of this lane's row (lane % 16) of each set in rW / rS; xrow: of its
-// X row (kOutOfRange for an empty column; any offset from there on reads
-// zeros). U steps' loads are issued together ahead of their MFMAs: bytes in
-// flight are what a weight stream needs.
+// acc[a][t] += W[16 rows of set a][K] . X[16 rows of tile t][K]^T over `steps`
+// K steps from this lane's kbase on. wrow / srow: byte offsets of this lane's
+// row of each set in rW / rS; xrow: of its X row (kOutOfRange for an empty
+// column; any offset from there on reads zeros). U steps' loads are issued
+// together ahead of their MFMAs: bytes in flight are what a weight stream
+// needs. lds: BlockScales::kLds bytes of this wave.
 template <int F, int NR, int NT, int U>
 __device__ inline void stream_dot(__amdgpu_buffer_rsrc_t rW, __amdgpu_buffer_rsrc_t rS, const uint32_t (&wrow)[NR],
                                   const uint32_t (&srow)[NR], __amdgpu_buffer_rsrc_t rX, const uint32_t (&xrow)[NT],
-                                  int K, int first, int stride, v4f (&acc)[NR][NT]) {
+                                  int K, int kbase, int steps, uint8_t* lds, v4f (&acc)[NR][NT]) {
   using W = WideFmt<F>;
-  const int g = (threadIdx.x & 63) >> 4;
-  const int nk = (K + W::kStepK - 1) / W::kStepK;
-  for (int kt = first; kt < nk; kt += stride * U) {
+  using S = BlockScales<F, NR, U>;
+  const int kg = W::kLaneK * ((threadIdx.x & 63) >> 4);
+  for (int kt = 0; kt < steps; kt += U) {
     v4i w[U][NR], x[U][NT][W::kMfma];
-    uint32_t sc[U][NR];
+    S sc;
+    const int k0 = kbase + kt * W::kStepK;
+    sc.load(rS, [&](int a) { return k0 < K ? srow[a] + (uint32_t)(k0 / W::kBlock) : kOutOfRange; });
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = (kt + stride * u) * W::kStepK + W::kLaneK * g;  // K is a multiple of kLaneK: all in or all out
-      const bool live = kt + stride * u < nk && k < K;
+      const int k = k0 + u * W::kStepK + kg;  // K is a multiple of kLaneK: a lane is all in or all out
+      const bool live = kt + u < steps && k < K;
 #pragma unroll
-      for (int a = 0; a < NR; ++a) {
-        w[u][a] = buffer_load16(rW, live ? wrow[a] + (uint32_t)W::row_bytes(k) : kOutOfRange);
-        sc[u][a] = load_block_scales<F>(rS, srow[a], k, live);
-      }
+      for (int a = 0; a < NR; ++a) w[u][a] = buffer_load16(rW, live ? wrow[a] + (uint32_t)W::row_bytes(k) : kOutOfRange);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -143,16 +205,21 @@ __device__ inline void stream_dot(__amdgpu_buffer_rsrc_t rW, __amdgpu_buffer_rsr
           x[u][t][i] = buffer_load16(rX, live ? xrow[t] + (uint32_t)(2 * k + 16 * i) : kOutOfRange);
     }
     __builtin_amdgcn_sched_barrier(0);
+    sc.spread(lds);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      uint32_t s[NR];
+#pragma unroll
+      for (int a = 0; a < NR; ++a) s[a] = S::get(lds, u, a);
 #pragma unroll
       for (int i = 0; i < W::kMfma; ++i)
 #pragma unroll
         for (int a = 0; a < NR; ++a) {
-          const v4i b = widen_part<F>(w[u][a], sc[u][a], i);
+          const v4i b = widen_part<F>(w[u][a], s[a], i);
 #pragma unroll
           for (int t = 0; t < NT; ++t) acc[a][t] = mfma_16x16x32_bf16(b, x[u][t][i], acc[a][t]);
         }
+    }
   }
 }
 
