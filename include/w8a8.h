@@ -550,8 +550,8 @@ size_t nvfp4_quantize_workspace_bytes(int64_t G, int64_t R, int64_t K);
  *           2^-96 and 2^112; a block whose scale would pass 448 saturates)
  *   workspace  nvfp4_quantize_workspace_bytes bytes; may be NULL where
  *           gscale_given != 0
- *   K a positive multiple of 16, R * K at most 2^40, at most 2^31 - 1 chunks
- *   of 32768 values in all.
+ *   K a positive multiple of 16, R * K at most 2^40; groups are cut into at
+ *   most 1024 chunks of 4096 values or more, at most 2^31 - 1 in all.
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, WORKSPACE, DEVICE,
  *         LAUNCH.
  */

@@ -782,35 +782,57 @@ def moe_mxfp4_ffn(x, routes, w13_q, w13_scale, w2_q, w2_scale, workspace=None):
 # gscale [groups].
 
 
+def _refuse(t, dtype, shape, dev, name):
+    """What is wrong with an argument that _same_device found wanting."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of x")
+    raise ValueError(f"{name} must be contiguous")
+
+
 def _same_device(x, *named):
     """The arguments of a call, each (tensor, dtype, shape, name): checked
     against x's device, their type and shape; all contiguous. Returns x's
     device index."""
-    if not x.is_cuda:
-        raise ValueError("x must be on a GPU")
     dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be on a GPU")
     for t, dtype, shape, name in named:
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be on the device of x")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+            _refuse(t, dtype, shape, dev, name)
     return dev
+
+
+_raw_stream = None
+
+
+def _stream_of(dev: int) -> int:
+    """Handle of device ``dev``'s current stream. torch's raw getter where there
+    is one: a tenth of the time of building a Stream object, which the calls
+    that take a few microseconds would wait for."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(dev)
 
 
 def _call(dev: int, name: str, *args):
     """The library's call on device ``dev`` and its current stream."""
     import torch
 
-    stream = torch.cuda.current_stream(dev).cuda_stream
     if torch.cuda.current_device() == dev:
-        _check(name, getattr(lib(), name)(*args, stream))
+        status = getattr(_lib or lib(), name)(*args, _stream_of(dev))
     else:
         with torch.cuda.device(dev):
-            _check(name, getattr(lib(), name)(*args, stream))
+            status = getattr(_lib or lib(), name)(*args, _stream_of(dev))
+    if status:
+        _check(name, status)
 
 
 def _nvfp4_groups(shape):

@@ -35,6 +35,8 @@
 
 #include <float.h>
 
+#include <type_traits>
+
 namespace w8a8 {
 namespace {
 
@@ -190,11 +192,10 @@ __global__ __launch_bounds__(512) void router_logits_mfma(const RouterArgs p) {
 
 // The choice: a wave per token, lane l holding the NV experts from NV * l on.
 // k times the largest of what is left: the lanes' largest, the wave's, and
-// the first lane that has it, so that equal scores go by index.
+// the first lane that has it, so that equal scores go by index. Lane j < k
+// returns the j-th expert and its weight.
 template <int NV>
-__global__ __launch_bounds__(64) void router_select(const RouterArgs p) {
-  const int lane = threadIdx.x;
-  const int t = blockIdx.x;
+__device__ inline void select_token(const RouterArgs& p, int t, int lane, int* id, float* tw) {
   const double* l = p.logits + (int64_t)t * p.E;
   double val[NV], sel[NV];
   float bias[NV];
@@ -255,9 +256,19 @@ __global__ __launch_bounds__(64) void router_select(const RouterArgs p) {
     for (int i = 0; i < NV; ++i)
       if (lane == from && i == at) sel[i] = -INFINITY;
   }
+  *id = mine_e;
+  *tw = (float)((p.renorm ? mine / all : mine) * (double)p.scale);
+}
+
+template <int NV>
+__global__ __launch_bounds__(64) void router_select(const RouterArgs p) {
+  const int lane = threadIdx.x, t = blockIdx.x;
+  int id;
+  float tw;
+  select_token<NV>(p, t, lane, &id, &tw);
   if (lane < p.k) {
-    p.ids[(int64_t)t * p.k + lane] = mine_e;
-    p.tw[(int64_t)t * p.k + lane] = (float)((p.renorm ? mine / all : mine) * (double)p.scale);
+    p.ids[(int64_t)t * p.k + lane] = id;
+    p.tw[(int64_t)t * p.k + lane] = tw;
   }
 }
 
@@ -360,7 +371,7 @@ template <int F, bool DOWN, int NT, int KS>
 constexpr int kRowsU = F == kFmtFp8 || (KS == 1 && !DOWN) ? 4 : 2;  // 2: a round fits 64 tokens' h, or a short split K
 
 template <int F, bool DOWN, int NT, int KS>
-__global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int wgs_per_group, int rounds,
+__global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(2, 4))) void few_rows(const FewArgs p, int wgs_per_group, int rounds,
                                                            int lds_bytes) {
   using W = WideFmt<F>;
   constexpr int U = kRowsU<F, DOWN, NT, KS>;
@@ -383,13 +394,24 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
   const int64_t rb = W::row_bytes(K), rs = W::row_scales(K);
   const Group grp = find_group<DOWN>(p, blockIdx.x / wgs_per_group, cols, colw);
   if (grp.e < 0) return;
-  const int e = grp.e, n = grp.n;
+  const int e = grp.e;
   const auto rW = make_rsrc((DOWN ? p.w2 : p.w13) + (int64_t)e * rows * rb, (int64_t)rows * rb);
   uint32_t skew;
   const auto rS = scale_rsrc(static_cast<const uint8_t*>(DOWN ? p.s2 : p.s13) + (int64_t)e * rows * rs, (int64_t)rows * rs,
                              &skew);
   const auto rX = DOWN ? make_rsrc(p.h, (int64_t)p.T * p.k * p.I * 4) : make_rsrc(p.x, (int64_t)p.T * p.H * 2);
 
+  // this wave's tiles: row0, row0 + tile_step, ...
+  const int tile_step = tile_rows * (kFewWaves / KS);
+  const int row_first = (blockIdx.x % wgs_per_group) * rounds * tile_step + (wave / KS) * tile_rows;
+  const int k_wave = ks * U * W::kStepK;          // this wave's part of a round
+  lds_barrier();  // cols, colw
+
+  // The pass over the weights for columns first .. first + n - 1 in TT column
+  // tiles: a copy of the code for each TT, so that none has a branch on the
+  // number of tiles inside.
+  auto pass = [&](auto tt, const int first, const int n) {
+  constexpr int TT = decltype(tt)::value;
   // KC: whole rounds, all of K if the n rows fit
   const int k_all = (K + kRound - 1) / kRound * kRound;
   const int fit = lds_bytes / (n * 2 * P) / kRound * kRound;
@@ -397,18 +419,18 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
   const int k_pad = (k_all + KC - 1) / KC * KC;
   const int cpr = KC >> 3;                        // 16-byte chunks of a staged row
 
-  // this wave's tiles: row0, row0 + tile_step, ...
-  const int tile_step = tile_rows * (kFewWaves / KS);
-  int row0 = (blockIdx.x % wgs_per_group) * rounds * tile_step + (wave / KS) * tile_rows;
-  const int k_wave = ks * U * W::kStepK;          // this wave's part of a round
+  int row0 = row_first;
   struct Buf {
     v4i w[U][2];
     S sc;
   } buf[2];
+  // The loads of one round. They are issued whether or not there is one (then
+  // out of range, which reads nothing): behind a branch the compiler would
+  // have to wait for all of them before the first use of the round before.
   int load_k = 0, load_row = row0;
-  auto load = [&](Buf& b) {
+  auto load = [&](Buf& b, bool there) {
     const int row = load_row + r16;
-    const bool in = load_row < out_rows;
+    const bool in = there && load_row < out_rows;
     const uint32_t w0 = (uint32_t)(row * rb), w1 = (uint32_t)((row + set_rows) * rb);
     const int kw = load_k + k_wave;
     b.sc.load(rS, [&](int a) {
@@ -427,8 +449,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
       load_row += tile_step;
     }
   };
-  load(buf[0]);
-  lds_barrier();  // cols, colw
+  load(buf[0], true);
 
   // Rows go to LDS in 1 KB pieces of 64 chunks; the 16-byte chunks of row r
   // are stored with their index XORed with r % 8, so that the 8 rows that 8
@@ -436,7 +457,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
   auto stage = [&](int k0) {
     for (int row = wave; row < P * n; row += kFewWaves) {
       const int part = row >= n ? 1 : 0;
-      const int slot = cols[row - part * n];
+      const int slot = cols[first + row - part * n];
       const uint32_t base = DOWN ? (uint32_t)slot * (uint32_t)p.I * 4u + (uint32_t)part * (uint32_t)p.I * 2u
                                  : (uint32_t)(slot / p.k) * (uint32_t)p.H * 2u;
       uint8_t* dst = smem + row * (KC * 2);
@@ -446,12 +467,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
       }
     }
   };
-  const int nt = (n + 15) >> 4;
-  uint32_t xrow[P][NT], xswz[P][NT];  // this lane's staged rows (columns past the last one read it again)
+  uint32_t xrow[P][TT], xswz[P][TT];  // this lane's staged rows (columns past the last one read it again)
 #pragma unroll
   for (int q = 0; q < P; ++q)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < TT; ++t) {
       const uint32_t row = (uint32_t)(q * n + min(t * 16 + r16, n - 1));
       xrow[q][t] = row * (uint32_t)(KC * 2);
       xswz[q][t] = (row & 7u) << 4;
@@ -466,11 +486,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
   };
   load_scales();
 
-  v4f acc[2][NT];
+  v4f acc[2][TT];
 #pragma unroll
   for (int a = 0; a < 2; ++a)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[a][t] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < TT; ++t) acc[a][t] = v4f{0.f, 0.f, 0.f, 0.f};
 
   auto compute = [&](const Buf& b, int kk) {  // kk: first K of the round inside the staged piece
     b.sc.spread(slds[wave]);
@@ -482,15 +502,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
       for (int i = 0; i < W::kMfma; ++i) {
         const v4i w0 = widen_part<F>(b.w[u][0], s0, i), w1 = widen_part<F>(b.w[u][1], s1, i);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (NT > 1 && t >= nt) break;
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             const v4i x = *reinterpret_cast<const v4i*>(smem + xrow[q][t] + ((at + 16u * i) ^ xswz[q][t]));
             acc[0][t] = mfma_16x16x32_bf16(w0, x, acc[0][t]);
             acc[1][t] = mfma_16x16x32_bf16(w1, x, acc[1][t]);
           }
-        }
       }
     }
   };
@@ -500,27 +518,27 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) red[((wave * 2 + a) * NT + t) * 64 + lane] = acc[a][t];
+        for (int t = 0; t < TT; ++t) red[((wave * 2 + a) * TT + t) * 64 + lane] = acc[a][t];
       lds_barrier();
       if (ks == 0) {
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int w = 1; w < KS; ++w) acc[a][t] += red[(((wave + w) * 2 + a) * NT + t) * 64 + lane];
+            for (int w = 1; w < KS; ++w) acc[a][t] += red[(((wave + w) * 2 + a) * TT + t) * 64 + lane];
       }
       lds_barrier();
     }
     if (ks == 0 && row0 < out_rows) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      for (int t = 0; t < TT; ++t) {
         const int c = t * 16 + r16;
         if (c < n) {
           const v4f v0 = acc[0][t] * scale[0], v1 = acc[1][t] * scale[1];
           if constexpr (DOWN) {
-            const float w = colw[c];
-            float* dst = p.y + (int64_t)cols[c] * p.H + row0 + 4 * g;
+            const float w = colw[first + c];
+            float* dst = p.y + (int64_t)cols[first + c] * p.H + row0 + 4 * g;
             *reinterpret_cast<v4f*>(dst) = v0 * v4f{w, w, w, w};
             *reinterpret_cast<v4f*>(dst + 16) = v1 * v4f{w, w, w, w};
           } else {
@@ -532,7 +550,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
             lo[1] = h[1] - bf16_hi(h0);
             lo[2] = h[2] - bf16_lo(h1);
             lo[3] = h[3] - bf16_hi(h1);
-            uint16_t* dst = p.h + (int64_t)cols[c] * 2 * p.I + row0 + 4 * g;
+            uint16_t* dst = p.h + (int64_t)cols[first + c] * 2 * p.I + row0 + 4 * g;
             *reinterpret_cast<uint2*>(dst) = make_uint2(h0, h1);
             *reinterpret_cast<uint2*>(dst + p.I) = make_uint2(bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]));
           }
@@ -542,7 +560,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[a][t] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < TT; ++t) acc[a][t] = v4f{0.f, 0.f, 0.f, 0.f};
     row0 += tile_step;
   };
 
@@ -554,7 +572,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
       if (r) lds_barrier();  // every wave is done with the piece before
       stage(k0);
     }
-    if (r + 1 < total) load(next);
+    load(next, r + 1 < total);
     if (fresh) {
       wait_vmem_all();
       lds_barrier();
@@ -573,6 +591,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows(const FewArgs p, int 
     step(r, buf[0], buf[1]);
     if (r + 1 < total) step(r + 1, buf[1], buf[0]);
   }
+  lds_barrier();  // every wave is done with the staged rows
+  };
+  for (int first = 0; first < grp.n; first += 16 * NT) {
+    const int n = min(grp.n - first, 16 * NT);
+    if (NT == 1 || n <= 16)
+      pass(std::integral_constant<int, 1>{}, first, n);
+    else if (n <= 32)
+      pass(std::integral_constant<int, NT >= 2 ? 2 : 1>{}, first, n);
+    else
+      pass(std::integral_constant<int, NT>{}, first, n);
+  }
 }
 
 // out[t] = bf16(sum of the token's rows, in the order of its slots). A slot
@@ -590,15 +619,15 @@ __global__ __launch_bounds__(256) void few_combine(const FewArgs p) {
   const float* y = p.y + (int64_t)t * p.k * p.H + c;
   v4f s = v4f{0.f, 0.f, 0.f, 0.f};
   while (rows) {
-    v4f v[4];
+    v4f v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       v[i] = v4f{0.f, 0.f, 0.f, 0.f};
       if (rows) v[i] = *reinterpret_cast<const v4f*>(y + (int64_t)__builtin_ctzll(rows) * p.H);
       rows &= rows - 1;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s += v[i];
+    for (int i = 0; i < 8; ++i) s += v[i];
   }
   *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.H + c) = make_uint2(bf16x2_rne(s[0], s[1]), bf16x2_rne(s[2], s[3]));
 }
@@ -682,11 +711,14 @@ void launch_rows_ks(const FewArgs& a, int groups, hipStream_t stream) {
   const int K = DOWN ? a.I : a.H, P = DOWN ? 2 : 1;
   const int tiles = (DOWN ? a.H : a.I) / (DOWN ? 32 : 16), per_wg = kFewWaves / KS;
   const int sets = (tiles + per_wg - 1) / per_wg;  // sets of tiles a group has
-  const int rounds = 1;
+  // two workgroups a CU run together; more tiles than they have are taken in
+  // turn, with the next tile's weights on their way (down, 64 tokens of 64
+  // experts: 20.6 us against 24.9 us for twice the workgroups)
+  const int rounds = groups * sets / 512 > 1 ? (groups * sets / 512 < 4 ? groups * sets / 512 : 4) : 1;
   const int wgs = (sets + rounds - 1) / rounds;
   const int round_k = kRowsU<F, DOWN, NT, KS> * KS * WideFmt<F>::kStepK;
   const int k_all = (K + round_k - 1) / round_k * round_k;
-  const int rows = (int)(a.T < 64 ? a.T : 64);
+  const int rows = a.T < 16 * NT ? a.T : 16 * NT;
   const int64_t want = (int64_t)rows * k_all * 2 * P;
   const int lds = (int)(want < 65536 ? (want + 1023) / 1024 * 1024 : 65536);  // a load writes 1 KB
   hipLaunchKernelGGL((few_rows<F, DOWN, NT, KS>), dim3((unsigned)(groups * wgs)), dim3(64 * kFewWaves), lds, stream, a, wgs,

@@ -21,7 +21,16 @@
 namespace w8a8 {
 namespace {
 
-constexpr int kChunk = 32768;  // values a workgroup reads
+constexpr int kStride = 2048;    // values 256 threads read at once, 8 each
+constexpr int kMaxParts = 1024;  // chunks of a group: every quantising workgroup reads their maxima
+
+// Values per chunk: two loads a thread, more where a group has more than
+// kMaxParts such chunks.
+int64_t chunk_of(int64_t n) {
+  const int64_t c = (n + kMaxParts - 1) / kMaxParts;
+  return c <= 2 * kStride ? 2 * kStride : (c + kStride - 1) / kStride * kStride;
+}
+
 constexpr float kGscaleMin = 0x1p-96f;
 
 __device__ inline float group_scale(uint32_t amax_bits) {
@@ -38,28 +47,18 @@ __device__ inline float quotient(float x, float d, float r) {
   return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q0, d, x), r, q0), x);
 }
 
-__device__ inline uint32_t block_max(uint32_t v, int mask) {
-#pragma unroll
-  for (int m = 1; m <= mask; m <<= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)v, m, 64);
-    v = v > o ? v : o;
-  }
-  return v;
-}
-
 // part[g * parts + c] = the largest |x| (BF16 bits) of chunk c of group g
-__global__ __launch_bounds__(256) void nvfp4_amax(const uint16_t* __restrict__ x, int64_t n, int parts,
+__global__ __launch_bounds__(256) void nvfp4_amax(const uint16_t* __restrict__ x, int64_t n, int64_t chunk, int parts,
                                                   uint32_t* __restrict__ part) {
   __shared__ uint32_t red[4];
-  const int64_t grp = blockIdx.x / parts;
-  const int64_t c0 = (int64_t)(blockIdx.x % parts) * kChunk;
-  const int64_t len = min((int64_t)kChunk, n - c0);
+  const int64_t grp = blockIdx.x / parts, c0 = (int64_t)(blockIdx.x % parts) * chunk;
+  const int64_t len = (min(chunk, n - c0)) >> 3;  // 16-byte pieces
   const v4i* p = reinterpret_cast<const v4i*>(x + grp * n + c0);
   uint32_t m = 0;
-  for (int i = threadIdx.x; i < (int)(len >> 3); i += 256) {
-    const v4i t = p[i];
-    const uint32_t a = absmax8(make_uint4((uint32_t)t.x, (uint32_t)t.y, (uint32_t)t.z, (uint32_t)t.w));
-    m = m > a ? m : a;
+  for (int64_t i = threadIdx.x; i < len; i += 512) {
+    const v4i a = p[i], b = i + 256 < len ? p[i + 256] : v4i{0, 0, 0, 0};
+    m = max(m, absmax8(make_uint4((uint32_t)a.x, (uint32_t)a.y, (uint32_t)a.z, (uint32_t)a.w)));
+    m = max(m, absmax8(make_uint4((uint32_t)b.x, (uint32_t)b.y, (uint32_t)b.z, (uint32_t)b.w)));
   }
   m = wave_max_u32(m);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
@@ -67,17 +66,47 @@ __global__ __launch_bounds__(256) void nvfp4_amax(const uint16_t* __restrict__ x
   if (threadIdx.x == 0) part[blockIdx.x] = max(max(red[0], red[1]), max(red[2], red[3]));
 }
 
-// Two lanes hold a 16-value block, 8 values each.
-__global__ __launch_bounds__(256) void nvfp4_quant(const uint16_t* __restrict__ x, int64_t n, int parts,
+// 8 values; two lanes (an even one and the next) hold a 16-value block.
+__device__ inline void quant8_nv(v4i t, float g, uint32_t* q, uint8_t* s, int64_t i) {
+  const uint32_t w[4] = {(uint32_t)t.x, (uint32_t)t.y, (uint32_t)t.z, (uint32_t)t.w};
+  uint32_t m = absmax8(make_uint4(w[0], w[1], w[2], w[3]));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 1, 64));
+  const float f = fminf((__uint_as_float(m << 16) / 6.0f) / g, 448.0f);
+  const uint32_t code = e4m3x4(f, 0.f, 0.f, 0.f) & 0xFFu;
+  const float d = __builtin_amdgcn_cvt_f32_fp8((int)code, 0) * g;
+  const float r = d > 0.f ? 1.0f / d : 0.f;
+  uint32_t c = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float v0 = fminf(fmaxf(quotient(bf16_lo(w[k]), d, r), -6.0f), 6.0f);
+    const float v1 = fminf(fmaxf(quotient(bf16_hi(w[k]), d, r), -6.0f), 6.0f);
+    c |= (__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v0, v1, 1.0f, 0) & 0xFFu) << (8 * k);
+  }
+  q[i] = c;
+  if ((i & 1) == 0) s[i >> 1] = (uint8_t)code;
+}
+
+__global__ __launch_bounds__(256) void nvfp4_quant(const uint16_t* __restrict__ x, int64_t n, int64_t chunk, int parts,
                                                    const uint32_t* __restrict__ part, uint8_t* __restrict__ q,
                                                    uint8_t* __restrict__ s, float* __restrict__ gscale) {
   __shared__ uint32_t red[4];
   const int64_t b = (int64_t)gridDim.x - 1 - blockIdx.x;
-  const int64_t grp = b / parts, c0 = (b % parts) * kChunk;
+  const int64_t grp = b / parts, c0 = (b % parts) * chunk;
+  const int64_t base = grp * n + c0, len = (min(chunk, n - c0)) >> 3;
+  const v4i* p = reinterpret_cast<const v4i*>(x + base);
+  uint32_t* qc = reinterpret_cast<uint32_t*>(q + (base >> 1));
+  uint8_t* sc = s + (base >> 4);
+  // the first values come while the group's maximum is put together
+  int64_t i = threadIdx.x;
+  v4i v0 = i < len ? p[i] : v4i{0, 0, 0, 0}, v1 = i + 256 < len ? p[i + 256] : v4i{0, 0, 0, 0};
   float g;
   if (part) {
     uint32_t m = 0;
-    for (int i = threadIdx.x; i < parts; i += 256) m = max(m, part[grp * parts + i]);
+#pragma unroll
+    for (int k = 0; k < kMaxParts / 256; ++k) {
+      const int j = threadIdx.x + 256 * k;
+      m = max(m, j < parts ? part[grp * parts + j] : 0u);
+    }
     m = wave_max_u32(m);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
     __syncthreads();
@@ -86,31 +115,17 @@ __global__ __launch_bounds__(256) void nvfp4_quant(const uint16_t* __restrict__ 
   } else {
     g = gscale[grp];
   }
-  const int64_t len = min((int64_t)kChunk, n - c0);
-  const int64_t base = grp * n + c0;
-  const v4i* p = reinterpret_cast<const v4i*>(x + base);
-  for (int i = threadIdx.x; i < (int)(len >> 3); i += 256) {
-    const v4i t = p[i];
-    const uint32_t w[4] = {(uint32_t)t.x, (uint32_t)t.y, (uint32_t)t.z, (uint32_t)t.w};
-    const uint32_t m = block_max(absmax8(make_uint4(w[0], w[1], w[2], w[3])), 1);
-    const float f = fminf((__uint_as_float(m << 16) / 6.0f) / g, 448.0f);
-    const uint32_t code = e4m3x4(f, 0.f, 0.f, 0.f) & 0xFFu;
-    const float d = __builtin_amdgcn_cvt_f32_fp8((int)code, 0) * g;
-    const float r = d > 0.f ? 1.0f / d : 0.f;
-    uint32_t c = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float v0 = bf16_lo(w[k]), v1 = bf16_hi(w[k]);
-      v0 = fminf(fmaxf(quotient(v0, d, r), -6.0f), 6.0f);
-      v1 = fminf(fmaxf(quotient(v1, d, r), -6.0f), 6.0f);
-      c |= (__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v0, v1, 1.0f, 0) & 0xFFu) << (8 * k);
-    }
-    reinterpret_cast<uint32_t*>(q + (base >> 1))[i] = c;
-    if ((i & 1) == 0) s[(base >> 4) + (i >> 1)] = (uint8_t)code;
+  while (true) {
+    if (i < len) quant8_nv(v0, g, qc, sc, i);
+    if (i + 256 < len) quant8_nv(v1, g, qc, sc, i + 256);
+    i += 512;
+    if (i >= len) break;
+    v0 = p[i];
+    v1 = i + 256 < len ? p[i + 256] : v4i{0, 0, 0, 0};
   }
 }
 
-// 32 values (16 code bytes, two scales) per thread.
+// 8 values (4 code bytes) per thread.
 __global__ __launch_bounds__(256) void nvfp4_dequant(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
                                                      const float* __restrict__ gscale, int64_t n, int64_t total,
                                                      uint16_t* __restrict__ y) {
@@ -129,18 +144,19 @@ __global__ __launch_bounds__(256) void nvfp4_dequant(const uint8_t* __restrict__
 
 }  // namespace
 
-int64_t nvfp4_parts(int64_t n) { return (n + kChunk - 1) / kChunk; }
+int64_t nvfp4_parts(int64_t n) { return (n + chunk_of(n) - 1) / chunk_of(n); }
 
 hipError_t launch_nvfp4_quantize(const uint16_t* x, int64_t G, int64_t n, uint8_t* q, uint8_t* s, float* gscale,
                                  bool given, uint32_t* part, hipStream_t stream) {
+  const int64_t chunk = chunk_of(n);
   const int parts = (int)nvfp4_parts(n);
   const dim3 grid((unsigned)(G * parts));
   if (!given) {
-    hipLaunchKernelGGL(nvfp4_amax, grid, dim3(256), 0, stream, x, n, parts, part);
+    hipLaunchKernelGGL(nvfp4_amax, grid, dim3(256), 0, stream, x, n, chunk, parts, part);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(nvfp4_quant, grid, dim3(256), 0, stream, x, n, parts, given ? nullptr : part, q, s, gscale);
+  hipLaunchKernelGGL(nvfp4_quant, grid, dim3(256), 0, stream, x, n, chunk, parts, given ? nullptr : part, q, s, gscale);
   return hipGetLastError();
 }
 

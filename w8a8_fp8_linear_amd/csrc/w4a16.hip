@@ -81,6 +81,71 @@ __global__ __launch_bounds__(256) void w4a16_skinny(const W4Args p) {
   }
 }
 
+// Some rows, too few for the tiled kernel to fill the GPU: 64 x 64 results a
+// workgroup, K split over its 4 waves, operands straight from global memory
+// (the activations from L2); a wave's K fits a few rounds of loads.
+template <int F>
+__global__ __launch_bounds__(256) void w4a16_mid(const W4Args p) {
+  using W = WideFmt<F>;
+  constexpr int TN = 4, TM = 4;
+  __shared__ v4f red[2][TN * TM][64];
+  __shared__ __attribute__((aligned(16))) uint8_t slds[4][BlockScales<F, TN, 1>::kLds];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles_n = (p.N + 63) / 64;
+  const int n0 = blockIdx.x % tiles_n * 64, m0 = blockIdx.x / tiles_n * 64;
+  const int64_t rb = W::row_bytes(p.K), rs = W::row_scales(p.K);
+  const auto rW = make_rsrc(p.w + n0 * rb, (p.N - n0) * rb);
+  uint32_t skew;
+  const auto rS = scale_rsrc(p.s + n0 * rs, (p.N - n0) * rs, &skew);
+  const auto rX = make_rsrc(p.x + (int64_t)m0 * p.K, (int64_t)(p.M - m0) * p.K * 2);
+  const int r16 = lane & 15, g = lane >> 4;
+  uint32_t wrow[TN], srow[TN], xrow[TM];
+#pragma unroll
+  for (int a = 0; a < TN; ++a) {
+    wrow[a] = (uint32_t)((a * 16 + r16) * rb);
+    srow[a] = skew + (uint32_t)((a * 16 + r16) * rs);
+  }
+#pragma unroll
+  for (int t = 0; t < TM; ++t) xrow[t] = (uint32_t)(t * 16 + r16) * (uint32_t)p.K * 2u;
+  const float gs = w4_scale<F>(p);
+  v4f acc[TN][TM];
+#pragma unroll
+  for (int a = 0; a < TN; ++a)
+#pragma unroll
+    for (int t = 0; t < TM; ++t) acc[a][t] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int steps = ((p.K + W::kStepK - 1) / W::kStepK + 3) / 4;  // of a wave's quarter of K
+  stream_dot<F, TN, TM, 1>(rW, rS, wrow, srow, rX, xrow, p.K, wave * steps * W::kStepK, steps, slds[wave], acc);
+  // waves 2, 3 add to 0, 1, then wave 1 to 0: each in half of the tiles at the end
+  if (wave >= 2) {
+#pragma unroll
+    for (int i = 0; i < TN * TM; ++i) red[wave - 2][i][lane] = acc[i / TM][i % TM];
+  }
+  __syncthreads();
+  if (wave < 2) {
+#pragma unroll
+    for (int i = 0; i < TN * TM; ++i) acc[i / TM][i % TM] += red[wave][i][lane];
+  }
+  __syncthreads();
+  if (wave < 2) {  // wave 0 keeps the first half of the tiles, wave 1 the second
+#pragma unroll
+    for (int i = 0; i < TN * TM / 2; ++i) {
+      red[wave][i][lane] = wave == 0 ? acc[(i + TN * TM / 2) / TM][i % TM] : acc[i / TM][i % TM];
+    }
+  }
+  __syncthreads();
+  if (wave >= 2) return;
+#pragma unroll
+  for (int i = 0; i < TN * TM / 2; ++i) {
+    const int a = wave == 0 ? i / TM : (i + TN * TM / 2) / TM, t = i % TM;
+    const v4f v = (wave == 0 ? acc[i / TM][t] : acc[(i + TN * TM / 2) / TM][t]) + red[1 - wave][i][lane];
+    const int n = n0 + a * 16 + 4 * g, m = m0 + t * 16 + r16;
+    if (n < p.N && m < p.M)
+      *reinterpret_cast<uint2*>(p.y + (int64_t)m * p.N + n) =
+          make_uint2(bf16x2_rne(v[0] * gs, v[1] * gs), bf16x2_rne(v[2] * gs, v[3] * gs));
+  }
+}
+
 template <int BM, int BN, int WGM, int WGN>
 struct Tiled4 {
   static constexpr int kThreads = 64 * WGM * WGN;
@@ -255,6 +320,11 @@ hipError_t launch_w4(const W4Args& a, hipStream_t stream) {
   }
   if (a.M <= 32) {
     hipLaunchKernelGGL((w4a16_skinny<F, 2, 2>), skinny_grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+  }
+  const int64_t big = (int64_t)((a.M + 255) / 256) * ((a.N + 191) / 192);
+  if (big < 128) {
+    hipLaunchKernelGGL(w4a16_mid<F>, dim3((unsigned)((a.M + 63) / 64 * ((a.N + 63) / 64))), dim3(256), 0, stream, a);
     return hipGetLastError();
   }
   return launch_tiled<F, 256, 192, 2, 4>(a, stream);
