@@ -702,9 +702,9 @@ int moe_router(const uint16_t* x_bf16, const uint16_t* w_router, const float* bi
   if (workspace_bytes < w8a8::router_workspace_bytes(T, E)) return W8A8_ERR_WORKSPACE;
   const int d = check_device();
   if (d != W8A8_OK) return d;
-  return launch_status(w8a8::launch_router(x_bf16, w_router, bias, topk_ids, topk_w, T, H, E, topk,
-                                           score == MOE_SCORE_SIGMOID, renormalize != 0, route_scale, workspace,
-                                           stream));
+  const w8a8::Router r{x_bf16,   w_router, bias, topk_ids, topk_w, score == MOE_SCORE_SIGMOID, renormalize != 0,
+                       route_scale};
+  return launch_status(w8a8::launch_router(r, T, H, E, topk, workspace, stream));
 }
 
 size_t moe_few_tokens_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
@@ -728,8 +728,8 @@ int moe_few_tokens(int format, const uint16_t* x_bf16, const int32_t* topk_ids, 
   if (workspace_bytes < w8a8::few_workspace_bytes(T, H, I, topk)) return W8A8_ERR_WORKSPACE;
   const int d = check_device();
   if (d != W8A8_OK) return d;
-  return launch_status(w8a8::launch_few(format, x_bf16, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale,
-                                        w2_gscale, out_bf16, T, H, I, E, topk, workspace, stream));
+  const w8a8::Few f{format, x_bf16, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale, w2_gscale, out_bf16};
+  return launch_status(w8a8::launch_few(f, nullptr, T, H, I, E, topk, workspace, stream));
 }
 
 int moe_few_tokens_layer(int format, const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int score,
@@ -750,12 +750,10 @@ int moe_few_tokens_layer(int format, const uint16_t* x_bf16, const uint16_t* w_r
   if (workspace_bytes < w8a8::few_layer_workspace_bytes(T, H, I, E, topk)) return W8A8_ERR_WORKSPACE;
   const int d = check_device();
   if (d != W8A8_OK) return d;
-  const hipError_t e = w8a8::launch_router(x_bf16, w_router, bias, topk_ids, topk_w, T, H, E, topk,
-                                           score == MOE_SCORE_SIGMOID, renormalize != 0, route_scale,
-                                           w8a8::few_layer_logits(workspace, T, I, topk), stream);
-  if (e != hipSuccess) return launch_status(e);
-  return launch_status(w8a8::launch_few(format, x_bf16, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale,
-                                        w2_gscale, out_bf16, T, H, I, E, topk, workspace, stream));
+  const w8a8::Router r{x_bf16,   w_router, bias, topk_ids, topk_w, score == MOE_SCORE_SIGMOID, renormalize != 0,
+                       route_scale};
+  const w8a8::Few f{format, x_bf16, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale, w2_gscale, out_bf16};
+  return launch_status(w8a8::launch_few(f, &r, T, H, I, E, topk, workspace, stream));
 }
 
 }  // extern "C"

@@ -306,9 +306,9 @@ struct Group {
 // cols[c] and (if asked) colw[c]: the first slot and the summed router weight
 // of the group's c-th token, written by wave 0; the caller's barrier follows.
 template <bool WEIGHTS>
-__device__ inline Group find_group(const FewArgs& p, int group, int* cols, float* colw) {
+__device__ inline Group find_group(const FewArgs& p, const int32_t* ids, int group, int* cols, float* colw) {
   const int lane = threadIdx.x & 63;
-  const int e = p.by_slot ? p.ids[group] : group;
+  const int e = p.by_slot ? ids[group] : group;
   int slot = -1;
   float w = 0.f;
   for (int j0 = 0; j0 < p.k; j0 += 8) {
@@ -318,7 +318,7 @@ __device__ inline Group find_group(const FewArgs& p, int group, int* cols, float
     for (int j = 0; j < 8; ++j) {
       const bool in = lane < p.T && j0 + j < p.k;
       const int s = lane * p.k + j0 + j;
-      id[j] = in ? p.ids[s] : -1;
+      id[j] = in ? ids[s] : -1;
       tw[j] = WEIGHTS && in ? p.tw[s] : 0.f;
     }
 #pragma unroll
@@ -370,9 +370,13 @@ __device__ inline v4f row_scales(const void* s, const float* g, int64_t row, int
 template <int F, bool DOWN, int NT, int KS>
 constexpr int kRowsU = F == kFmtFp8 || (KS == 1 && !DOWN) ? 4 : 2;  // 2: a round fits 64 tokens' h, or a short split K
 
-template <int F, bool DOWN, int NT, int KS>
-__global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(2, 4))) void few_rows(const FewArgs p, int wgs_per_group, int rounds,
-                                                           int lds_bytes) {
+//
+// ROUTE (at most kFewWaves tokens, few workgroups): the choice is made here
+// from the logits, a wave per token, by every workgroup for itself, and
+// written out by the first. That is 1 us of latency more, and a launch less.
+template <int F, bool DOWN, int NT, int KS, bool ROUTE>
+__global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(2, 4)))
+void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int rounds, int lds_bytes) {
   using W = WideFmt<F>;
   constexpr int U = kRowsU<F, DOWN, NT, KS>;
   using S = BlockScales<F, 2, U>;
@@ -392,7 +396,28 @@ __global__ __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(
   const int out_rows = DOWN ? p.H : p.I;
   const int set_rows = DOWN ? 16 : p.I;           // distance of the two row sets
   const int64_t rb = W::row_bytes(K), rs = W::row_scales(K);
-  const Group grp = find_group<DOWN>(p, blockIdx.x / wgs_per_group, cols, colw);
+  __shared__ int32_t chosen[ROUTE ? kFewWaves * 64 : 1];
+  const int32_t* ids = p.ids;
+  if constexpr (ROUTE) {
+    if (wave < p.T) {
+      int id;
+      float tw;
+      if (route.E <= 64)
+        select_token<1>(route, wave, lane, &id, &tw);
+      else
+        select_token<4>(route, wave, lane, &id, &tw);
+      if (lane < p.k) {
+        chosen[wave * p.k + lane] = id;
+        if (blockIdx.x == 0) {
+          route.ids[wave * p.k + lane] = id;
+          route.tw[wave * p.k + lane] = tw;
+        }
+      }
+    }
+    lds_barrier();
+    ids = chosen;
+  }
+  const Group grp = find_group<DOWN>(p, ids, blockIdx.x / wgs_per_group, cols, colw);
   if (grp.e < 0) return;
   const int e = grp.e;
   const auto rW = make_rsrc((DOWN ? p.w2 : p.w13) + (int64_t)e * rows * rb, (int64_t)rows * rb);
@@ -706,8 +731,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_small(const FewArgs p) {
 // into one operand.
 bool few_small(int64_t T, int64_t topk) { return T <= 8 && T * topk <= 64; }
 
-template <int F, bool DOWN, int NT, int KS>
-void launch_rows_ks(const FewArgs& a, int groups, hipStream_t stream) {
+template <int F, bool DOWN, int NT, int KS, bool ROUTE = false>
+void launch_rows_ks(const FewArgs& a, int groups, hipStream_t stream, const RouterArgs& route = {}) {
   const int K = DOWN ? a.I : a.H, P = DOWN ? 2 : 1;
   const int tiles = (DOWN ? a.H : a.I) / (DOWN ? 32 : 16), per_wg = kFewWaves / KS;
   const int sets = (tiles + per_wg - 1) / per_wg;  // sets of tiles a group has
@@ -721,19 +746,35 @@ void launch_rows_ks(const FewArgs& a, int groups, hipStream_t stream) {
   const int rows = a.T < 16 * NT ? a.T : 16 * NT;
   const int64_t want = (int64_t)rows * k_all * 2 * P;
   const int lds = (int)(want < 65536 ? (want + 1023) / 1024 * 1024 : 65536);  // a load writes 1 KB
-  hipLaunchKernelGGL((few_rows<F, DOWN, NT, KS>), dim3((unsigned)(groups * wgs)), dim3(64 * kFewWaves), lds, stream, a, wgs,
-                     rounds, lds);
+  hipLaunchKernelGGL((few_rows<F, DOWN, NT, KS, ROUTE>), dim3((unsigned)(groups * wgs)), dim3(64 * kFewWaves), lds, stream,
+                     a, route, wgs, rounds, lds);
+}
+
+int few_groups(const FewArgs& a) { return a.by_slot ? a.T * a.k : a.E; }
+
+constexpr int kSplit4 = 768, kSplit2 = 1536;  // tiles up to which 4 or 2 waves share one
+
+// Whether the gate/up launch makes the choice: every workgroup does, so they
+// must be few.
+bool few_routes(const FewArgs& a) {
+  return a.T <= kFewWaves && a.E <= 256 && few_groups(a) * (a.I / 16) <= kSplit4;
 }
 
 template <int F, bool DOWN>
-hipError_t launch_rows(const FewArgs& a, hipStream_t stream) {
-  const int groups = a.by_slot ? a.T * a.k : a.E;
+hipError_t launch_rows(const FewArgs& a, const RouterArgs* route, hipStream_t stream) {
+  const int groups = few_groups(a);
   const int tiles = groups * ((DOWN ? a.H : a.I) / (DOWN ? 32 : 16));
+  if constexpr (!DOWN) {
+    if (route) {
+      launch_rows_ks<F, DOWN, 1, 4, true>(a, groups, stream, *route);
+      return hipGetLastError();
+    }
+  }
   if (a.T > 16)
     launch_rows_ks<F, DOWN, 4, 1>(a, groups, stream);
-  else if (tiles <= 768)
+  else if (tiles <= kSplit4)
     launch_rows_ks<F, DOWN, 1, 4>(a, groups, stream);
-  else if (tiles <= 1536)
+  else if (tiles <= kSplit2)
     launch_rows_ks<F, DOWN, 1, 2>(a, groups, stream);
   else
     launch_rows_ks<F, DOWN, 1, 1>(a, groups, stream);
@@ -741,8 +782,8 @@ hipError_t launch_rows(const FewArgs& a, hipStream_t stream) {
 }
 
 template <int F>
-hipError_t launch_few_fmt(const FewArgs& a, hipStream_t stream) {
-  hipError_t e = launch_rows<F, false>(a, stream);
+hipError_t launch_few_fmt(const FewArgs& a, const RouterArgs* route, hipStream_t stream) {
+  hipError_t e = launch_rows<F, false>(a, route, stream);
   if (e != hipSuccess) return e;
   if (few_small(a.T, a.k)) {
     if (a.T <= 4)
@@ -751,7 +792,7 @@ hipError_t launch_few_fmt(const FewArgs& a, hipStream_t stream) {
       hipLaunchKernelGGL((few_down_small<F, 8, 16>), dim3(a.H / 8), dim3(64 * 16), 0, stream, a);
     return hipGetLastError();
   }
-  e = launch_rows<F, true>(a, stream);
+  e = launch_rows<F, true>(a, nullptr, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(few_combine, dim3((a.H + 1023) / 1024, a.T), dim3(256), 0, stream, a);
   return hipGetLastError();
@@ -763,27 +804,33 @@ size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 size_t router_workspace_bytes(int64_t T, int64_t E) { return (size_t)(T * E * 8); }
 
-hipError_t launch_router(const uint16_t* x, const uint16_t* wr, const float* bias, int32_t* ids, float* tw, int64_t T,
-                         int64_t H, int64_t E, int64_t topk, int sigmoid, int renorm, float scale, void* ws,
-                         hipStream_t stream) {
-  const RouterArgs a{x, wr, bias, static_cast<double*>(ws), ids, tw, (int)T, (int)H, (int)E, (int)topk, sigmoid, renorm,
-                     scale};
-  const unsigned e4 = (unsigned)((E + 3) / 4);
-  if (T <= 2)
-    hipLaunchKernelGGL(router_logits_few<1>, dim3(e4, (unsigned)T), dim3(256), 0, stream, a);
-  else if (T <= 64)
-    hipLaunchKernelGGL(router_logits_few<4>, dim3(e4, (unsigned)((T + 3) / 4)), dim3(256), 0, stream, a);
+static hipError_t launch_logits(const RouterArgs& a, hipStream_t stream) {
+  const unsigned e4 = (unsigned)((a.E + 3) / 4);
+  if (a.T <= 2)
+    hipLaunchKernelGGL(router_logits_few<1>, dim3(e4, (unsigned)a.T), dim3(256), 0, stream, a);
+  else if (a.T <= 64)
+    hipLaunchKernelGGL(router_logits_few<4>, dim3(e4, (unsigned)((a.T + 3) / 4)), dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL(router_logits_mfma, dim3((unsigned)((T + 15) / 16 * ((E + 15) / 16))), dim3(512), 0, stream, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (E <= 64)
-    hipLaunchKernelGGL(router_select<1>, dim3((unsigned)T), dim3(64), 0, stream, a);
-  else if (E <= 256)
-    hipLaunchKernelGGL(router_select<4>, dim3((unsigned)T), dim3(64), 0, stream, a);
-  else
-    hipLaunchKernelGGL(router_select<16>, dim3((unsigned)T), dim3(64), 0, stream, a);
+    hipLaunchKernelGGL(router_logits_mfma, dim3((unsigned)((a.T + 15) / 16 * ((a.E + 15) / 16))), dim3(512), 0, stream, a);
   return hipGetLastError();
+}
+
+static hipError_t launch_router(const RouterArgs& a, hipStream_t stream) {
+  const hipError_t e = launch_logits(a, stream);
+  if (e != hipSuccess) return e;
+  if (a.E <= 64)
+    hipLaunchKernelGGL(router_select<1>, dim3((unsigned)a.T), dim3(64), 0, stream, a);
+  else if (a.E <= 256)
+    hipLaunchKernelGGL(router_select<4>, dim3((unsigned)a.T), dim3(64), 0, stream, a);
+  else
+    hipLaunchKernelGGL(router_select<16>, dim3((unsigned)a.T), dim3(64), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_router(const Router& r, int64_t T, int64_t H, int64_t E, int64_t topk, void* ws, hipStream_t stream) {
+  return launch_router(RouterArgs{r.x, r.wr, r.bias, static_cast<double*>(ws), r.ids, r.tw, (int)T, (int)H, (int)E,
+                                  (int)topk, r.sigmoid, r.renorm, r.scale},
+                       stream);
 }
 
 // h, then the y rows; the router's logits, which are read before y is
@@ -799,21 +846,24 @@ size_t few_layer_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int
   return few_h_bytes(T, I, topk) + (y > l ? y : l);
 }
 
-void* few_layer_logits(void* ws, int64_t T, int64_t I, int64_t topk) {
-  return static_cast<uint8_t*>(ws) + few_h_bytes(T, I, topk);
-}
-
-hipError_t launch_few(int format, const uint16_t* x, const int32_t* ids, const float* tw, const uint8_t* w13,
-                      const void* s13, const float* g13, const uint8_t* w2, const void* s2, const float* g2,
-                      uint16_t* out, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, void* ws,
+hipError_t launch_few(const Few& f, const Router* r, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, void* ws,
                       hipStream_t stream) {
   uint8_t* b = static_cast<uint8_t*>(ws);
-  const FewArgs a{x,  ids, tw, w13, s13, g13, w2, s2, g2, reinterpret_cast<uint16_t*>(b),
-                  reinterpret_cast<float*>(b + few_h_bytes(T, I, topk)), out, (int)T, (int)H, (int)I, (int)E, (int)topk,
-                  T * topk <= E ? 1 : 0};
-  if (format == kFmtFp8) return launch_few_fmt<kFmtFp8>(a, stream);
-  if (format == kFmtMxfp4) return launch_few_fmt<kFmtMxfp4>(a, stream);
-  return launch_few_fmt<kFmtNvfp4>(a, stream);
+  uint8_t* rest = b + few_h_bytes(T, I, topk);
+  const FewArgs a{f.x, f.ids, f.tw, f.w13, f.s13, f.g13, f.w2, f.s2, f.g2, reinterpret_cast<uint16_t*>(b),
+                  reinterpret_cast<float*>(rest), f.out, (int)T, (int)H, (int)I, (int)E, (int)topk, T * topk <= E ? 1 : 0};
+  RouterArgs route{};
+  const bool fused = r && few_routes(a);
+  if (r) {
+    route = RouterArgs{r->x, r->wr, r->bias, reinterpret_cast<double*>(rest), r->ids, r->tw, (int)T, (int)H, (int)E,
+                       (int)topk, r->sigmoid, r->renorm, r->scale};
+    const hipError_t e = fused ? launch_logits(route, stream) : launch_router(route, stream);
+    if (e != hipSuccess) return e;
+  }
+  const RouterArgs* choose = fused ? &route : nullptr;
+  if (f.format == kFmtFp8) return launch_few_fmt<kFmtFp8>(a, choose, stream);
+  if (f.format == kFmtMxfp4) return launch_few_fmt<kFmtMxfp4>(a, choose, stream);
+  return launch_few_fmt<kFmtNvfp4>(a, choose, stream);
 }
 
 }  // namespace w8a8

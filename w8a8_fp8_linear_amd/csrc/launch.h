@@ -142,16 +142,35 @@ hipError_t launch_w4a16_gemm(int format, const uint16_t* x, const uint8_t* w, co
 
 // The few-token routed-expert layer (few.hip).
 constexpr int64_t kFewMaxTokens = 64, kFewMaxSlots = 1024;
-hipError_t launch_router(const uint16_t* x, const uint16_t* wr, const float* bias, int32_t* ids, float* tw, int64_t T,
-                         int64_t H, int64_t E, int64_t topk, int sigmoid, int renorm, float scale, void* ws,
-                         hipStream_t stream);
+struct Router {
+  const uint16_t *x, *wr;  // [T, H], [E, H]
+  const float* bias;       // [E] or NULL
+  int32_t* ids;            // [T, topk]
+  float* tw;               // [T, topk]
+  int sigmoid, renorm;
+  float scale;
+};
 size_t router_workspace_bytes(int64_t T, int64_t E);
+hipError_t launch_router(const Router& r, int64_t T, int64_t H, int64_t E, int64_t topk, void* ws, hipStream_t stream);
+
+struct Few {
+  int format;
+  const uint16_t* x;
+  const int32_t* ids;
+  const float* tw;
+  const uint8_t* w13;
+  const void* s13;
+  const float* g13;
+  const uint8_t* w2;
+  const void* s2;
+  const float* g2;
+  uint16_t* out;
+};
 size_t few_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t topk);
 size_t few_layer_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
-void* few_layer_logits(void* ws, int64_t T, int64_t I, int64_t topk);  // the router's part of the layer's workspace
-hipError_t launch_few(int format, const uint16_t* x, const int32_t* ids, const float* tw, const uint8_t* w13,
-                      const void* s13, const float* g13, const uint8_t* w2, const void* s2, const float* g2,
-                      uint16_t* out, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, void* ws,
+// r (may be NULL): the router that makes f's ids and tw first; the workspace
+// is then few_layer_workspace_bytes, else few_workspace_bytes.
+hipError_t launch_few(const Few& f, const Router* r, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, void* ws,
                       hipStream_t stream);
 
 }  // namespace w8a8
