@@ -44,15 +44,18 @@ namespace {
 
 typedef double v4d __attribute__((ext_vector_type(4)));
 
-__device__ inline double shfl_xor_f64(double v, int m) { return __shfl_xor(v, m, 64); }
+// Wave-wide reductions by DPP: row shifts by 1, 2, 4, 8, then the row
+// broadcasts leave the result in lane 63. A DPP move takes a few cycles where
+// a shuffle through LDS takes a hundred.
+template <int CTRL, int ROWS = 0xF>
+__device__ inline uint32_t dpp_u32(uint32_t old, uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, ROWS, 0xF, false);
+}
 
-// v of the lane that a DPP control names, `v` itself where there is none.
-template <int CTRL>
-__device__ inline double dpp_f64(double v) {
-  const uint2 u = __builtin_bit_cast(uint2, v);
-  return __builtin_bit_cast(
-      double, make_uint2((uint32_t)__builtin_amdgcn_update_dpp((int)u.x, (int)u.x, CTRL, 0xF, 0xF, false),
-                         (uint32_t)__builtin_amdgcn_update_dpp((int)u.y, (int)u.y, CTRL, 0xF, 0xF, false)));
+template <int CTRL, int ROWS = 0xF>
+__device__ inline double dpp_f64(double old, double v) {
+  const uint2 u = __builtin_bit_cast(uint2, v), o = __builtin_bit_cast(uint2, old);
+  return __builtin_bit_cast(double, make_uint2(dpp_u32<CTRL, ROWS>(o.x, u.x), dpp_u32<CTRL, ROWS>(o.y, u.y)));
 }
 
 __device__ inline double readlane_f64(double v, int lane) {
@@ -61,16 +64,33 @@ __device__ inline double readlane_f64(double v, int lane) {
                                                (uint32_t)__builtin_amdgcn_readlane((int)u.y, lane)));
 }
 
-// The wave's largest value, in every lane: row shifts by 1, 2, 4, 8, then the
-// row broadcasts leave it in lane 63. DPP moves take a few cycles where a
-// shuffle through LDS takes a hundred.
-__device__ inline double wave_max_f64(double v) {
-  v = fmax(v, dpp_f64<0x111>(v));
-  v = fmax(v, dpp_f64<0x112>(v));
-  v = fmax(v, dpp_f64<0x114>(v));
-  v = fmax(v, dpp_f64<0x118>(v));
-  v = fmax(v, dpp_f64<0x142>(v));
-  v = fmax(v, dpp_f64<0x143>(v));
+__device__ inline uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp_u32<0x111>(0, v));
+  v = max(v, dpp_u32<0x112>(0, v));
+  v = max(v, dpp_u32<0x114>(0, v));
+  v = max(v, dpp_u32<0x118>(0, v));
+  v = max(v, dpp_u32<0x142>(0, v));
+  v = max(v, dpp_u32<0x143>(0, v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+__device__ inline double wave_max(double v) {
+  v = fmax(v, dpp_f64<0x111>(v, v));
+  v = fmax(v, dpp_f64<0x112>(v, v));
+  v = fmax(v, dpp_f64<0x114>(v, v));
+  v = fmax(v, dpp_f64<0x118>(v, v));
+  v = fmax(v, dpp_f64<0x142>(v, v));
+  v = fmax(v, dpp_f64<0x143>(v, v));
+  return readlane_f64(v, 63);
+}
+
+__device__ inline double wave_sum(double v) {  // the same order of additions whatever the values
+  v += dpp_f64<0x111>(0.0, v);
+  v += dpp_f64<0x112>(0.0, v);
+  v += dpp_f64<0x114>(0.0, v);
+  v += dpp_f64<0x118>(0.0, v);
+  v += dpp_f64<0x142, 0xA>(0.0, v);
+  v += dpp_f64<0x143, 0xC>(0.0, v);
   return readlane_f64(v, 63);
 }
 
@@ -132,9 +152,8 @@ __global__ __launch_bounds__(256) void router_logits_few(const RouterArgs p) {
   }
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) acc[t] += shfl_xor_f64(acc[t], m);
-    if (lane == 0 && t0 + t < p.T) p.logits[(int64_t)(t0 + t) * p.E + e] = acc[t];
+    const double s = wave_sum(acc[t]);
+    if (lane == 0 && t0 + t < p.T) p.logits[(int64_t)(t0 + t) * p.E + e] = s;
   }
 }
 
@@ -213,16 +232,14 @@ __device__ inline void select_token(const RouterArgs& p, int t, int lane, int* i
     double mx = val[0];
 #pragma unroll
     for (int i = 1; i < NV; ++i) mx = fmax(mx, val[i]);
-    mx = wave_max_f64(mx);
+    mx = wave_max(mx);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       val[i] = exp(val[i] - mx);
       sum += val[i];
     }
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) sum += shfl_xor_f64(sum, m);
-    inv = 1.0 / sum;
+    inv = 1.0 / wave_sum(sum);
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -243,8 +260,18 @@ __device__ inline void select_token(const RouterArgs& p, int t, int lane, int* i
       v = up ? val[i] : v;
       at = up ? i : at;
     }
-    const double mx = wave_max_f64(best);
-    const int from = __builtin_ctzll(__ballot(best == mx));
+    // the largest, by the bits of the float64 made to order as unsigned
+    // numbers: the upper halves decide unless they are equal
+    const uint2 bits = __builtin_bit_cast(uint2, best);
+    const uint32_t neg = (uint32_t)((int)bits.y >> 31);
+    const uint32_t hi = bits.y ^ (neg | 0x80000000u), lo = bits.x ^ neg;
+    const bool top = hi == wave_max(hi);
+    uint64_t who = __ballot(top);
+    if (who & (who - 1)) {
+      const uint32_t low = wave_max(top ? lo : 0u);  // by all lanes
+      who = __ballot(top && lo == low);
+    }
+    const int from = __builtin_ctzll(who);
     const double score = readlane_f64(v, from) * inv;
     const int e = from * NV + __builtin_amdgcn_readlane(at, from);
     all += score;
@@ -342,6 +369,7 @@ __device__ inline Group find_group(const FewArgs& p, const int32_t* ids, int gro
 }
 
 constexpr int kFewWaves = 4;
+constexpr int kFewMaxE = 1024;
 
 template <int F>
 __device__ inline v4f row_scales(const void* s, const float* g, int64_t row, int e) {
@@ -668,7 +696,8 @@ template <int F, int R, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void few_down_small(const FewArgs p) {
   using W = WideFmt<F>;
   constexpr int C = 16 / R;   // places of K
-  constexpr int U = F == kFmtFp8 ? 4 : 2;
+  constexpr int U = F == kFmtFp8 ? R / 2 : R / 4;  // the steps of one place of 512 inputs
+  __shared__ uint32_t first[kFewMaxE];             // the first slot of every expert
   __shared__ v4f red[WAVES][64];
   __shared__ __attribute__((aligned(16))) uint8_t slds[WAVES][BlockScales<F, 1, U>::kLds];
   const int lane = threadIdx.x & 63;
@@ -678,19 +707,23 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_small(const FewArgs p) {
   const int slots = p.T * p.k;
   const int id = lane < slots ? p.ids[lane] : -1;
   const float tw = lane < slots ? p.tw[lane] : 0.f;
+  const bool valid = id >= 0 && id < p.E;
+  for (int i = threadIdx.x; i < p.E; i += 64 * WAVES) first[i] = 64;
+  __syncthreads();
+  if (wave == 0 && valid) atomicMin(&first[id], (uint32_t)lane);
+  __syncthreads();
+  uint64_t leaders = __ballot(valid && first[id] == (uint32_t)lane);
   const int tok = r16 % R;
   const int64_t rb = W::row_bytes(p.I), rs = W::row_scales(p.I);
   const int steps = ((p.I + W::kStepK - 1) / W::kStepK + C - 1) / C;  // of one place
   const auto rX = make_rsrc(p.h, (int64_t)slots * p.I * 4);
   const uint32_t wrow[1] = {(uint32_t)((r16 % R) * rb)};
   v4f y = v4f{0.f, 0.f, 0.f, 0.f};
-  int turn = wave;  // experts until this wave's next one
-  for (int s = 0; s < slots; ++s) {
-    const int e = __builtin_amdgcn_readlane(id, s);
-    if (e < 0 || e >= p.E) continue;
+  for (int i = 0; i < wave; ++i) leaders &= leaders - 1;
+  while (leaders) {
+    const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(leaders));
     const uint64_t same = __ballot(id == e);
-    if (__builtin_ctzll(same) != s || turn-- != 0) continue;
-    turn = WAVES - 1;
+    for (int i = 0; i < WAVES; ++i) leaders &= leaders - 1;
     const auto rW = make_rsrc(p.w2 + ((int64_t)e * p.H + row0) * rb, R * rb);
     uint32_t skew;
     const auto rS = scale_rsrc(static_cast<const uint8_t*>(p.s2) + ((int64_t)e * p.H + row0) * rs, R * rs, &skew);
