@@ -127,6 +127,19 @@ def test_gemm_parity(fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", [(2051, 3280, 96), (2050, 3088, 1056), (1800, 4112, 2112), (2048, 3264, 32)])
+def test_gemm_parity_many_tiles(fmt, M, N, K):
+    """Sizes of the tiled kernel: ragged edges, one step, scales that begin inside a dword and run over chunks."""
+    print(f"[{fmt}_gemm] {M}x{N}x{K}", flush=True)
+    rng = np.random.default_rng(M + N + K)
+    x = synth.activations(rng, M, K, n_outlier=2)
+    q = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    w = (q, rng.integers(120, 130, (N, K // 32), dtype=np.uint8)) if fmt == "mxfp4" else \
+        (q, rng.integers(0, 0x70, (N, K // 16), dtype=np.uint8), np.float32([0.01]))
+    assert _bound_ok(fmt, x, w, _gemm(fmt, x, w)) == 0
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("M", [3, 40])
 def test_gemm_every_code_and_scale(fmt, M):
     """A one-hot activation row reads one weight: every code, under every block scale (E8M0 2^-126 .. 2^124, all

@@ -332,11 +332,16 @@ struct Group {
 // expert. Lane t < T looks through its token's ids, eight loads at a time.
 // cols[c] and (if asked) colw[c]: the first slot and the summed router weight
 // of the group's c-th token, written by wave 0; the caller's barrier follows.
-template <bool WEIGHTS>
-__device__ inline Group find_group(const FewArgs& p, const int32_t* ids, int group, int* cols, float* colw) {
+// `early` is called with the expert once it is known, when the ids are on their
+// way: the first weights' loads go out there. (A copy that turns out not to be
+// its expert's first has then read what the first one reads too; an expert
+// without tokens, one round of loads for nothing.)
+template <bool WEIGHTS, class EARLY>
+__device__ inline Group find_group(const FewArgs& p, const int32_t* ids, int group, int* cols, float* colw,
+                                   const EARLY& early) {
   const int lane = threadIdx.x & 63;
-  const int e = p.by_slot ? ids[group] : group;
-  int slot = -1;
+  const int own = p.by_slot ? ids[group] : 0;
+  int slot = -1, e = -1;
   float w = 0.f;
   for (int j0 = 0; j0 < p.k; j0 += 8) {
     int id[8];
@@ -348,6 +353,11 @@ __device__ inline Group find_group(const FewArgs& p, const int32_t* ids, int gro
       id[j] = in ? ids[s] : -1;
       tw[j] = WEIGHTS && in ? p.tw[s] : 0.f;
     }
+    if (j0 == 0) {
+      e = __builtin_amdgcn_readfirstlane(p.by_slot ? own : group);
+      if (e < 0 || e >= p.E) return {-1, 0};
+      early(e);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (id[j] == e) {
@@ -356,7 +366,6 @@ __device__ inline Group find_group(const FewArgs& p, const int32_t* ids, int gro
       }
     }
   }
-  if (e < 0 || e >= p.E) return {-1, 0};  // a group's own id may be none; then nothing above matters
   const uint64_t mask = __ballot(slot >= 0);
   if (mask == 0) return {-1, 0};
   if (p.by_slot && __builtin_amdgcn_readlane(slot, __builtin_ctzll(mask)) != group) return {-1, 0};
@@ -445,19 +454,48 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
     lds_barrier();
     ids = chosen;
   }
-  const Group grp = find_group<DOWN>(p, ids, blockIdx.x / wgs_per_group, cols, colw);
-  if (grp.e < 0) return;
-  const int e = grp.e;
-  const auto rW = make_rsrc((DOWN ? p.w2 : p.w13) + (int64_t)e * rows * rb, (int64_t)rows * rb);
-  uint32_t skew;
-  const auto rS = scale_rsrc(static_cast<const uint8_t*>(DOWN ? p.s2 : p.s13) + (int64_t)e * rows * rs, (int64_t)rows * rs,
-                             &skew);
-  const auto rX = DOWN ? make_rsrc(p.h, (int64_t)p.T * p.k * p.I * 4) : make_rsrc(p.x, (int64_t)p.T * p.H * 2);
-
   // this wave's tiles: row0, row0 + tile_step, ...
   const int tile_step = tile_rows * (kFewWaves / KS);
   const int row_first = (blockIdx.x % wgs_per_group) * rounds * tile_step + (wave / KS) * tile_rows;
   const int k_wave = ks * U * W::kStepK;          // this wave's part of a round
+
+  // The loads of one round of the expert's weights. They are issued whether or
+  // not there is one (then out of range, which reads nothing): behind a branch
+  // the compiler would have to wait for all of them before the first use of
+  // the round before.
+  struct Buf {
+    v4i w[U][2];
+    S sc;
+  } buf[2];
+  __amdgpu_buffer_rsrc_t rW, rS;
+  uint32_t skew;
+  auto load = [&](Buf& b, int k, int row_at, bool there) {
+    const int row = row_at + r16;
+    const bool in = there && row_at < out_rows;
+    const uint32_t w0 = (uint32_t)(row * rb), w1 = (uint32_t)((row + set_rows) * rb);
+    const int kw = k + k_wave;
+    b.sc.load(rS, [&](int a) {
+      return in && kw < K ? skew + (uint32_t)((row + a * set_rows) * rs) + (uint32_t)(kw / W::kBlock) : kOutOfRange;
+    });
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int ku = kw + u * W::kStepK + W::kLaneK * g;
+      const bool live = in && ku < K;
+      b.w[u][0] = buffer_load16(rW, live ? w0 + (uint32_t)W::row_bytes(ku) : kOutOfRange);
+      b.w[u][1] = buffer_load16(rW, live ? w1 + (uint32_t)W::row_bytes(ku) : kOutOfRange);
+    }
+  };
+  const Group grp = find_group<DOWN>(p, ids, blockIdx.x / wgs_per_group, cols, colw, [&](int e) {
+    rW = make_rsrc((DOWN ? p.w2 : p.w13) + (int64_t)e * rows * rb, (int64_t)rows * rb);
+    rS = scale_rsrc(static_cast<const uint8_t*>(DOWN ? p.s2 : p.s13) + (int64_t)e * rows * rs, (int64_t)rows * rs, &skew);
+    if (!DOWN) {
+      load(buf[0], 0, row_first, true);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  });
+  if (grp.e < 0) return;
+  const int e = grp.e;
+  const auto rX = DOWN ? make_rsrc(p.h, (int64_t)p.T * p.k * p.I * 4) : make_rsrc(p.x, (int64_t)p.T * p.H * 2);
   lds_barrier();  // cols, colw
 
   // The pass over the weights for columns first .. first + n - 1 in TT column
@@ -473,36 +511,21 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
   const int cpr = KC >> 3;                        // 16-byte chunks of a staged row
 
   int row0 = row_first;
-  struct Buf {
-    v4i w[U][2];
-    S sc;
-  } buf[2];
-  // The loads of one round. They are issued whether or not there is one (then
-  // out of range, which reads nothing): behind a branch the compiler would
-  // have to wait for all of them before the first use of the round before.
-  int load_k = 0, load_row = row0;
-  auto load = [&](Buf& b, bool there) {
-    const int row = load_row + r16;
-    const bool in = there && load_row < out_rows;
-    const uint32_t w0 = (uint32_t)(row * rb), w1 = (uint32_t)((row + set_rows) * rb);
-    const int kw = load_k + k_wave;
-    b.sc.load(rS, [&](int a) {
-      return in && kw < K ? skew + (uint32_t)((row + a * set_rows) * rs) + (uint32_t)(kw / W::kBlock) : kOutOfRange;
-    });
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = kw + u * W::kStepK + W::kLaneK * g;
-      const bool live = in && k < K;
-      b.w[u][0] = buffer_load16(rW, live ? w0 + (uint32_t)W::row_bytes(k) : kOutOfRange);
-      b.w[u][1] = buffer_load16(rW, live ? w1 + (uint32_t)W::row_bytes(k) : kOutOfRange);
-    }
+  int load_k = 0, load_row = row0;  // the next round to load
+  auto load_next = [&](Buf& b, bool there) {
+    load(b, load_k, load_row, there);
     load_k += kRound;
     if (load_k >= k_pad) {
       load_k = 0;
       load_row += tile_step;
     }
   };
-  load(buf[0], true);
+  if (!DOWN && first == 0) {  // loaded while the group was found
+    load_k = kRound < k_pad ? kRound : 0;
+    load_row += load_k ? 0 : tile_step;
+  } else {
+    load_next(buf[0], true);
+  }
 
   // Rows go to LDS in 1 KB pieces of 64 chunks; the 16-byte chunks of row r
   // are stored with their index XORed with r % 8, so that the 8 rows that 8
@@ -625,7 +648,7 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
       if (r) lds_barrier();  // every wave is done with the piece before
       stage(k0);
     }
-    load(next, r + 1 < total);
+    load_next(next, r + 1 < total);
     if (fresh) {
       wait_vmem_all();
       lds_barrier();
@@ -772,7 +795,8 @@ void launch_rows_ks(const FewArgs& a, int groups, hipStream_t stream, const Rout
   // two workgroups a CU run together; more tiles than they have are taken in
   // turn, with the next tile's weights on their way (down, 64 tokens of 64
   // experts: 20.6 us against 24.9 us for twice the workgroups)
-  const int rounds = groups * sets / 512 > 1 ? (groups * sets / 512 < 4 ? groups * sets / 512 : 4) : 1;
+  const int full = a.by_slot ? 1 : groups * sets / 512;  // by copies, many workgroups find nothing to do
+  const int rounds = full < 1 ? 1 : full < 4 ? full : 4;
   const int wgs = (sets + rounds - 1) / rounds;
   const int round_k = kRowsU<F, DOWN, NT, KS> * KS * WideFmt<F>::kStepK;
   const int k_all = (K + round_k - 1) / round_k * round_k;
@@ -785,7 +809,13 @@ void launch_rows_ks(const FewArgs& a, int groups, hipStream_t stream, const Rout
 
 int few_groups(const FewArgs& a) { return a.by_slot ? a.T * a.k : a.E; }
 
-constexpr int kSplit4 = 768, kSplit2 = 1536;  // tiles up to which 4 or 2 waves share one
+// Tiles up to which 4 or 2 waves share one. A 4-bit tile has more arithmetic
+// to its bytes, and more waves to spread it over pay off longer (8 tokens of 64
+// experts, 2048 tiles, gate/up: nvfp4 17.9 us with two waves a tile against
+// 19.7 us with one, fp8 28.7 against 26.0 us).
+constexpr int kSplit4 = 768;
+template <int F>
+constexpr int kSplit2 = F == kFmtFp8 ? 1536 : 2048;
 
 // Whether the gate/up launch makes the choice: every workgroup does, so they
 // must be few.
@@ -807,7 +837,7 @@ hipError_t launch_rows(const FewArgs& a, const RouterArgs* route, hipStream_t st
     launch_rows_ks<F, DOWN, 4, 1>(a, groups, stream);
   else if (tiles <= kSplit4)
     launch_rows_ks<F, DOWN, 1, 4>(a, groups, stream);
-  else if (tiles <= kSplit2)
+  else if (tiles <= kSplit2<F>)
     launch_rows_ks<F, DOWN, 1, 2>(a, groups, stream);
   else
     launch_rows_ks<F, DOWN, 1, 1>(a, groups, stream);
@@ -819,10 +849,13 @@ hipError_t launch_few_fmt(const FewArgs& a, const RouterArgs* route, hipStream_t
   hipError_t e = launch_rows<F, false>(a, route, stream);
   if (e != hipSuccess) return e;
   if (few_small(a.T, a.k)) {
-    if (a.T <= 4)
+    // Every workgroup reads all of h: 8 columns each halve that against 4. One
+    // token's h is small, and its few experts need the workgroups (1 of 128
+    // experts, fp8: 4.4 us against 4.8 us; 2 of 64: 7.4 against 8.7 us).
+    if (a.T == 1)
       hipLaunchKernelGGL((few_down_small<F, 4, 8>), dim3(a.H / 4), dim3(64 * 8), 0, stream, a);
     else
-      hipLaunchKernelGGL((few_down_small<F, 8, 16>), dim3(a.H / 8), dim3(64 * 16), 0, stream, a);
+      hipLaunchKernelGGL((few_down_small<F, 8, 8>), dim3(a.H / 8), dim3(64 * 8), 0, stream, a);
     return hipGetLastError();
   }
   e = launch_rows<F, true>(a, nullptr, stream);
