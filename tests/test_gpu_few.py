@@ -51,7 +51,8 @@ def _check_router(x, wr, k, **kw):
 
 
 @pytest.mark.parametrize("T,H,E,k", [(1, 1024, 192, 4), (3, 8, 1, 1), (5, 24, 2, 2), (64, 520, 65, 8), (7, 2056, 8, 8),
-                                     (2, 512, 1024, 64), (257, 96, 130, 6), (300, 1024, 64, 8), (263, 40, 1000, 33)])
+                                     (2, 512, 1024, 64), (257, 96, 130, 6), (300, 1024, 64, 8), (263, 40, 1000, 33),
+                                     (2051, 264, 50, 5)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_router(T, H, E, k, score):
     print(f"[router] T={T} H={H} E={E} k={k} {score}", flush=True)
