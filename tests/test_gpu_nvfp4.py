@@ -42,7 +42,7 @@ def _quant_matches(x_bits, gscale=None):
 
 
 @pytest.mark.parametrize("G,R,K", [(1, 1, 16), (1, 3, 48), (5, 7, 32), (3, 64, 1040), (2, 33, 4096), (1, 1, 65552),
-                                   (9, 130, 272)])
+                                   (9, 130, 272), (2, 2050, 4112), (130, 8, 16400)])
 def test_quantize_bit_exact(G, R, K):
     print(f"[nvfp4] {G}x{R}x{K}", flush=True)
     rng = np.random.default_rng(G * R + K)
@@ -127,7 +127,9 @@ def test_gemm_parity(fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
-@pytest.mark.parametrize("M,N,K", [(2051, 3280, 96), (2050, 3088, 1056), (1800, 4112, 2112), (2048, 3264, 32)])
+@pytest.mark.parametrize("M,N,K", [(2051, 3280, 96), (2050, 3088, 1056), (1800, 4112, 2112), (2048, 3264, 32),
+                                   (900, 2000, 1504), (257, 4096, 32), (1030, 2032, 1248), (4100, 2064, 1120),
+                                   (2050, 6160, 96)])
 def test_gemm_parity_many_tiles(fmt, M, N, K):
     """Sizes of the tiled kernel: ragged edges, one step, scales that begin inside a dword and run over chunks."""
     print(f"[{fmt}_gemm] {M}x{N}x{K}", flush=True)
@@ -225,3 +227,40 @@ def test_refusals():
         buf = torch.zeros(4 * 64 + 4, dtype=torch.bfloat16, device="cuda")
         w8.mxfp4_gemm(buf[4:].view(4, 64), q, s32)
     assert e.value.status == 3
+
+
+@pytest.mark.parametrize("M", [1, 40, 700])
+def test_quantise_and_multiply_in_a_graph(M):
+    """Weights quantised, multiplied and read back in one captured stream: every replay gives the eager bits."""
+    print(f"[graph] M {M}", flush=True)
+    N, K = 1552, 608
+    rng = np.random.default_rng(M)
+    w = to_dev_bf16(synth.f32_to_bf16_bits(rng.standard_normal((N, K), dtype=np.float32)))
+    xs = [to_dev_bf16(synth.f32_to_bf16_bits(rng.standard_normal((M, K), dtype=np.float32))) for _ in range(3)]
+
+    def chain(x):
+        q, s, g = w8.nvfp4_quantize(w)
+        mq, ms = w8.mxfp4_quantize(w)
+        return w8.nvfp4_gemm(x, q, s, g), w8.mxfp4_gemm(x, mq, ms), w8.nvfp4_dequantize(q, s, g)
+
+    want = [[bf16_bits(y) for y in chain(x)] for x in xs]
+    torch.cuda.synchronize()
+    x = xs[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        chain(x)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain(x)
+    for i in (0, 1, 2, 1):
+        x.copy_(xs[i])
+        for o in out:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for o, r in zip(out, want[i]):
+            assert np.array_equal(bf16_bits(o), r)
+        chain(xs[2])
+        torch.cuda.synchronize()

@@ -26,6 +26,8 @@
 namespace w8a8 {
 namespace {
 
+constexpr int kCUs = 256;
+
 typedef int v2i __attribute__((ext_vector_type(2)));
 
 struct W4Args {
@@ -123,30 +125,23 @@ __global__ __launch_bounds__(256) void w4a16_mid(const W4Args p) {
     for (int t = 0; t < TM; ++t) acc[a][t] = v4f{0.f, 0.f, 0.f, 0.f};
   const int steps = ((p.K + W::kStepK - 1) / W::kStepK + 3) / 4;  // of a wave's quarter of K
   stream_dot<F, TN, TM, 1>(rW, rS, wrow, srow, rX, xrow, p.K, wave * steps * W::kStepK, steps, slds[wave], acc);
-  // waves 2, 3 add to 0, 1, then wave 1 to 0: each in half of the tiles at the end
-  if (wave >= 2) {
+  // two waves leave their sums, the other two add theirs, then every wave
+  // finishes the tiles of one column tile
 #pragma unroll
-    for (int i = 0; i < TN * TM; ++i) red[wave - 2][i][lane] = acc[i / TM][i % TM];
-  }
-  __syncthreads();
-  if (wave < 2) {
+  for (int turn = 0; turn < 2; ++turn) {
+    if (wave >> 1 == turn) {
 #pragma unroll
-    for (int i = 0; i < TN * TM; ++i) acc[i / TM][i % TM] += red[wave][i][lane];
-  }
-  __syncthreads();
-  if (wave < 2) {  // wave 0 keeps the first half of the tiles, wave 1 the second
-#pragma unroll
-    for (int i = 0; i < TN * TM / 2; ++i) {
-      red[wave][i][lane] = wave == 0 ? acc[(i + TN * TM / 2) / TM][i % TM] : acc[i / TM][i % TM];
+      for (int i = 0; i < TN * TM; ++i) {
+        v4f& r = red[wave & 1][i][lane];
+        r = turn ? r + acc[i / TM][i % TM] : acc[i / TM][i % TM];
+      }
     }
+    __syncthreads();
   }
-  __syncthreads();
-  if (wave >= 2) return;
 #pragma unroll
-  for (int i = 0; i < TN * TM / 2; ++i) {
-    const int a = wave == 0 ? i / TM : (i + TN * TM / 2) / TM, t = i % TM;
-    const v4f v = (wave == 0 ? acc[i / TM][t] : acc[(i + TN * TM / 2) / TM][t]) + red[1 - wave][i][lane];
-    const int n = n0 + a * 16 + 4 * g, m = m0 + t * 16 + r16;
+  for (int t = 0; t < TM; ++t) {
+    const v4f v = red[0][wave * TM + t][lane] + red[1][wave * TM + t][lane];
+    const int n = n0 + wave * 16 + 4 * g, m = m0 + t * 16 + r16;
     if (n < p.N && m < p.M)
       *reinterpret_cast<uint2*>(p.y + (int64_t)m * p.N + n) =
           make_uint2(bf16x2_rne(v[0] * gs, v[1] * gs), bf16x2_rne(v[2] * gs, v[3] * gs));
@@ -173,8 +168,8 @@ struct Tiled4 {
   static_assert(WM % 16 == 0 && WN % 16 == 0, "wave tile must be a multiple of 16");
 };
 
-template <int F, int BM, int BN, int WGM, int WGN>
-__global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(1, 2)))
+template <int F, int BM, int BN, int WGM, int WGN, int PER_EU>
+__global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(1, PER_EU)))
 void w4a16_tiled(const W4Args p, int tiles_m, int tiles_n) {
   using C = Tiled4<BM, BN, WGM, WGN>;
   using W = WideFmt<F>;
@@ -312,7 +307,7 @@ void w4a16_tiled(const W4Args p, int tiles_m, int tiles_n) {
 #pragma unroll
     for (int i = 0; i < C::SN * C::SM; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, (kWiden + 7) / 8, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, (kWiden + C::SM - 1) / C::SM, 0);
     }
   };
   uint8_t *st = smem, *st1 = smem + C::kStage, *st2 = smem + 2 * C::kStage;
@@ -379,10 +374,10 @@ void w4a16_tiled(const W4Args p, int tiles_m, int tiles_n) {
   }
 }
 
-template <int F, int BM, int BN, int WGM, int WGN>
+template <int F, int BM, int BN, int WGM, int WGN, int PER_EU>
 hipError_t launch_tiled(const W4Args& a, hipStream_t stream) {
   const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN;
-  hipLaunchKernelGGL((w4a16_tiled<F, BM, BN, WGM, WGN>), dim3(tiles_m * tiles_n), dim3(64 * WGM * WGN), 0, stream, a,
+  hipLaunchKernelGGL((w4a16_tiled<F, BM, BN, WGM, WGN, PER_EU>), dim3(tiles_m * tiles_n), dim3(64 * WGM * WGN), 0, stream, a,
                      tiles_m, tiles_n);
   return hipGetLastError();
 }
@@ -408,12 +403,23 @@ hipError_t launch_w4(const W4Args& a, hipStream_t stream) {
       hipLaunchKernelGGL((w4a16_skinny<F, 1, 2, 2, 4>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
   }
-  const int64_t big = (int64_t)((a.M + 255) / 256) * ((a.N + 191) / 192);
-  if (big < 128) {
-    hipLaunchKernelGGL(w4a16_mid<F>, dim3((unsigned)((a.M + 63) / 64 * ((a.N + 63) / 64))), dim3(256), 0, stream, a);
+  // The tile grows with the work, so that each kernel starts with at most one
+  // workgroup a CU: 64 x 64 with K split (64 x 6144 x 2048: 14.8 us against
+  // 20.8 us in 64 x 128 tiles), 64 x 128 (256 x 6144 x 2048: 21.6 us against
+  // 25.2 us in 64 x 64 and 27.0 us in 128 x 128), 128 x 128 (512 x 6144 x 2048:
+  // 27.3 us against 35.3 us in 64 x 64 and 49.8 us in 256 x 192).
+  const auto tiles = [&](int bm, int bn) { return (int64_t)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  if (tiles(64, 64) <= kCUs) {
+    hipLaunchKernelGGL(w4a16_mid<F>, dim3((unsigned)tiles(64, 64)), dim3(256), 0, stream, a);
     return hipGetLastError();
   }
-  return launch_tiled<F, 256, 192, 2, 4>(a, stream);
+  if (tiles(64, 128) <= kCUs) return launch_tiled<F, 64, 128, 1, 4, 2>(a, stream);
+  // From there on by rounds of 256 tiles: one of 128 x 128 costs two fifths of
+  // one of 256 x 192 (K 2048: 20 us and 49 us; measured 60 against 53 us at 1536 x
+  // 6144, 89 against 103 us at 2304, 124 against 103 us at 4096).
+  const auto rounds = [](int64_t n) { return (n + kCUs - 1) / kCUs; };
+  if (2 * rounds(tiles(128, 128)) < 5 * rounds(tiles(256, 192))) return launch_tiled<F, 128, 128, 2, 4, 4>(a, stream);
+  return launch_tiled<F, 256, 192, 2, 4, 2>(a, stream);
 }
 
 }  // namespace
