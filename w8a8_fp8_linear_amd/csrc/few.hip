@@ -498,10 +498,11 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
   const auto rX = DOWN ? make_rsrc(p.h, (int64_t)p.T * p.k * p.I * 4) : make_rsrc(p.x, (int64_t)p.T * p.H * 2);
   lds_barrier();  // cols, colw
 
-  // The pass over the weights for columns first .. first + n - 1 in TT column
-  // tiles: a copy of the code for each TT, so that none has a branch on the
-  // number of tiles inside.
-  auto pass = [&](auto tt, const int first, const int n) {
+  // The pass over the weights for the group's n tokens in TT column tiles: a
+  // copy of the code for each TT, so that none has a branch on the number of
+  // tiles inside.
+  const int n = grp.n;
+  auto pass = [&](auto tt) {
   constexpr int TT = decltype(tt)::value;
   // KC: whole rounds, all of K if the n rows fit
   const int k_all = (K + kRound - 1) / kRound * kRound;
@@ -520,7 +521,7 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
       load_row += tile_step;
     }
   };
-  if (!DOWN && first == 0) {  // loaded while the group was found
+  if (!DOWN) {  // loaded while the group was found
     load_k = kRound < k_pad ? kRound : 0;
     load_row += load_k ? 0 : tile_step;
   } else {
@@ -533,7 +534,7 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
   auto stage = [&](int k0) {
     for (int row = wave; row < P * n; row += kFewWaves) {
       const int part = row >= n ? 1 : 0;
-      const int slot = cols[first + row - part * n];
+      const int slot = cols[row - part * n];
       const uint32_t base = DOWN ? (uint32_t)slot * (uint32_t)p.I * 4u + (uint32_t)part * (uint32_t)p.I * 2u
                                  : (uint32_t)(slot / p.k) * (uint32_t)p.H * 2u;
       uint8_t* dst = smem + row * (KC * 2);
@@ -613,8 +614,8 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
         if (c < n) {
           const v4f v0 = acc[0][t] * scale[0], v1 = acc[1][t] * scale[1];
           if constexpr (DOWN) {
-            const float w = colw[first + c];
-            float* dst = p.y + (int64_t)cols[first + c] * p.H + row0 + 4 * g;
+            const float w = colw[c];
+            float* dst = p.y + (int64_t)cols[c] * p.H + row0 + 4 * g;
             *reinterpret_cast<v4f*>(dst) = v0 * v4f{w, w, w, w};
             *reinterpret_cast<v4f*>(dst + 16) = v1 * v4f{w, w, w, w};
           } else {
@@ -626,7 +627,7 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
             lo[1] = h[1] - bf16_hi(h0);
             lo[2] = h[2] - bf16_lo(h1);
             lo[3] = h[3] - bf16_hi(h1);
-            uint16_t* dst = p.h + (int64_t)cols[first + c] * 2 * p.I + row0 + 4 * g;
+            uint16_t* dst = p.h + (int64_t)cols[c] * 2 * p.I + row0 + 4 * g;
             *reinterpret_cast<uint2*>(dst) = make_uint2(h0, h1);
             *reinterpret_cast<uint2*>(dst + p.I) = make_uint2(bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]));
           }
@@ -667,17 +668,14 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
     step(r, buf[0], buf[1]);
     if (r + 1 < total) step(r + 1, buf[1], buf[0]);
   }
-  lds_barrier();  // every wave is done with the staged rows
   };
-  for (int first = 0; first < grp.n; first += 16 * NT) {
-    const int n = min(grp.n - first, 16 * NT);
-    if (NT == 1 || n <= 16)
-      pass(std::integral_constant<int, 1>{}, first, n);
-    else if (n <= 32)
-      pass(std::integral_constant<int, NT >= 2 ? 2 : 1>{}, first, n);
-    else
-      pass(std::integral_constant<int, NT>{}, first, n);
-  }
+  // n <= 16 NT
+  if (NT == 1 || n <= 16)
+    pass(std::integral_constant<int, 1>{});
+  else if (n <= 32)
+    pass(std::integral_constant<int, NT == 1 ? 1 : 2>{});
+  else
+    pass(std::integral_constant<int, NT>{});
 }
 
 // out[t] = bf16(sum of the token's rows, in the order of its slots). A slot

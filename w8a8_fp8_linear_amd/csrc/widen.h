@@ -85,41 +85,6 @@ struct WideFmt {
   __host__ __device__ static constexpr int64_t row_scales(int64_t K) { return F == kFmtFp8 ? 0 : K / kBlock; }
 };
 
-// A lane's 16 code bytes hold consecutive inputs: lane g of a row's four has
-// inputs kLaneK g .. of the step. This exchanges them among the four lanes so
-// that MFMA i's operand is inputs 32 i + 8 g .. of the step instead: the
-// activations it needs are then 64 consecutive bytes per row for the four
-// lanes of one load, where they would be 16 bytes every 32 or 64 (measured on
-// an mxfp4 layer of 24 x 6160 x 2048: see w4a16_skinny). FP4: a transposition
-// of the 4 x 4 dwords, lane bits against register bits; FP8: the halves'
-// bit against both lane bits in turn.
-template <int F>
-__device__ inline v4i in_order(v4i w) {
-  uint32_t d[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
-  auto swap32 = [&](int a, int b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(d[a], d[b], false, false);
-    d[a] = r[0];
-    d[b] = r[1];
-  };
-  auto swap16 = [&](int a, int b) {
-    const auto r = __builtin_amdgcn_permlane16_swap(d[a], d[b], false, false);
-    d[a] = r[0];
-    d[b] = r[1];
-  };
-  if constexpr (F == kFmtFp8) {
-    swap16(0, 2);
-    swap16(1, 3);
-    swap32(0, 2);
-    swap32(1, 3);
-  } else {
-    swap32(0, 2);
-    swap32(1, 3);
-    swap16(0, 1);
-    swap16(2, 3);
-  }
-  return v4i{(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
-}
-
 // LDS written and read by the lanes of one wave: the hardware keeps a wave's
 // LDS accesses in order, this keeps the compiler to it.
 __device__ inline void wave_lds_order() {
@@ -185,42 +150,7 @@ struct BlockScales {
     }
     return 0;
   }
-
-  // The scales of step u, set a for operands in order (in_order): part i's is
-  // scale(s, i).
-  static __device__ inline uint2 get_in_order(const uint8_t* lds, int u, int a) {
-    if constexpr (kAny) {
-      const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
-      const int at = u * kStepBytes;
-      const uint8_t* s = lds + (r16 + 16 * (a * kPieces + at / 16)) * 16 + at % 16;
-      if constexpr (F == kFmtMxfp4) return make_uint2(*reinterpret_cast<const uint32_t*>(s), 0u);
-      const uint2 v = *reinterpret_cast<const uint2*>(s);  // part i: byte 2 i + g / 2
-      const uint32_t sh = (uint32_t)(g >> 1) * 8u;
-      return make_uint2(v.x >> sh, v.y >> sh);
-    }
-    return make_uint2(0u, 0u);
-  }
 };
-
-// The MFMA operand i of a lane's codes in order.
-template <int F>
-__device__ inline v4i widen_in_order(v4i w, uint2 sc, int i) {
-  const uint32_t d[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
-  if constexpr (F == kFmtFp8) {
-    return widen8(d[2 * i], d[2 * i + 1]);
-  } else if constexpr (F == kFmtMxfp4) {
-    return widen8_mx(d[i], __uint_as_float(i == 0   ? (sc.x & 0xFFu) << 23
-                                           : i == 1 ? (sc.x & 0xFF00u) << 15
-                                           : i == 2 ? (sc.x & 0xFF0000u) << 7
-                                                    : (sc.x >> 1) & 0x7F800000u));
-  } else {
-    const float s = i == 0   ? __builtin_amdgcn_cvt_f32_fp8((int)sc.x, 0)
-                    : i == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)sc.x, 2)
-                    : i == 2 ? __builtin_amdgcn_cvt_f32_fp8((int)sc.y, 0)
-                             : __builtin_amdgcn_cvt_f32_fp8((int)sc.y, 2);
-    return widen8_nv(d[i], s);
-  }
-}
 
 // A resource over the scale rows of one matrix that begins at any byte:
 // `skew` is where the matrix begins in it.
@@ -266,32 +196,27 @@ __device__ inline void stream_dot(__amdgpu_buffer_rsrc_t rW, __amdgpu_buffer_rsr
     for (int u = 0; u < U; ++u) {
       const int ku = k0 + u * W::kStepK;
       const int kw = ku + W::kLaneK * g;  // K is a multiple of kLaneK: a lane is all in or all out
-      const bool step = kt + u < steps, live = step && kw < K;
+      const bool live = kt + u < steps && kw < K;
 #pragma unroll
       for (int a = 0; a < NR; ++a) w[u][a] = buffer_load16(rW, live ? wrow[a] + (uint32_t)W::row_bytes(kw) : kOutOfRange);
 #pragma unroll
-      for (int i = 0; i < W::kMfma; ++i) {
-        const int kx = ku + 32 * i + 8 * g;
-        const bool in = step && kx < K;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) x[u][t][i] = buffer_load16(rX, in ? xrow[t] + 2u * (uint32_t)kx : kOutOfRange);
-      }
+        for (int i = 0; i < W::kMfma; ++i)
+          x[u][t][i] = buffer_load16(rX, live ? xrow[t] + 2u * (uint32_t)kw + 16u * i : kOutOfRange);
     }
     __builtin_amdgcn_sched_barrier(0);
     sc.spread(lds);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      uint2 s[NR];
+      uint32_t s[NR];
 #pragma unroll
-      for (int a = 0; a < NR; ++a) {
-        w[u][a] = in_order<F>(w[u][a]);
-        s[a] = S::get_in_order(lds, u, a);
-      }
+      for (int a = 0; a < NR; ++a) s[a] = S::get(lds, u, a);
 #pragma unroll
       for (int i = 0; i < W::kMfma; ++i)
 #pragma unroll
         for (int a = 0; a < NR; ++a) {
-          const v4i b = widen_in_order<F>(w[u][a], s[a], i);
+          const v4i b = widen_part<F>(w[u][a], s[a], i);
 #pragma unroll
           for (int t = 0; t < NT; ++t) acc[a][t] = mfma_16x16x32_bf16(b, x[u][t][i], acc[a][t]);
         }
