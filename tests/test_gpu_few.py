@@ -130,7 +130,10 @@ def _check_few(rng, fmt, x, ids, tw, ex, E, **kw):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,H,I,E,k", [(1, 32, 32, 1, 1), (1, 1024, 512, 16, 4), (2, 160, 96, 5, 3), (5, 288, 32, 40, 4),
                                        (16, 96, 160, 7, 2), (17, 256, 128, 6, 3), (32, 64, 64, 33, 8), (33, 128, 96, 4, 2),
-                                       (64, 160, 64, 3, 3), (64, 96, 224, 200, 16)])
+                                       (64, 160, 64, 3, 3), (64, 96, 224, 200, 16),
+                                       # 8 tokens or fewer with more than 64 copies; 9 to 16 ids a token; inputs of several staged pieces
+                                       (8, 64, 96, 40, 16), (5, 96, 64, 300, 33), (4, 128, 64, 600, 12),
+                                       (64, 4128, 32, 2, 2), (24, 64, 2080, 3, 2), (16, 4128, 64, 2, 2)])
 def test_few_tokens(fmt, T, H, I, E, k):
     print(f"[few] {fmt} T={T} H={H} I={I} E={E} k={k}", flush=True)
     rng = np.random.default_rng(T * 31 + H + I + E)
@@ -186,6 +189,18 @@ def test_layer_is_router_then_experts(fmt, T):
     bias = torch.linspace(-0.1, 0.1, 24, device="cuda")
     out, ids, w = w8.moe_few_tokens_layer(x, wr, w13, w2, 4, bias=bias, score="sigmoid", route_scale=1.5)
     i2, t2 = w8.moe_router(x, wr, 4, bias=bias, score="sigmoid", route_scale=1.5)
+    o2 = w8.moe_few_tokens(x, i2, t2, w13, w2)
+    assert torch.equal(ids, i2) and torch.equal(w, t2) and torch.equal(out, o2)
+
+
+@pytest.mark.parametrize("T,E,k,score", [(4, 300, 6, "softmax"), (4, 256, 3, "sigmoid"), (3, 65, 12, "softmax"),
+                                         (2, 9, 9, "sigmoid"), (4, 3, 2, "softmax"), (5, 64, 4, "softmax")])
+def test_layer_choice_in_the_first_projection(T, E, k, score):
+    """Up to four tokens the layer may choose inside its first projection: the same choice, weights and output bits as
+    the separate calls, by copies and by experts, below and above the sizes at which it does."""
+    x, wr, w13, w2 = _layer_state("mxfp4", T, 160, 64, E, seed=E)
+    out, ids, w = w8.moe_few_tokens_layer(x, wr, w13, w2, k, score=score, renormalize=k % 2 == 0)
+    i2, t2 = w8.moe_router(x, wr, k, score=score, renormalize=k % 2 == 0)
     o2 = w8.moe_few_tokens(x, i2, t2, w13, w2)
     assert torch.equal(ids, i2) and torch.equal(w, t2) and torch.equal(out, o2)
 
@@ -289,3 +304,20 @@ def test_refusals():
     with pytest.raises(w8.W8A8Error) as e:
         w8.moe_few_tokens(x, ids, w, w13, w2, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 5
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_layer_inputs_that_begin_inside_a_larger_tensor(fmt):
+    """Views into larger tensors (a batch's rows, an expert range of a stack), the router's outputs given, canaries
+    behind the output and in the rows that no token has."""
+    T, H, I, E, k = 3, 96, 64, 12, 2
+    x, wr, w13, w2 = _layer_state(fmt, T + 5, H, I, E + 4, seed=2)
+    sub13, sub2 = (tuple(t[4:] for t in w) for w in (w13, w2))
+    out = torch.full((T + 5, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    ids = torch.full((T + 5, k), 77, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 5, k), 7.0, device="cuda")
+    w8.moe_few_tokens_layer(x[2:2 + T], wr[4:], sub13, sub2, k, out=out[:T], ids=ids[:T], weights=w[:T])
+    o2, i2, t2 = w8.moe_few_tokens_layer(x[2:2 + T].clone(), wr[4:].clone(), tuple(t.clone() for t in sub13),
+                                         tuple(t.clone() for t in sub2), k)
+    assert torch.equal(out[:T], o2) and torch.equal(ids[:T], i2) and torch.equal(w[:T], t2)
+    assert (out[T:] == 7).all() and (ids[T:] == 77).all() and (w[T:] == 7).all()
