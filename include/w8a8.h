@@ -550,6 +550,7 @@ size_t nvfp4_quantize_workspace_bytes(int64_t G, int64_t R, int64_t K);
  *           2^-96 and 2^112; a block whose scale would pass 448 saturates)
  *   workspace  nvfp4_quantize_workspace_bytes bytes; may be NULL where
  *           gscale_given != 0
+ *   With R = 0 nothing is written, gscale neither.
  *   K a positive multiple of 16, R * K at most 2^40; groups are cut into at
  *   most 1024 chunks of 4096 values or more, at most 2^31 - 1 in all.
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, WORKSPACE, DEVICE,
@@ -571,8 +572,8 @@ int nvfp4_dequantize(const uint8_t* q_fp4, const uint8_t* scale_e4m3, const floa
  *   mxfp4: y[m,n] = bf16( sum_k x[m,k] * 2^(w_scale[n,k/32] - 127) * dec(w_q[n,k]) )
  * A code times its block scale is exact in BF16, products are exact in
  * float32, sums are float32, gscale is applied in float32 and the result is
- * rounded to nearest even. M <= 32 runs a weight-streaming kernel, larger M a
- * tiled one.
+ * rounded to nearest even. M <= 32 runs a weight-streaming kernel, larger M
+ * tiles that grow with the work.
  *   x_bf16 [M, K]; w_q [N, K/2]; w_scale [N, K/16] or [N, K/32]
  *   w_gscale  [1] float32, on the device, 4-byte aligned (it may be an element
  *             of a vector)

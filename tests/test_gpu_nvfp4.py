@@ -264,3 +264,26 @@ def test_quantise_and_multiply_in_a_graph(M):
             assert np.array_equal(bf16_bits(o), r)
         chain(xs[2])
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", [(1, 64, 96), (20, 4112, 160), (40, 96, 32), (900, 2000, 96), (1030, 2032, 1120),
+                                   (4100, 2064, 32)])
+def test_gemm_nan_scales_stay_in_their_row(fmt, M, N, K):
+    """A NaN block scale is its row's alone: K ends inside a step, where the next bytes are the next row's."""
+    print(f"[{fmt} NaN] {M}x{N}x{K}", flush=True)
+    rng = np.random.default_rng(N)
+    x = synth.activations(rng, M, K)
+    (q, s, *g), _ = random_codes(rng, fmt, N, K)
+    q, s, g = q[0], s[0].copy(), [np.float32([v[0]]) for v in g]
+    want = _gemm(fmt, x, (q, s, *g))
+    bad = np.arange(1, N, 5)
+    s[bad] = 0xFF if fmt == "mxfp4" else 0x7F
+    got = _gemm(fmt, x, (q, s, *g))
+    keep = np.setdiff1d(np.arange(N), bad)
+    assert np.array_equal(got[:, keep], want[:, keep])
+
+
+def test_quantize_no_rows():
+    q, s, g = w8.nvfp4_quantize(torch.empty((3, 0, 32), dtype=torch.bfloat16, device="cuda"))
+    assert q.shape == (3, 0, 16) and s.shape == (3, 0, 2) and g.tolist() == [1.0, 1.0, 1.0]

@@ -856,8 +856,8 @@ def nvfp4_quantize(x, gscale=None, q=None, scale=None, workspace=None):
         q = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=x.device)
     if scale is None:
         scale = torch.empty(lead + (K // 16,), dtype=torch.uint8, device=x.device)
-    if gscale is None:
-        gscale = torch.empty((G,), dtype=torch.float32, device=x.device)
+    if gscale is None:  # groups without rows count as all-zero ones; the library writes the others'
+        gscale = (torch.empty if R else torch.ones)((G,), dtype=torch.float32, device=x.device)
     dev = _same_device(x, (x, torch.bfloat16, lead + (K,), "x"), (q, torch.uint8, lead + (K // 2,), "q"),
                        (scale, torch.uint8, lead + (K // 16,), "scale"), (gscale, torch.float32, (G,), "gscale"))
     if workspace is None and not given:

@@ -569,8 +569,8 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[a][t] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](const Buf& b, int kk) {  // kk: first K of the round inside the staged piece
-    b.sc.spread(slds[wave]);
+  auto compute = [&](const Buf& b, int k0, int kk) {  // first K of the round, and inside the staged piece
+    b.sc.spread(slds[wave], (K - k0 - k_wave) / W::kBlock);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t at = 2u * (uint32_t)(kk + k_wave + u * W::kStepK + W::kLaneK * g);
@@ -655,7 +655,7 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
       lds_barrier();
     }
     __builtin_amdgcn_sched_barrier(0);
-    compute(cur, kk);
+    compute(cur, k0, kk);
     k0 += kRound;
     kk = kk + kRound < KC ? kk + kRound : 0;
     if (k0 >= k_pad) {

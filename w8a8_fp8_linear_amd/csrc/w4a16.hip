@@ -248,8 +248,9 @@ void w4a16_tiled(const W4Args p, int tiles_m, int tiles_n) {
       const uint32_t shift = (skew + (uint32_t)(piece / kRowPieces * rs) + (uint32_t)(k / W::kBlock)) & 3u;
       const uint32_t d[5] = {(uint32_t)sq[i].x, (uint32_t)sq[i].y, (uint32_t)sq[i].z, (uint32_t)sq[i].w, stop[i]};
       uint32_t* o = reinterpret_cast<uint32_t*>(dst + piece / kRowPieces * C::kScaleStride + piece % kRowPieces * 16);
+      const int left = (K - k) / W::kBlock;  // past the row's end 0, not the next row's
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_alignbyte(d[j + 1], d[j], shift);
+      for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_alignbyte(d[j + 1], d[j], shift) & low_bytes(left - 4 * j);
     }
   };
   v4f acc[C::SN][C::SM];

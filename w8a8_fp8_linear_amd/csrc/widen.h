@@ -92,6 +92,9 @@ __device__ inline void wave_lds_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// A mask of the lowest n bytes of a dword: none for n <= 0, all for n >= 4.
+__device__ inline uint32_t low_bytes(int n) { return n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u; }
+
 // The block scales of U consecutive steps of NR sets of 16 weight rows. Read
 // where they are used they would be one or two bytes a lane, 16 cache lines
 // per load for 64 or 128 bytes; instead lane 16 g + r loads 16 bytes of row r
@@ -125,13 +128,20 @@ struct BlockScales {
     }
   }
 
-  // To the wave's LDS; the scales of step u, set a are then at get().
-  __device__ inline void spread(uint8_t* lds) const {
+  // To the wave's LDS; the scales of step u, set a are then at get(). `bytes`:
+  // what is left of the row; past its end a scale is 0, not the next row's,
+  // whose NaN would be one here too although the codes there count as 0.
+  __device__ inline void spread(uint8_t* lds, int bytes) const {
     if constexpr (kAny) {
       const uint32_t d[5] = {(uint32_t)q.x, (uint32_t)q.y, (uint32_t)q.z, (uint32_t)q.w, top};
       v4i o;
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = (int)__builtin_amdgcn_alignbyte(d[i + 1], d[i], shift);
+      const int left = bytes - ((threadIdx.x & 63) >> 4) % kPieces * 16;
+      if (left < 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] &= (int)low_bytes(left - 4 * i);
+      }
       wave_lds_order();
       *reinterpret_cast<v4i*>(lds + (threadIdx.x & 63) * 16) = o;
       wave_lds_order();
@@ -206,7 +216,7 @@ __device__ inline void stream_dot(__amdgpu_buffer_rsrc_t rW, __amdgpu_buffer_rsr
           x[u][t][i] = buffer_load16(rX, live ? xrow[t] + 2u * (uint32_t)kw + 16u * i : kOutOfRange);
     }
     __builtin_amdgcn_sched_barrier(0);
-    sc.spread(lds);
+    sc.spread(lds, (K - k0) / W::kBlock);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       uint32_t s[NR];
