@@ -15,13 +15,13 @@
 //    score + bias, and their weights.
 //  * few_rows (gate/up): tiles of 16 columns of h: the 16 gate and 16 up rows
 //    of an expert, for every token that picked it (the MFMA's column side).
-//    h = silu(g) * u is written as a
-//    pair of BF16 values, h = hi + lo: 16 significant bits, so that the down
-//    product of an h kept in float32 (the reading of the grouped calls) is
-//    met to 2^-17 while it runs on the BF16 matrix cores.
-//  * few_down_small (at most 8 tokens and 64 routed copies): one workgroup per 4 or
-//    8 output columns walks all picked experts, a wave an expert, and adds
-//    the router-weighted results per token in registers.
+//    h = silu(g) * u is written as a pair of BF16 values, h = hi + lo: 16
+//    significant bits, so that the down product of an h kept in float32 (the
+//    reading of the grouped calls) is met to 2^-17 while it runs on the BF16
+//    matrix cores.
+//  * few_down_small (at most 8 tokens and 64 routed copies): one workgroup per
+//    4 or 8 output columns walks all picked experts, a wave an expert, and
+//    adds the router-weighted results per token in registers.
 //  * few_rows (down) + few_combine (more): tiles of 32 rows of an expert's W2
 //    leave its tokens' weighted float32 rows, and the rows of a token are
 //    added in the order of its slots.
@@ -115,7 +115,10 @@ struct RouterArgs {
   float scale;
 };
 
-// Few tokens: a wave per expert, lanes along K, TT tokens.
+// Few tokens: a wave per expert, lanes along K, TT tokens. One round of load
+// latency (1 token, 192 experts, H 1024: 2.8 us; 64 tokens, 64 experts, H
+// 2048: 4.7 us), so up to two tokens get workgroups of their own; more share
+// a read of the expert's row.
 template <int TT>
 __global__ __launch_bounds__(256) void router_logits_few(const RouterArgs p) {
   constexpr int U = TT <= 2 ? 4 : 2;  // 512-value pieces of the rows loaded together
@@ -161,7 +164,9 @@ __global__ __launch_bounds__(256) void router_logits_few(const RouterArgs p) {
 // cores, K split over the 8 waves in 32-deep steps. A lane loads 8
 // consecutive values of its token's and of its expert's row (K 8 g .. of the
 // step); MFMA i takes value i of each, so the step's K order is permuted alike
-// on both sides.
+// on both sides. Bound by the float64 matrix units (4096 tokens x 64 experts x
+// 2048: 25.0 us, 14.5 us at their full rate; four expert tiles a workgroup with
+// loads a step ahead: 24.0 us, not worth a second variant for fewer tokens).
 __global__ __launch_bounds__(512) void router_logits_mfma(const RouterArgs p) {
   __shared__ double red[8][256];
   constexpr int U = 4;
@@ -212,7 +217,8 @@ __global__ __launch_bounds__(512) void router_logits_mfma(const RouterArgs p) {
 // The choice: a wave per token, lane l holding the NV experts from NV * l on.
 // k times the largest of what is left: the lanes' largest, the wave's, and
 // the first lane that has it, so that equal scores go by index. Lane j < k
-// returns the j-th expert and its weight.
+// returns the j-th expert and its weight. A chain of dependent steps: 2.8 us
+// for one token's 4 of 192, 4.8 us for 4096 tokens' 8 of 64.
 template <int NV>
 __device__ inline void select_token(const RouterArgs& p, int t, int lane, int* id, float* tw) {
   const double* l = p.logits + (int64_t)t * p.E;
@@ -393,6 +399,11 @@ __device__ inline v4f row_scales(const void* s, const float* g, int64_t row, int
   }
 }
 
+// Steps of a round of few_rows. 2: a round fits 64 tokens' h in LDS, or a
+// short K split over waves.
+template <int F, bool DOWN, int NT, int KS>
+constexpr int kRowsU = F == kFmtFp8 || (KS == 1 && !DOWN) ? 4 : 2;
+
 // One projection of one group of tokens. A tile is two sets of 16 weight rows
 // (gate/up: 16 gate rows and their up rows; down: 32 rows); KS waves split a
 // tile's K, so a workgroup holds kFewWaves / KS tiles at a time and takes
@@ -404,9 +415,11 @@ __device__ inline v4f row_scales(const void* s, const float* g, int64_t row, int
 // of 2 x 16 rows x 64 bytes at a time, with the next U steps' loads issued
 // before the current ones are used: nothing but the start waits for the
 // weight stream, and with two workgroups per CU 128 KB of it are in flight.
-template <int F, bool DOWN, int NT, int KS>
-constexpr int kRowsU = F == kFmtFp8 || (KS == 1 && !DOWN) ? 4 : 2;  // 2: a round fits 64 tokens' h, or a short split K
-
+//
+// FP8, 64 tokens of 64 experts, 2048 x 512: gate/up 134 MB in 30 us (4.5
+// TB/s), down 67 MB in 21 us (both parts of h are read from LDS for every
+// weight). 8 tokens, nvfp4: gate/up about 50 MB in 17.5 us, of which some 4 us
+// are the start (ids, then inputs and weights).
 //
 // ROUTE (at most kFewWaves tokens, few workgroups): the choice is made here
 // from the logits, a wave per token, by every workgroup for itself, and
@@ -679,7 +692,8 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
 }
 
 // out[t] = bf16(sum of the token's rows, in the order of its slots). A slot
-// counts if its id is valid and no earlier slot of the token names it.
+// counts if its id is valid and no earlier slot of the token names it. 4.7 us
+// for 64 tokens' 8 rows of 2048: the ids, then eight rows' loads at once.
 __global__ __launch_bounds__(256) void few_combine(const FewArgs p) {
   const int t = blockIdx.y, lane = threadIdx.x & 63;
   const int c = (blockIdx.x * 256 + threadIdx.x) * 4;
@@ -712,7 +726,10 @@ __global__ __launch_bounds__(256) void few_combine(const FewArgs p) {
 // tokens at the same places: of the 16 x 16 results those count whose row and
 // column are at the same place of K, and the places are added at the end. A
 // wave takes every WAVES-th expert, in the order of their first slots; lane s
-// holds slot s's id and weight, so a ballot finds the expert's tokens.
+// holds slot s's id and weight, so a ballot finds the expert's tokens. Bound
+// by the reads of h, 8 times the 4-bit weights' bytes at R = 8 (8 tokens of 64
+// nvfp4 experts, 2048 x 512: 12.0 us; loads a piece ahead do not help, 13.6
+// us). One token's 4 fp8 experts, 1024 x 512: 4.3 us.
 template <int F, int R, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void few_down_small(const FewArgs p) {
   using W = WideFmt<F>;

@@ -10,15 +10,19 @@
 // are exact in float32, sums are float32, g is applied once in float32 and
 // the result is rounded to nearest even.
 //
-//  * w4a16_skinny: at most 32 rows, set by the weight stream. 16 or 32 weight
-//    rows per workgroup, the 4 waves split K, every lane widens the 32 codes of
-//    its 16-byte load in registers.
-//  * w4a16_tiled: more rows. BM x BN tiles, 64-deep K steps in three
-//    LDS stages by direct loads (128 bytes of activations, 32 bytes of codes a
-//    row). The tile's block scales come 16 steps at a time, through registers
-//    (scale rows need not start on a dword), and are read from LDS; a byte load
-//    per lane and step instead was more than half of all requests to L2
-//    (nvfp4, 4096 x 6144 x 2048: 148 us).
+//  * w4a16_skinny: at most 32 rows, bound by the weight stream's latency and
+//    the activations' L2 traffic. 16 or 32 weight rows per workgroup, the 4
+//    waves split K, every lane widens the 32 codes of its 16-byte load in
+//    registers (nvfp4 1 x 8192 x 2048: 4.8 us for 9.4 MB; mxfp4 24 x 6160 x
+//    2048: 6.7 us).
+//  * w4a16_mid: 64 x 64 results a workgroup (mxfp4 301 x 1040 x 1056: 8.2 us).
+//  * w4a16_tiled: BM x BN tiles, 64-deep K steps in three LDS stages by direct
+//    loads (128 bytes of activations, 32 bytes of codes a row). The tile's
+//    block scales come 16 steps at a time, through registers (scale rows need
+//    not start on a dword), and are read from LDS; a byte load per lane and
+//    step instead was more than half of all requests to L2. A SIMD's MFMAs,
+//    widening and LDS reads share its time (nvfp4, 4096 x 6144 x 2048: 101 us
+//    back to back, 1016 TFLOP/s; mxfp4 95 us).
 #include "device.h"
 #include "launch.h"
 #include "widen.h"
