@@ -15,7 +15,7 @@ def _no_gpu():
 
 def test_nvfp4_quantize():
     f, need = w8.lib().nvfp4_quantize, w8.lib().nvfp4_quantize_workspace_bytes
-    assert need(1, 1, 16) == 256 and need(3, 1024, 1024) == 3072 and need(1, 1 << 20, 1024) == 4096 and need(1, 1, 24) == 0 and need(-1, 1, 16) == 0
+    assert need(1, 1, 16) == 256 and need(5, 1024, 1024) == 5120 and need(1, 1 << 20, 1024) == 4096 and need(1, 1, 24) == 0 and need(-1, 1, 16) == 0
     assert f(P, -1, 1, 16, P, P, P, 0, P, 256, None) == SHAPE
     assert f(P, 1 << 40, 1 << 20, 1 << 20, P, P, P, 0, P, 256, None) == SHAPE
     assert f(P, 1, 4, 24, P, P, P, 0, P, 256, None) == UNSUP
