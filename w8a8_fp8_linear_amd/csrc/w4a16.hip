@@ -15,7 +15,8 @@
 //    waves split K, every lane widens the 32 codes of its 16-byte load in
 //    registers (nvfp4 1 x 8192 x 2048: 4.8 us for 9.4 MB; mxfp4 24 x 6160 x
 //    2048: 6.7 us).
-//  * w4a16_mid: 64 x 64 results a workgroup (mxfp4 301 x 1040 x 1056: 8.2 us).
+//  * w4a16_mid: 32 x 64 or 64 x 64 results a workgroup, bound by a few rounds of
+//    load latency and L1's rate (mxfp4 301 x 1040 x 1056: 5.9 us).
 //  * w4a16_tiled: BM x BN tiles, 64-deep K steps in three LDS stages by direct
 //    loads (128 bytes of activations, 32 bytes of codes a row). The tile's
 //    block scales come 16 steps at a time, through registers (scale rows need
@@ -94,19 +95,19 @@ __global__ __launch_bounds__(64 * WAVES) void w4a16_skinny(const W4Args p) {
   }
 }
 
-// Some rows, too few for the tiled kernel to fill the GPU: 64 x 64 results a
+// Some rows, too few for the tiled kernel to fill the GPU: 16 TM x 64 results a
 // workgroup, K split over its 4 waves, operands straight from global memory
 // (the activations from L2); a wave's K fits a few rounds of loads.
-template <int F>
+template <int F, int TM>
 __global__ __launch_bounds__(256) void w4a16_mid(const W4Args p) {
   using W = WideFmt<F>;
-  constexpr int TN = 4, TM = 4;
+  constexpr int TN = 4;
   __shared__ v4f red[2][TN * TM][64];
   __shared__ __attribute__((aligned(16))) uint8_t slds[4][BlockScales<F, TN, 1>::kLds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles_n = (p.N + 63) / 64;
-  const int n0 = blockIdx.x % tiles_n * 64, m0 = blockIdx.x / tiles_n * 64;
+  const int n0 = blockIdx.x % tiles_n * 64, m0 = blockIdx.x / tiles_n * 16 * TM;
   const int64_t rb = W::row_bytes(p.K), rs = W::row_scales(p.K);
   const auto rW = make_rsrc(p.w + n0 * rb, (p.N - n0) * rb);
   uint32_t skew;
@@ -409,13 +410,18 @@ hipError_t launch_w4(const W4Args& a, hipStream_t stream) {
     return hipGetLastError();
   }
   // The tile grows with the work, so that each kernel starts with at most one
-  // workgroup a CU: 64 x 64 with K split (64 x 6144 x 2048: 14.8 us against
-  // 20.8 us in 64 x 128 tiles), 64 x 128 (256 x 6144 x 2048: 21.6 us against
+  // workgroup a CU: 32 x 64 with K split (64 x 6144 x 2048: 10.6 us against
+  // 15.0 us in 64 x 64; but 128 x 6144 x 2048: 16.4 against 15.1 us), 64 x 64
+  // (64 x 16384 x 2048: 15.9 us against 20.8 us in 64 x 128 tiles), 64 x 128 (256 x 6144 x 2048: 21.6 us against
   // 25.2 us in 64 x 64 and 27.0 us in 128 x 128), 128 x 128 (512 x 6144 x 2048:
   // 27.3 us against 35.3 us in 64 x 64 and 49.8 us in 256 x 192).
   const auto tiles = [&](int bm, int bn) { return (int64_t)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  if (tiles(32, 64) <= kCUs) {
+    hipLaunchKernelGGL((w4a16_mid<F, 2>), dim3((unsigned)tiles(32, 64)), dim3(256), 0, stream, a);
+    return hipGetLastError();
+  }
   if (tiles(64, 64) <= kCUs) {
-    hipLaunchKernelGGL(w4a16_mid<F>, dim3((unsigned)tiles(64, 64)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((w4a16_mid<F, 4>), dim3((unsigned)tiles(64, 64)), dim3(256), 0, stream, a);
     return hipGetLastError();
   }
   if (tiles(64, 128) <= kCUs) return launch_tiled<F, 64, 128, 1, 4, 2>(a, stream);
