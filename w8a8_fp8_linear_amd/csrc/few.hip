@@ -773,6 +773,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_small(const FewArgs p) {
     const int slot = mine ? tok * p.k + __builtin_ctzll(mine) : 0;
     const uint32_t at = (uint32_t)slot * (uint32_t)p.I * 4u;
     const uint32_t xrow[2] = {mine ? at : kOutOfRange, mine ? at + (uint32_t)p.I * 2u : kOutOfRange};
+    const bool picked = mine != 0;
     float w = 0.f;
     while (__ballot(mine != 0)) {  // once, or again for a token that names the expert again
       const float v = __shfl(tw, mine ? tok * p.k + __builtin_ctzll(mine) : 0, 64);
@@ -781,8 +782,11 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_small(const FewArgs p) {
     }
     v4f acc[1][2] = {{v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}}};
     stream_dot<F, 1, 2, U>(rW, rS, wrow, srow, rX, xrow, p.I, (r16 / R) * steps * W::kStepK, steps, slds[wave], acc);
-    y += (acc[0][0] + acc[0][1]) * row_scales<F>(p.s2, p.g2, (int64_t)e * p.H + row0 + (4 * g) % R, e) *
-         v4f{w, w, w, w};
+    // added for the tokens that picked the expert alone: 0 times its NaN would be NaN for the others
+    const v4f add = (acc[0][0] + acc[0][1]) * row_scales<F>(p.s2, p.g2, (int64_t)e * p.H + row0 + (4 * g) % R, e) *
+                    v4f{w, w, w, w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = picked ? y[i] + add[i] : y[i];
   }
   // lane (r16, g): rows 4 g .. 4 g + 3 of the operand, that is output columns
   // row0 + (4 g) % R .. at place 4 g / R; column r16: token r16 % R at place r16 / R
