@@ -632,8 +632,7 @@ size_t moe_few_tokens_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E
 /*
  * moe_few_tokens — one routed-expert pass for at most 64 tokens:
  *   g, u   = gate and up halves of W13[e] . x[t]          (float32)
- *   h      = silu(g) * u                                  (float32, carried
- *            as the sum of two BF16 values, 16 significant bits)
+ *   h      = silu(g) * u                                  (float32)
  *   out[t] = bf16( sum over j with a valid id of topk_w[t,j] * (W2[e] . h) )
  * Sums are float32 in an order fixed by the ids; a token that names an expert
  * twice counts it with the sum of the two weights; a token without a valid id

@@ -1024,8 +1024,8 @@ def moe_few_tokens(x, topk_ids, topk_w, w13, w2, out=None, workspace=None):
     """One routed-expert pass in the default maths for at most 64 tokens: BF16 [T, H].
 
     x BF16 [T, H] as it is, the experts' FP8, MXFP4 or NVFP4 weights widened
-    as they are multiplied; h = silu(g) * u is not rounded below 16 bits and a
-    token's weighted sum is rounded to BF16 once."""
+    as they are multiplied; h = silu(g) * u stays in float32 and a token's
+    weighted sum is rounded to BF16 once."""
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be [T, k]")
     dev, fmt, experts, out, sizes, ws = _few_args(x, topk_ids, topk_w, w13, w2, out, workspace, topk_ids.shape[1])

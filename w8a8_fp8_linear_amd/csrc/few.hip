@@ -15,16 +15,14 @@
 //    score + bias, and their weights.
 //  * few_rows (gate/up): tiles of 16 columns of h: the 16 gate and 16 up rows
 //    of an expert, for every token that picked it (the MFMA's column side).
-//    h = silu(g) * u is written as a pair of BF16 values, h = hi + lo: 16
-//    significant bits, so that the down product of an h kept in float32 (the
-//    reading of the grouped calls) is met to 2^-17 while it runs on the BF16
-//    matrix cores.
+//    h = silu(g) * u is kept in float32 (the reading of the grouped calls).
 //  * few_down_small (at most 8 tokens and 64 routed copies): one workgroup per
-//    4 or 8 output columns walks all picked experts, a wave an expert, and
-//    adds the router-weighted results per token in registers.
+//    8 output columns walks all picked experts, a wave an expert, and
+//    adds the router-weighted results per token in registers, by float32 FMAs.
 //  * few_rows (down) + few_combine (more): tiles of 32 rows of an expert's W2
 //    leave its tokens' weighted float32 rows, and the rows of a token are
-//    added in the order of its slots.
+//    added in the order of its slots. The BF16 matrix cores take h as three
+//    BF16 values, h = hi + mid + lo: 3 x 8 significant bits are float32's 24.
 // The output is rounded to BF16 once. Every sum's order is fixed by the ids
 // and the sizes alone.
 //
@@ -317,7 +315,7 @@ struct FewArgs {
   const uint8_t* w2;      // [E, H, I] codes
   const void* s2;
   const float* g2;
-  uint16_t* h;            // [T * k, 2, I]: hi and lo of every routed copy's h
+  float* h;               // [T * k, I]: every routed copy's h
   float* y;               // [T * k, H]: weighted float32 rows (few_down_rows)
   uint16_t* out;          // [T, H]
   int T, H, I, E, k, by_slot;
@@ -399,26 +397,46 @@ __device__ inline v4f row_scales(const void* s, const float* g, int64_t row, int
   }
 }
 
-// Steps of a round of few_rows. 2: a round fits 64 tokens' h in LDS, or a
-// short K split over waves.
+// Steps of a round of few_rows: fewer for a short K split over waves, and where
+// four waves' rounds would not leave the staged h (three values) in LDS.
 template <int F, bool DOWN, int NT, int KS>
-constexpr int kRowsU = F == kFmtFp8 || (KS == 1 && !DOWN) ? 4 : 2;
+constexpr int kRowsU = (F == kFmtFp8 || (KS == 1 && !DOWN) ? 4 : 2) / (DOWN && KS == 4 ? 2 : 1);
+
+// LDS for the staged rows, so that two workgroups share a CU.
+constexpr int kRowsLds = 65536;
+
+// 8 float32 values -> three BF16 operands whose sum is the values: each is the
+// upper half of what the ones before leave, 8 significant bits. The
+// subtractions are exact.
+__device__ inline void split3(const float (&h)[8], v4i (&part)[3]) {
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = h[i];
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[q][i] = (int)pack_bf16(r[2 * i], r[2 * i + 1]);
+    if (q == 2) break;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] -= __uint_as_float(__float_as_uint(r[i]) & 0xFFFF0000u);
+  }
+}
 
 // One projection of one group of tokens. A tile is two sets of 16 weight rows
 // (gate/up: 16 gate rows and their up rows; down: 32 rows); KS waves split a
 // tile's K, so a workgroup holds kFewWaves / KS tiles at a time and takes
 // `rounds` such sets of tiles one after another.
 //
-// The group's input rows (gate/up: x; down: hi and lo of h) are staged in LDS
-// once, in pieces of KC inputs if they do not fit whole, and every wave reads
-// its MFMA columns from there. The weights go straight to registers, U steps
+// The group's input rows (gate/up: x; down: the three parts of h, taken apart on
+// the way) are staged in LDS once, in pieces of KC inputs if they do not fit
+// whole, and every wave reads its MFMA columns from there. The weights go straight to registers, U steps
 // of 2 x 16 rows x 64 bytes at a time, with the next U steps' loads issued
 // before the current ones are used: nothing but the start waits for the
 // weight stream, and with two workgroups per CU 128 KB of it are in flight.
 //
 // FP8, 64 tokens of 64 experts, 2048 x 512: gate/up 134 MB in 30 us (4.5
-// TB/s), down 67 MB in 21 us (both parts of h are read from LDS for every
-// weight). 8 tokens, nvfp4: gate/up about 50 MB in 17.5 us, of which some 4 us
+// TB/s), down 67 MB in 22 us (nvfp4 21 us), of which the third part of h is 1.2
+// us and taking h apart another. 8 tokens, nvfp4: gate/up about 50 MB in 17.5 us, of which some 4 us
 // are the start (ids, then inputs and weights).
 //
 // ROUTE (at most kFewWaves tokens, few workgroups): the choice is made here
@@ -430,7 +448,7 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
   using W = WideFmt<F>;
   constexpr int U = kRowsU<F, DOWN, NT, KS>;
   using S = BlockScales<F, 2, U>;
-  constexpr int P = DOWN ? 2 : 1;                 // parts of the input: h = hi + lo
+  constexpr int P = DOWN ? 3 : 1;                 // parts of the input: h = hi + mid + lo
   constexpr int kRound = U * KS * W::kStepK;      // K values a round of loads covers
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   __shared__ int cols[64];
@@ -517,10 +535,13 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
   const int n = grp.n;
   auto pass = [&](auto tt) {
   constexpr int TT = decltype(tt)::value;
-  // KC: whole rounds, all of K if the n rows fit
+  // KC: all of K if the n rows fit, else whole rounds; half a round where the
+  // most rows that TT has would not fit otherwise
+  constexpr int SUB = 16 * TT * 2 * P * kRound > kRowsLds ? 2 : 1;
+  static_assert(16 * TT * 2 * P * kRound / SUB <= kRowsLds && (SUB == 1 || KS == 1), "a piece of all rows must fit");
   const int k_all = (K + kRound - 1) / kRound * kRound;
   const int fit = lds_bytes / (n * 2 * P) / kRound * kRound;
-  const int KC = fit < k_all ? fit : k_all;
+  const int KC = fit == 0 ? kRound / SUB : fit < k_all ? fit : k_all;
   const int k_pad = (k_all + KC - 1) / KC * KC;
   const int cpr = KC >> 3;                        // 16-byte chunks of a staged row
 
@@ -541,31 +562,64 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
     load_next(buf[0], true);
   }
 
-  // Rows go to LDS in 1 KB pieces of 64 chunks; the 16-byte chunks of row r
-  // are stored with their index XORed with r % 8, so that the 8 rows that 8
-  // lanes read at one K lie in different banks.
-  auto stage = [&](int k0) {
-    for (int row = wave; row < P * n; row += kFewWaves) {
-      const int part = row >= n ? 1 : 0;
-      const int slot = cols[row - part * n];
-      const uint32_t base = DOWN ? (uint32_t)slot * (uint32_t)p.I * 4u + (uint32_t)part * (uint32_t)p.I * 2u
-                                 : (uint32_t)(slot / p.k) * (uint32_t)p.H * 2u;
-      uint8_t* dst = smem + row * (KC * 2);
-      for (int c0 = 0; c0 < cpr; c0 += 64) {
-        const int k = k0 + 8 * ((c0 + lane) ^ (row & 7));
-        if (c0 + lane < cpr) buffer_load16_lds(rX, dst + c0 * 16, k < K ? base + 2u * (uint32_t)k : kOutOfRange);
+  // A staged row holds its parts one after another; the 16-byte chunks of row
+  // r are stored with their index XORed with r % 8, so that the 8 rows that 8
+  // lanes read at one K lie in different banks. `loads` is called once the first
+  // rows' loads are on their way.
+  auto stage = [&](int k0, auto loads) {
+    if constexpr (DOWN) {
+      // four runs of 8 values a thread at a time
+      const int runs = n * cpr;
+      const float per_row = 1.0f / (float)cpr;
+      auto batch = [&](int i0, auto between) {
+        v4i v[4][2];
+        uint32_t dst[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + 64 * kFewWaves * j;
+          const int row = i < runs ? (int)(((float)i + 0.5f) * per_row) : 0;  // i / cpr: i is below 2^12
+          const int c = i - row * cpr, k = k0 + 8 * c;
+          const uint32_t at = i < runs && k < K ? ((uint32_t)cols[row] * (uint32_t)p.I + (uint32_t)k) * 4u : kOutOfRange;
+          v[j][0] = buffer_load16(rX, at);
+          v[j][1] = buffer_load16(rX, at + 16u);
+          dst[j] = (uint32_t)(row * KC * (2 * P) + ((c ^ (row & 7)) << 4));
+        }
+        between();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (i0 + 64 * kFewWaves * j >= runs) break;
+          float h[8];
+          v4i part[P];
+#pragma unroll
+          for (int e8 = 0; e8 < 8; ++e8) h[e8] = __int_as_float(v[j][e8 >> 2][e8 & 3]);
+          split3(h, part);
+#pragma unroll
+          for (int q = 0; q < P; ++q) *reinterpret_cast<v4i*>(smem + dst[j] + q * (KC * 2)) = part[q];
+        }
+      };
+      batch(tid, loads);
+      for (int i0 = tid + 64 * kFewWaves * 4; i0 < runs; i0 += 64 * kFewWaves * 4) batch(i0, [] {});
+    } else {
+      for (int row = wave; row < n; row += kFewWaves) {  // in 1 KB pieces of 64 chunks
+        const uint32_t base = (uint32_t)(cols[row] / p.k) * (uint32_t)p.H * 2u;
+        uint8_t* dst = smem + row * (KC * 2);
+        for (int c0 = 0; c0 < cpr; c0 += 64) {
+          const int k = k0 + 8 * ((c0 + lane) ^ (row & 7));
+          if (c0 + lane < cpr) buffer_load16_lds(rX, dst + c0 * 16, k < K ? base + 2u * (uint32_t)k : kOutOfRange);
+        }
       }
+      loads();
+      wait_vmem_all();
     }
   };
-  uint32_t xrow[P][TT], xswz[P][TT];  // this lane's staged rows (columns past the last one read it again)
+  uint32_t xrow[TT], xswz[TT];  // this lane's staged rows (columns past the last one read it again)
 #pragma unroll
-  for (int q = 0; q < P; ++q)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const uint32_t row = (uint32_t)(q * n + min(t * 16 + r16, n - 1));
-      xrow[q][t] = row * (uint32_t)(KC * 2);
-      xswz[q][t] = (row & 7u) << 4;
-    }
+  for (int t = 0; t < TT; ++t) {
+    const uint32_t row = (uint32_t)min(t * 16 + r16, n - 1);
+    xrow[t] = row * (uint32_t)(KC * 2 * P);
+    xswz[t] = (row & 7u) << 4;
+  }
   v4f scale[2];  // the current tile's row scales
   auto load_scales = [&]() {
 #pragma unroll
@@ -582,11 +636,10 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[a][t] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](const Buf& b, int k0, int kk) {  // first K of the round, and inside the staged piece
-    b.sc.spread(slds[wave], (K - k0 - k_wave) / W::kBlock);
+  auto compute = [&](const Buf& b, int sub, int kk) {  // part of the round, its first K inside the staged piece
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t at = 2u * (uint32_t)(kk + k_wave + u * W::kStepK + W::kLaneK * g);
+    for (int u = sub * (U / SUB); u < (sub + 1) * (U / SUB); ++u) {
+      const uint32_t at = 2u * (uint32_t)(kk + k_wave + (u - sub * (U / SUB)) * W::kStepK + W::kLaneK * g);
       const uint32_t s0 = S::get(slds[wave], u, 0), s1 = S::get(slds[wave], u, 1);
 #pragma unroll
       for (int i = 0; i < W::kMfma; ++i) {
@@ -595,7 +648,7 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
         for (int t = 0; t < TT; ++t)
 #pragma unroll
           for (int q = 0; q < P; ++q) {
-            const v4i x = *reinterpret_cast<const v4i*>(smem + xrow[q][t] + ((at + 16u * i) ^ xswz[q][t]));
+            const v4i x = *reinterpret_cast<const v4i*>(smem + xrow[t] + q * (KC * 2) + ((at + 16u * i) ^ xswz[t]));
             acc[0][t] = mfma_16x16x32_bf16(w0, x, acc[0][t]);
             acc[1][t] = mfma_16x16x32_bf16(w1, x, acc[1][t]);
           }
@@ -632,17 +685,10 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
             *reinterpret_cast<v4f*>(dst) = v0 * v4f{w, w, w, w};
             *reinterpret_cast<v4f*>(dst + 16) = v1 * v4f{w, w, w, w};
           } else {
-            float h[4], lo[4];
+            v4f h;
 #pragma unroll
             for (int r = 0; r < 4; ++r) h[r] = silu_f32(v0[r]) * v1[r];
-            const uint32_t h0 = bf16x2_rne(h[0], h[1]), h1 = bf16x2_rne(h[2], h[3]);
-            lo[0] = h[0] - bf16_lo(h0);
-            lo[1] = h[1] - bf16_hi(h0);
-            lo[2] = h[2] - bf16_lo(h1);
-            lo[3] = h[3] - bf16_hi(h1);
-            uint16_t* dst = p.h + (int64_t)cols[c] * 2 * p.I + row0 + 4 * g;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(h0, h1);
-            *reinterpret_cast<uint2*>(dst + p.I) = make_uint2(bf16x2_rne(lo[0], lo[1]), bf16x2_rne(lo[2], lo[3]));
+            *reinterpret_cast<v4f*>(p.h + (int64_t)cols[c] * p.I + row0 + 4 * g) = h;
           }
         }
       }
@@ -657,20 +703,25 @@ void few_rows(const FewArgs p, const RouterArgs route, int wgs_per_group, int ro
   const int total = rounds * (k_pad / kRound);
   int k0 = 0, kk = 0;  // first K of the current round inside its tile, inside the staged piece
   auto step = [&](int r, const Buf& cur, Buf& next) {
-    const bool fresh = kk == 0 && (KC < k_pad || r == 0);  // a new piece of the input rows
-    if (fresh) {
-      if (r) lds_barrier();  // every wave is done with the piece before
-      stage(k0);
+#pragma unroll
+    for (int sub = 0; sub < SUB; ++sub) {
+      const bool fresh = kk == 0 && (KC < k_pad || r == 0);  // a new piece of the input rows
+      auto loads = [&]() {
+        if (sub == 0) load_next(next, r + 1 < total);
+      };
+      if (fresh) {
+        if (r || sub) lds_barrier();  // every wave is done with the piece before
+        stage(k0 + sub * (kRound / SUB), loads);
+        lds_barrier();
+      } else {
+        loads();
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (sub == 0) cur.sc.spread(slds[wave], (K - k0 - k_wave) / W::kBlock);
+      compute(cur, sub, kk);
+      kk = kk + kRound / SUB < KC ? kk + kRound / SUB : 0;
     }
-    load_next(next, r + 1 < total);
-    if (fresh) {
-      wait_vmem_all();
-      lds_barrier();
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    compute(cur, k0, kk);
     k0 += kRound;
-    kk = kk + kRound < KC ? kk + kRound : 0;
     if (k0 >= k_pad) {
       k0 = 0;
       finish();
@@ -720,45 +771,70 @@ __global__ __launch_bounds__(256) void few_combine(const FewArgs p) {
   *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.H + c) = make_uint2(bf16x2_rne(s[0], s[1]), bf16x2_rne(s[2], s[3]));
 }
 
-// At most R tokens (R = 4 or 8) and 64 slots: R output columns a workgroup,
-// so that a narrow output still fills the GPU. The 16 rows of an MFMA's
-// weight operand are R weight rows at 16 / R places of K, its 16 columns R
-// tokens at the same places: of the 16 x 16 results those count whose row and
-// column are at the same place of K, and the places are added at the end. A
-// wave takes every WAVES-th expert, in the order of their first slots; lane s
-// holds slot s's id and weight, so a ballot finds the expert's tokens. 8 tokens
-// of 64 nvfp4 experts, 2048 x 512: 12.0 us, 3 us and 0.23 us an expert, with
-// 273 vector instructions and 20 loads per expert and wave. No single thing
-// bounds it: loads a piece ahead (13.6 us), all of h in LDS and four pieces
-// ahead (15.0 us) and 16 waves (12.9 us) are no faster. One token's 4 fp8
-// experts, 1024 x 512: 4.3 us.
-template <int F, int R, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void few_down_small(const FewArgs p) {
+// 16 codes (FP8) or 32 (4-bit) of a lane's 16 bytes -> float32, MXFP4's times their block's scale (in its exponent).
+template <int F>
+__device__ inline void codes_f32(v4i w, float scale, float* f) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const uint32_t c = (uint32_t)w[d];
+    if constexpr (F == kFmtFp8) {
+      const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
+      f[4 * d] = a[0], f[4 * d + 1] = a[1], f[4 * d + 2] = b[0], f[4 * d + 3] = b[1];
+    } else {
+      const auto a0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 0), a1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 1);
+      const auto a2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 2), a3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 3);
+      f[8 * d] = a0[0], f[8 * d + 1] = a0[1], f[8 * d + 2] = a1[0], f[8 * d + 3] = a1[1];
+      f[8 * d + 4] = a2[0], f[8 * d + 5] = a2[1], f[8 * d + 6] = a3[0], f[8 * d + 7] = a3[1];
+    }
+  }
+}
+
+// At most 8 tokens and 64 slots: 8 output columns a workgroup, so that a narrow
+// output still fills the GPU. A wave takes every 16th expert, in the order of
+// their first slots; lane s holds slot s's id and weight, so a ballot finds the
+// expert's tokens. Lane (r16, g) works on row r16 % 8 in half r16 / 8 of K and
+// loads 16 code bytes a step; the h rows of the expert's tokens go to LDS by
+// direct loads, 512 values of two tokens at a time, and a token's dot product is
+// float32 FMAs: h keeps its 24 bits, a token that did not pick the expert is not
+// touched, and most experts of so few tokens have one or two, where an MFMA
+// would fill 8 columns. 8 tokens of 64 nvfp4 experts, 2048 x 512: 11.7 us (8 waves:
+// 14.0 us), 1 token 4.7 us; one token's 4 fp8 experts, 1024 x 512: 3.9 us. A wave's
+// experts are a chain of load latencies: with 42 picked experts, three each.
+template <int F>
+__global__ __launch_bounds__(1024) void few_down_small(const FewArgs p) {
   using W = WideFmt<F>;
-  constexpr int C = 16 / R;   // places of K
-  constexpr int U = F == kFmtFp8 ? R / 2 : R / 4;  // the steps of one place of 512 inputs
+  constexpr int WAVES = 16, R = 8, TOK = 8;
+  constexpr int B = 2;                       // tokens staged together
+  constexpr int U = F == kFmtFp8 ? 4 : 2;    // steps of a round
+  constexpr int kHalf = U * W::kStepK;       // inputs of a round in one half of K
+  static_assert(2 * kHalf == 512, "a token's h of a round is two loads of a wave");
+  using S = BlockScales<F, 1, U>;
   __shared__ uint32_t first[kFewMaxE];             // the first slot of every expert
-  __shared__ v4f red[WAVES][64];
-  __shared__ __attribute__((aligned(16))) uint8_t slds[WAVES][BlockScales<F, 1, U>::kLds];
+  __shared__ __attribute__((aligned(1024))) float hbuf[WAVES][B][512];
+  __shared__ __attribute__((aligned(16))) uint8_t slds[WAVES][S::kLds];
+  __shared__ float red[WAVES][TOK][72], sums[WAVES][TOK * R];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r16 = lane & 15, g = lane >> 4;
+  const int r16 = lane & 15, g = lane >> 4, row = r16 % R, half = r16 / R;
   const int row0 = blockIdx.x * R;
   const int slots = p.T * p.k;
   const int id = lane < slots ? p.ids[lane] : -1;
   const float tw = lane < slots ? p.tw[lane] : 0.f;
+  const int slot_tok = lane / p.k;
   const bool valid = id >= 0 && id < p.E;
   for (int i = threadIdx.x; i < p.E; i += 64 * WAVES) first[i] = 64;
   __syncthreads();
   if (wave == 0 && valid) atomicMin(&first[id], (uint32_t)lane);
   __syncthreads();
   uint64_t leaders = __ballot(valid && first[id] == (uint32_t)lane);
-  const int tok = r16 % R;
   const int64_t rb = W::row_bytes(p.I), rs = W::row_scales(p.I);
-  const int steps = ((p.I + W::kStepK - 1) / W::kStepK + C - 1) / C;  // of one place
+  const int steps = ((p.I + W::kStepK - 1) / W::kStepK + 1) / 2;  // of one half
+  const int kbase = half * steps * W::kStepK;
   const auto rX = make_rsrc(p.h, (int64_t)slots * p.I * 4);
-  const uint32_t wrow[1] = {(uint32_t)((r16 % R) * rb)};
-  v4f y = v4f{0.f, 0.f, 0.f, 0.f};
+  const uint64_t kmask = p.k == 64 ? ~0ull : (1ull << p.k) - 1;
+  float y[TOK];
+#pragma unroll
+  for (int t = 0; t < TOK; ++t) y[t] = 0.f;
   for (int i = 0; i < wave; ++i) leaders &= leaders - 1;
   while (leaders) {
     const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(leaders));
@@ -767,40 +843,121 @@ __global__ __launch_bounds__(64 * WAVES) void few_down_small(const FewArgs p) {
     const auto rW = make_rsrc(p.w2 + ((int64_t)e * p.H + row0) * rb, R * rb);
     uint32_t skew;
     const auto rS = scale_rsrc(static_cast<const uint8_t*>(p.s2) + ((int64_t)e * p.H + row0) * rs, R * rs, &skew);
-    const uint32_t srow[1] = {skew + (uint32_t)((r16 % R) * rs)};
-    const uint64_t kmask = p.k == 64 ? ~0ull : (1ull << p.k) - 1;
-    uint64_t mine = tok < p.T ? (same >> (tok * p.k)) & kmask : 0;
-    const int slot = mine ? tok * p.k + __builtin_ctzll(mine) : 0;
-    const uint32_t at = (uint32_t)slot * (uint32_t)p.I * 4u;
-    const uint32_t xrow[2] = {mine ? at : kOutOfRange, mine ? at + (uint32_t)p.I * 2u : kOutOfRange};
-    const bool picked = mine != 0;
-    float w = 0.f;
-    while (__ballot(mine != 0)) {  // once, or again for a token that names the expert again
-      const float v = __shfl(tw, mine ? tok * p.k + __builtin_ctzll(mine) : 0, 64);
-      w += mine ? v : 0.f;
-      mine &= mine - 1;
+    float scale = 1.f;
+    if constexpr (F == kFmtFp8) scale = static_cast<const float*>(p.s2)[(int64_t)e * p.H + row0 + row];
+    if constexpr (F == kFmtNvfp4) scale = p.g2[e];
+    for (int kt = 0; kt < steps; kt += U) {
+      const int k0 = kbase + kt * W::kStepK;
+      v4i w[U];
+      S sc;
+      sc.load(rS, [&](int) { return k0 < p.I ? skew + (uint32_t)(row * rs) + (uint32_t)(k0 / W::kBlock) : kOutOfRange; });
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * W::kStepK + W::kLaneK * g;
+        w[u] = buffer_load16(rW, kt + u < steps && k < p.I ? (uint32_t)(row * rb) + (uint32_t)W::row_bytes(k) : kOutOfRange);
+      }
+      uint32_t hk[2];  // bytes into an h row of the 4 values that this lane brings to LDS for each half
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = 4 * lane;
+        const int k = (i * steps + kt) * W::kStepK + at;
+        hk[i] = kt + at / W::kStepK < steps && k < p.I ? (uint32_t)k * 4u : kOutOfRange;
+      }
+      float f[U][W::kLaneK], s[U][2];
+      uint64_t rest = same;  // slots of the tokens that are still to come
+      bool begun = false;
+      do {  // B tokens
+        int tok[B], slot[B];
+        float weight[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          tok[b] = -1, slot[b] = 0, weight[b] = 0.f;
+          if (rest) {
+            slot[b] = __builtin_ctzll(rest);
+            tok[b] = __builtin_amdgcn_readlane(slot_tok, slot[b]);
+            const uint64_t all = kmask << (tok[b] * p.k);
+            for (uint64_t m = rest & all; m; m &= m - 1)
+              weight[b] += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(tw), __builtin_ctzll(m)));
+            rest &= ~all;
+          }
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): what the batch before reads has arrived
+        wave_lds_order();
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          if (tok[b] < 0) break;
+          const uint32_t at = (uint32_t)slot[b] * (uint32_t)p.I * 4u;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            buffer_load16_lds(rX, &hbuf[wave][b][256 * i], hk[i] == kOutOfRange ? kOutOfRange : at + hk[i]);
+        }
+        wait_vmem_all();
+        wave_lds_order();
+        if (!begun) {
+          begun = true;
+          sc.spread(slds[wave], (p.I - k0) / W::kBlock);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const uint32_t code = S::get(slds[wave], u, 0);
+            codes_f32<F>(w[u], F == kFmtMxfp4 ? mx_scale_value(code) : 1.0f, f[u]);
+            if constexpr (F == kFmtNvfp4) {
+              const auto two = __builtin_amdgcn_cvt_pk_f32_fp8((int)code, false);
+              s[u][0] = two[0], s[u][1] = two[1];
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          if (tok[b] < 0) break;
+          const float* h = &hbuf[wave][b][half * kHalf + W::kLaneK * g];
+          float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int c0 = 0; c0 < W::kLaneK; c0 += 16) {  // 16 values: a block of NVFP4
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int c = c0; c < c0 + 16; c += 4) {
+                const v4f x = *reinterpret_cast<const v4f*>(h + u * W::kStepK + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if constexpr (F == kFmtNvfp4)
+                    d[i] = __builtin_fmaf(f[u][c + i], x[i], d[i]);
+                  else
+                    a[i] = __builtin_fmaf(f[u][c + i], x[i], a[i]);
+                }
+              }
+              if constexpr (F == kFmtNvfp4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(d[i], s[u][c0 / 16], a[i]);
+              }
+            }
+          }
+          const float add = ((a[0] + a[1]) + (a[2] + a[3])) * scale * weight[b];
+#pragma unroll
+          for (int t = 0; t < TOK; ++t) y[t] = tok[b] == t ? y[t] + add : y[t];
+        }
+      } while (rest);
     }
-    v4f acc[1][2] = {{v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}}};
-    stream_dot<F, 1, 2, U>(rW, rS, wrow, srow, rX, xrow, p.I, (r16 / R) * steps * W::kStepK, steps, slds[wave], acc);
-    // added for the tokens that picked the expert alone: 0 times its NaN would be NaN for the others
-    const v4f add = (acc[0][0] + acc[0][1]) * row_scales<F>(p.s2, p.g2, (int64_t)e * p.H + row0 + (4 * g) % R, e) *
-                    v4f{w, w, w, w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = picked ? y[i] + add[i] : y[i];
   }
-  // lane (r16, g): rows 4 g .. 4 g + 3 of the operand, that is output columns
-  // row0 + (4 g) % R .. at place 4 g / R; column r16: token r16 % R at place r16 / R
-  red[wave][lane] = y;
-  __syncthreads();
-  if (threadIdx.x < R * R / 4) {
-    const int t = threadIdx.x % R, q = threadIdx.x / R;  // token, quarter of the columns
-    if (t >= p.T) return;
-    v4f s = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int w = 0; w < WAVES; ++w)
+  // the sum over the lanes that have the same row, then over the waves
 #pragma unroll
-      for (int c = 0; c < C; ++c) s += red[w][(c * (R / 4) + q) * 16 + c * R + t];
-    *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.H + row0 + 4 * q) =
-        make_uint2(bf16x2_rne(s[0], s[1]), bf16x2_rne(s[2], s[3]));
+  for (int t = 0; t < TOK; ++t) red[wave][t][lane] = y[t];
+  wave_lds_order();
+  if (lane < TOK * R) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 64 / R; ++i) v += red[wave][lane / R][i * R + lane % R];
+    sums[wave][lane] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x < TOK * R) {
+    const int t = threadIdx.x / R;
+    if (t >= p.T) return;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) v += sums[w][threadIdx.x];
+    p.out[(int64_t)t * p.H + row0 + threadIdx.x % R] = (uint16_t)bf16x2_rne(v, 0.f);
   }
 }
 
@@ -810,12 +967,12 @@ bool few_small(int64_t T, int64_t topk) { return T <= 8 && T * topk <= 64; }
 
 template <int F, bool DOWN, int NT, int KS, bool ROUTE = false>
 void launch_rows_ks(const FewArgs& a, int groups, hipStream_t stream, const RouterArgs& route = {}) {
-  const int K = DOWN ? a.I : a.H, P = DOWN ? 2 : 1;
+  const int K = DOWN ? a.I : a.H, P = DOWN ? 3 : 1;
   const int tiles = (DOWN ? a.H : a.I) / (DOWN ? 32 : 16), per_wg = kFewWaves / KS;
   const int sets = (tiles + per_wg - 1) / per_wg;  // sets of tiles a group has
   // two workgroups a CU run together; more tiles than they have are taken in
   // turn, with the next tile's weights on their way (down, 64 tokens of 64
-  // experts: 20.6 us against 24.9 us for twice the workgroups)
+  // experts: 22.4 us against 26.9 us for twice the workgroups)
   const int full = a.by_slot ? 1 : groups * sets / 512;  // by copies, many workgroups find nothing to do
   const int rounds = full < 1 ? 1 : full < 4 ? full : 4;
   const int wgs = (sets + rounds - 1) / rounds;
@@ -823,7 +980,7 @@ void launch_rows_ks(const FewArgs& a, int groups, hipStream_t stream, const Rout
   const int k_all = (K + round_k - 1) / round_k * round_k;
   const int rows = a.T < 16 * NT ? a.T : 16 * NT;
   const int64_t want = (int64_t)rows * k_all * 2 * P;
-  const int lds = (int)(want < 65536 ? (want + 1023) / 1024 * 1024 : 65536);  // a load writes 1 KB
+  const int lds = (int)(want < kRowsLds ? (want + 1023) / 1024 * 1024 : kRowsLds);  // a load writes 1 KB
   hipLaunchKernelGGL((few_rows<F, DOWN, NT, KS, ROUTE>), dim3((unsigned)(groups * wgs)), dim3(64 * kFewWaves), lds, stream,
                      a, route, wgs, rounds, lds);
 }
@@ -870,13 +1027,7 @@ hipError_t launch_few_fmt(const FewArgs& a, const RouterArgs* route, hipStream_t
   hipError_t e = launch_rows<F, false>(a, route, stream);
   if (e != hipSuccess) return e;
   if (few_small(a.T, a.k)) {
-    // Every workgroup reads all of h: 8 columns each halve that against 4. One
-    // token's h is small, and its few experts need the workgroups (1 of 128
-    // experts, fp8: 4.4 us against 4.8 us; 2 of 64: 7.4 against 8.7 us).
-    if (a.T == 1)
-      hipLaunchKernelGGL((few_down_small<F, 4, 8>), dim3(a.H / 4), dim3(64 * 8), 0, stream, a);
-    else
-      hipLaunchKernelGGL((few_down_small<F, 8, 8>), dim3(a.H / 8), dim3(64 * 8), 0, stream, a);
+    hipLaunchKernelGGL(few_down_small<F>, dim3(a.H / 8), dim3(1024), 0, stream, a);
     return hipGetLastError();
   }
   e = launch_rows<F, true>(a, nullptr, stream);
@@ -937,7 +1088,7 @@ hipError_t launch_few(const Few& f, const Router* r, int64_t T, int64_t H, int64
                       hipStream_t stream) {
   uint8_t* b = static_cast<uint8_t*>(ws);
   uint8_t* rest = b + few_h_bytes(T, I, topk);
-  const FewArgs a{f.x, f.ids, f.tw, f.w13, f.s13, f.g13, f.w2, f.s2, f.g2, reinterpret_cast<uint16_t*>(b),
+  const FewArgs a{f.x, f.ids, f.tw, f.w13, f.s13, f.g13, f.w2, f.s2, f.g2, reinterpret_cast<float*>(b),
                   reinterpret_cast<float*>(rest), f.out, (int)T, (int)H, (int)I, (int)E, (int)topk, T * topk <= E ? 1 : 0};
   RouterArgs route{};
   const bool fused = r && few_routes(a);
