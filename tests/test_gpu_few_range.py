@@ -1,7 +1,7 @@
 """The few-token experts where a value leaves the ordinary range, or another token's does.
 
 * An expert with NaN or infinite scales reaches the tokens that picked it and no other bit.
-* h between the two projections keeps float32's 24 bits.
+* h between the two projections keeps float32's 24 bits and its range, infinities among it.
 """
 import numpy as np
 import pytest
@@ -112,3 +112,32 @@ def test_h_is_held_in_float32(fmt, T, E):
     ref = h - h * (1 + 2.0 ** -12)
     off = np.abs(y - ref) - (60 * U32 * np.abs(h) + 2.0 ** -18 * np.abs(ref) + 0.5 * bf16_ulp(y))
     assert (off <= 0).all(), (int((off > 0).sum()), float((off / (U32 * np.abs(h))).max()))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,E", _STEPS)
+def test_h_beyond_bf16_and_infinite(fmt, T, E):
+    """h of each token has one value that is not 0: 2^127 (2 - 2^-15), which is finite and above the largest BF16 value,
+    or +-infinity. W2 reads it with both signs; the outputs are that value's multiples, the router weight being 2^-10."""
+    print(f"[few large h] {fmt} T={T} E={E}", flush=True)
+    I, H = 64, 96
+    x = np.zeros((T, H), np.float32)
+    top = np.float32(2 - 2.0 ** -7) * np.float32(2.0 ** 122)
+    kind = np.arange(T) % 3
+    x[:, 0] = np.where(kind == 2, -top, top)
+    x[:, 1] = x[:, 0] * np.float32(2.0 ** -8)       # u = 2^122 (2 - 2^-15) in two BF16 values
+    x[:, 2] = np.where(kind == 0, 32.0, 4096.0)     # silu(32) = 32: 1 + e^-32 is 1 in float32
+    w13, w2 = _ones(fmt, E, 2 * I, H), _ones(fmt, E, H, I)
+    for e in range(E):
+        _set(fmt, w13, e, 7, 2)
+        _set(fmt, w13, e, I + 7, 0)
+        _set(fmt, w13, e, I + 7, 1)
+        for c in range(H):
+            for i in range(I):
+                _set(fmt, w2, e, c, i, negative=bool(c & 1))   # no zero: infinity times 0 is NaN
+    ids = (np.arange(T, dtype=np.int32) % E)[:, None]
+    tw = np.full((T, 1), 2.0 ** -10, np.float32)
+    got = w8.moe_few_tokens(to_dev_bf16(synth.f32_to_bf16_bits(x)), to_dev(ids), to_dev(tw), _dev(w13), _dev(w2))
+    y = oracle.bf16_bits_to_f64(bf16_bits(got))
+    value = np.where(kind == 0, 2.0 ** 118, np.where(kind == 1, np.inf, -np.inf))   # 2^117 (2 - 2^-15) rounds up to 2^118
+    assert np.array_equal(y, value[:, None] * np.where(np.arange(H) & 1, -1.0, 1.0))

@@ -407,7 +407,8 @@ constexpr int kRowsLds = 65536;
 
 // 8 float32 values -> three BF16 operands whose sum is the values: each is the
 // upper half of what the ones before leave, 8 significant bits. The
-// subtractions are exact.
+// subtractions are exact; infinity and NaN are the first operand's alone (their
+// difference with themselves is NaN). A quiet NaN keeps its upper half's bits.
 __device__ inline void split3(const float (&h)[8], v4i (&part)[3]) {
   float r[8];
 #pragma unroll
@@ -418,7 +419,10 @@ __device__ inline void split3(const float (&h)[8], v4i (&part)[3]) {
     for (int i = 0; i < 4; ++i) part[q][i] = (int)pack_bf16(r[2 * i], r[2 * i + 1]);
     if (q == 2) break;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] -= __uint_as_float(__float_as_uint(r[i]) & 0xFFFF0000u);
+    for (int i = 0; i < 8; ++i) {
+      const float left = r[i] - __uint_as_float(__float_as_uint(r[i]) & 0xFFFF0000u);
+      r[i] = q == 0 && !__builtin_isfinite(r[i]) ? 0.f : left;
+    }
   }
 }
 
