@@ -48,13 +48,17 @@ __device__ inline float group_scale(uint32_t amax_bits) {
   return fmaxf(__uint_as_float(amax_bits << 16) / 2688.0f, kGscaleMin);
 }
 
-// fl32(x / d) for r = fl32(1 / d), both correctly rounded: one residual
+// fl32(x / d) held to +-6, for r = fl32(1 / d), both correctly rounded, and
+// lim = fl32(6 d). x is held before the division: where the scale is given,
+// x / d may pass the largest float32, and infinity would leave NaN. (What is
+// held at lim comes out within a step of 6 and is code 7 or 15.) One residual
 // correction of x * r (Markstein's method). Exact where the quotient matters:
 // d >= 2^-105 (g >= 2^-96, s >= 2^-9), so the residual of any quotient that
 // does not round to code 0 is a normal number.
-__device__ inline float quotient(float x, float d, float r) {
-  const float q0 = x * r;
-  return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q0, d, x), r, q0), x);
+__device__ inline float quotient(float x, float d, float r, float lim) {
+  const float v = __builtin_amdgcn_fmed3f(x, -lim, lim);
+  const float q0 = v * r;
+  return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q0, d, v), r, q0), x);
 }
 
 // part[g * parts + c] = the largest |x| (BF16 bits) of chunk c of group g
@@ -84,12 +88,11 @@ __device__ inline void quant8_nv(v4i t, float g, uint32_t* q, uint8_t* s, int64_
   const float f = fminf((__uint_as_float(m << 16) / 6.0f) / g, 448.0f);
   const uint32_t code = e4m3x4(f, 0.f, 0.f, 0.f) & 0xFFu;
   const float d = __builtin_amdgcn_cvt_f32_fp8((int)code, 0) * g;
-  const float r = d > 0.f ? 1.0f / d : 0.f;
+  const float r = d > 0.f ? 1.0f / d : 0.f, lim = 6.0f * d;
   uint32_t c = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float v0 = fminf(fmaxf(quotient(bf16_lo(w[k]), d, r), -6.0f), 6.0f);
-    const float v1 = fminf(fmaxf(quotient(bf16_hi(w[k]), d, r), -6.0f), 6.0f);
+    const float v0 = quotient(bf16_lo(w[k]), d, r, lim), v1 = quotient(bf16_hi(w[k]), d, r, lim);
     c |= (__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v0, v1, 1.0f, 0) & 0xFFu) << (8 * k);
   }
   q[i] = c;
