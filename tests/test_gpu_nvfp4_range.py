@@ -1,6 +1,7 @@
 """NVFP4 quantisation and the 4-bit products at the ends of the number range.
 
-* nvfp4_quantize with a given scale: values far beyond what the scale can hold saturate, with their sign.
+* nvfp4_quantize with a given scale: values far beyond what the scale can hold saturate, with their sign;
+  at the smallest scales quotients next to a border round as a division does.
 """
 import numpy as np
 import pytest
@@ -45,3 +46,29 @@ def test_given_scale_with_every_bf16_value(g):
     mixed = np.random.default_rng(3).permutation(x.reshape(-1)).reshape(x.shape)
     _matches(mixed, np.float32(g))
     _matches(synth.f32_to_bf16_bits(np.float32([[2.0 ** 42, -2.0 ** 42, 2.55e38, -2.55e38] * 4])), np.float32(g))
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_quotients_next_to_a_border_at_the_smallest_scales(given):
+    """Scales near the smallest: x / d within a float32 step of a border between two codes is rounded as a division does.
+
+    With d = 2^-104 (1 - 2^-24) and x = 2^-106, x / d is 0.25 (1 + 2^-24 + 2^-48): its float32 is above 0.25, so the code is
+    1 (0.5). What is left of x after the product of a first quotient with d needs bits below the smallest float32 there."""
+    g = np.float32(2.0 ** -95) * np.float32(1 - 2.0 ** -24)
+    rng = np.random.default_rng(6)
+    rows = []
+    for k in range(64):
+        # the block's maximum picks the scale byte (1 to some tens), its values the borders 0.25 .. 5 times d and near
+        top = np.float32(2.0 ** -102) * np.float32(2.0 ** (k % 6)) * np.float32(1 + rng.integers(0, 128) / 128)
+        near = np.float32(rng.choice([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 0.5, 3.0], 15) * 2.0 ** -104)
+        near = near * np.float32(2.0) ** rng.integers(0, 5, 15).astype(np.float32) * (1 + rng.integers(-1, 2, 15) / 128).astype(np.float32)
+        rows.append(np.concatenate([[top], near * rng.choice([-1, 1], 15)]))
+    rows.append(np.float32([2.0 ** -102] + [2.0 ** -106, -2.0 ** -106] * 7 + [2.0 ** -105]))
+    x = np.float32(rows).reshape(-1, 16)
+    if given:
+        _matches(synth.f32_to_bf16_bits(x), g)
+    else:
+        # the group's maximum makes the scale: amax / 2688 in the same binade as g
+        for amax in (2.0 ** -84, 2.0 ** -84 * (1 + 5 / 128), 2.0 ** -83 * (1 + 39 / 128), 2.0 ** -82 * (1 + 125 / 128)):
+            y = np.concatenate([np.float32([[amax] + [0] * 15]), x])
+            _matches(synth.f32_to_bf16_bits(y))

@@ -52,9 +52,12 @@ __device__ inline float group_scale(uint32_t amax_bits) {
 // lim = fl32(6 d). x is held before the division: where the scale is given,
 // x / d may pass the largest float32, and infinity would leave NaN. (What is
 // held at lim comes out within a step of 6 and is code 7 or 15.) One residual
-// correction of x * r (Markstein's method). Exact where the quotient matters:
-// d >= 2^-105 (g >= 2^-96, s >= 2^-9), so the residual of any quotient that
-// does not round to code 0 is a normal number.
+// correction of x * r (Markstein's method), exact where the residual x - q0 d is
+// a float32: its last bit is worth ulp(q0) ulp(d), 2^-49 d at least for a
+// quotient from 2^-3 on (a smaller one is code 0 either way), so d >= 2^-100.
+// g >= 2^-91 gives that, s being 2^-9 at least; below it a division is made.
+constexpr float kQuotientMinGscale = 0x1p-91f;
+
 __device__ inline float quotient(float x, float d, float r, float lim) {
   const float v = __builtin_amdgcn_fmed3f(x, -lim, lim);
   const float q0 = v * r;
@@ -92,7 +95,14 @@ __device__ inline void quant8_nv(v4i t, float g, uint32_t* q, uint8_t* s, int64_
   uint32_t c = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float v0 = quotient(bf16_lo(w[k]), d, r, lim), v1 = quotient(bf16_hi(w[k]), d, r, lim);
+    float v0 = bf16_lo(w[k]), v1 = bf16_hi(w[k]);
+    if (__builtin_expect(g >= kQuotientMinGscale, 1)) {
+      v0 = quotient(v0, d, r, lim);
+      v1 = quotient(v1, d, r, lim);
+    } else {
+      v0 = d > 0.f ? __builtin_amdgcn_fmed3f(v0, -lim, lim) / d : __builtin_copysignf(0.f, v0);
+      v1 = d > 0.f ? __builtin_amdgcn_fmed3f(v1, -lim, lim) / d : __builtin_copysignf(0.f, v1);
+    }
     c |= (__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v0, v1, 1.0f, 0) & 0xFFu) << (8 * k);
   }
   q[i] = c;
