@@ -551,8 +551,8 @@ size_t nvfp4_quantize_workspace_bytes(int64_t G, int64_t R, int64_t K);
  *   workspace  nvfp4_quantize_workspace_bytes bytes; may be NULL where
  *           gscale_given != 0
  *   With R = 0 nothing is written, gscale neither.
- *   K a positive multiple of 16, R * K at most 2^40; groups are cut into at
- *   most 1024 chunks of 4096 values or more, at most 2^31 - 1 in all.
+ *   K a positive multiple of 16; groups are cut into at most 1024 chunks of
+ *   4096 values or more, at most 2^24 - 1 in all; G * R * K at most 2^35 - 2048.
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, WORKSPACE, DEVICE,
  *         LAUNCH.
  */

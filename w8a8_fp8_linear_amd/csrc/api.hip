@@ -591,9 +591,10 @@ constexpr int64_t kNvBlock = 16;
 
 int check_nvfp4_shape(int64_t G, int64_t R, int64_t K) {
   if (G < 0 || R < 0 || K < 0 || !mul_ok(R, K) || !mul_ok(G, R * K) || !mul_ok(G * R * K, 4)) return W8A8_ERR_BAD_SHAPE;
-  if (K == 0 || K % kNvBlock != 0 || R * K > (int64_t(1) << 40)) return W8A8_ERR_UNSUPPORTED;
-  if (!mul_ok(G, w8a8::nvfp4_parts(R * K)) || G * w8a8::nvfp4_parts(R * K) > INT32_MAX ||
-      G * R * K / 2048 > INT32_MAX)
+  if (K == 0 || K % kNvBlock != 0) return W8A8_ERR_UNSUPPORTED;
+  // a grid holds less than 2^32 threads: 256 a chunk, and 256 for 2048 values on the way back
+  if (!mul_ok(G, w8a8::nvfp4_parts(R * K)) || G * w8a8::nvfp4_parts(R * K) >= int64_t(1) << 24 ||
+      G * R * K > (int64_t(1) << 35) - 2048)
     return W8A8_ERR_UNSUPPORTED;
   return W8A8_OK;
 }
