@@ -612,7 +612,8 @@ enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
  *   topk_ids [T, topk] int32; topk_w [T, topk] float32
  *   workspace  moe_router_workspace_bytes bytes (the logits)
  *   1 <= topk <= min(E, 64), E <= 1024, H a positive multiple of 8,
- *   E * H <= 2^29, H <= 2^20, T <= 2^24
+ *   E * H <= 2^29, H <= 2^20, T <= 2^24, fewer than 2^23 tiles of 16 tokens and
+ *   16 experts
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, WORKSPACE, DEVICE,
  *         LAUNCH.
  */

@@ -38,3 +38,17 @@ def test_nvfp4_values():
         assert _nvfp4(*shape)[0] > 0, shape
         if _no_gpu():
             assert _nvfp4(*shape)[1:] == (DEV, DEV), shape
+
+
+def test_router_workgroups():
+    """512 threads for 16 tokens and 16 experts: 2^23 such tiles are too many."""
+    def call(T, E, H=8):
+        n = w8.lib().moe_router_workspace_bytes(T, E)
+        return n, w8.lib().moe_router(P, P, None, P, P, T, H, E, 1, 0, 1, 1.0, P, max(n, T * E * 8), None)
+
+    for T, E in (1 << 23, 256), (1 << 21, 1024), ((1 << 21) - 15, 1009), (1 << 24, 113):
+        assert call(T, E) == (0, UNSUP), (T, E)
+    for T, E in ((1 << 23) - 16, 256), ((1 << 21) - 16, 1024), (1 << 24, 112):
+        assert call(T, E)[0] == T * E * 8
+        if _no_gpu():
+            assert call(T, E)[1] == DEV

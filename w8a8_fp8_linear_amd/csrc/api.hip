@@ -663,11 +663,15 @@ int mxfp4_gemm(const uint16_t* x_bf16, const uint8_t* w_q, const uint8_t* w_scal
 // ---- router and few-token experts ------------------------------------------------
 namespace {
 
+// Tiles of 16 tokens and 16 experts, 512 threads each: a grid holds less than 2^32.
+bool router_fits(int64_t T, int64_t E) { return ((T + 15) / 16) * ((E + 15) / 16) < int64_t(1) << 23; }
+
 int check_router_shape(int64_t T, int64_t H, int64_t E, int64_t topk, int score) {
   if (T < 0 || H < 0 || E < 0 || topk < 0 || !mul_ok(E, H) || !mul_ok(T, H) || !mul_ok(T * H, 2) || !mul_ok(T, topk))
     return W8A8_ERR_BAD_SHAPE;
   if (E < 1 || E > kMaxExperts || topk < 1 || topk > kMaxTopk || topk > E) return W8A8_ERR_UNSUPPORTED;
-  if (H == 0 || H % 8 != 0 || H > (int64_t(1) << 20) || E * H > (int64_t(1) << 29) || T > (int64_t(1) << 24))
+  if (H == 0 || H % 8 != 0 || H > (int64_t(1) << 20) || E * H > (int64_t(1) << 29) || T > (int64_t(1) << 24) ||
+      !router_fits(T, E))
     return W8A8_ERR_UNSUPPORTED;
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return W8A8_ERR_UNSUPPORTED;
   return W8A8_OK;
@@ -688,7 +692,7 @@ int check_few_shape(int format, int64_t T, int64_t H, int64_t I, int64_t E, int6
 extern "C" {
 
 size_t moe_router_workspace_bytes(int64_t T, int64_t E) {
-  if (T < 0 || E < 1 || E > kMaxExperts || T > (int64_t(1) << 24)) return 0;
+  if (T < 0 || E < 1 || E > kMaxExperts || T > (int64_t(1) << 24) || !router_fits(T, E)) return 0;
   return w8a8::router_workspace_bytes(T, E);
 }
 
