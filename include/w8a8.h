@@ -570,7 +570,9 @@ int nvfp4_dequantize(const uint8_t* q_fp4, const uint8_t* scale_e4m3, const floa
  * nvfp4_gemm, mxfp4_gemm — BF16 activations times 4-bit weights:
  *   nvfp4: y[m,n] = bf16( gscale * sum_k x[m,k] * dec(w_scale[n,k/16]) * dec(w_q[n,k]) )
  *   mxfp4: y[m,n] = bf16( sum_k x[m,k] * 2^(w_scale[n,k/32] - 127) * dec(w_q[n,k]) )
- * A code times its block scale is exact in BF16, products are exact in
+ * A code times its block scale is exact in BF16 (MXFP4: for scale bytes up to
+ * 252, the largest that mxfp4_quantize writes; from there on a value of 2^128 or
+ * more is infinite, as in float32, and 255 is NaN), products are exact in
  * float32, sums are float32, gscale is applied in float32 and the result is
  * rounded to nearest even. M <= 32 runs a weight-streaming kernel, larger M
  * tiles that grow with the work.
@@ -641,7 +643,7 @@ size_t moe_few_tokens_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E
  *   x_bf16 [T, H]; topk_ids, topk_w [T, topk]; ids outside [0, E) are dropped
  *   format    w13_q        w13_scale               w13_gscale
  *   MOE_FP8   [E, 2I, H]   float32 [E, 2I]         NULL
- *   MOE_MXFP4 [E, 2I, H/2] E8M0 [E, 2I, H/32]      NULL
+ *   MOE_MXFP4 [E, 2I, H/2] E8M0 [E, 2I, H/32]      NULL     (bytes as for mxfp4_gemm)
  *   MOE_NVFP4 [E, 2I, H/2] E4M3 [E, 2I, H/16]      float32 [E]
  *   w2_q [E, H, I] or [E, H, I/2] with scales likewise (along I)
  *   out_bf16 [T, H]

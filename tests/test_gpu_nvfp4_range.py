@@ -2,13 +2,14 @@
 
 * nvfp4_quantize with a given scale: values far beyond what the scale can hold saturate, with their sign;
   at the smallest scales quotients next to a border round as a division does.
+* mxfp4_gemm at the ends of the scale byte.
 """
 import numpy as np
 import pytest
 
 import oracle
 import synth
-from gpu_util import to_dev, to_dev_bf16
+from gpu_util import bf16_bits, to_dev, to_dev_bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +73,36 @@ def test_quotients_next_to_a_border_at_the_smallest_scales(given):
         for amax in (2.0 ** -84, 2.0 ** -84 * (1 + 5 / 128), 2.0 ** -83 * (1 + 39 / 128), 2.0 ** -82 * (1 + 125 / 128)):
             y = np.concatenate([np.float32([[amax] + [0] * 15]), x])
             _matches(synth.f32_to_bf16_bits(y))
+
+
+@pytest.mark.parametrize("M", [5, 20, 40, 700, 2100])
+def test_mxfp4_products_at_both_ends_of_the_scale(M):
+    """Every code under every scale byte that the format's quantiser writes (0 .. 252), one product a result: exact before the
+    last rounding, subnormal values among them."""
+    K, N = 32, 4112
+    codes = np.tile(np.arange(K) % 16, (N, 1)).astype(np.uint8)
+    q = (codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8)
+    s = (np.arange(N) % 253).astype(np.uint8)[:, None]
+    val = oracle.mx_dequant(q, s)
+    for at in (1.0, 2.0 ** 20, 2.0 ** -20):
+        x = np.zeros((M, K), np.float32)
+        x[np.arange(M), np.arange(M) % K] = at
+        y = oracle.bf16_bits_to_f64(bf16_bits(w8.mxfp4_gemm(to_dev_bf16(synth.f32_to_bf16_bits(x)), to_dev(q), to_dev(s))))
+        ref = oracle.bf16_bits_to_f64(oracle.round_to_bf16_bits(val.T[np.arange(M) % K] * at))
+        assert np.array_equal(y, ref)
+
+
+@pytest.mark.parametrize("M", [5, 40, 2100])
+def test_mxfp4_scale_bytes_beyond_the_range(M):
+    """253 and 254: a value of 2^128 or more is infinite, as in float32, the others are exact; 255 is NaN."""
+    K, N = 32, 4096
+    code, byte = np.arange(N) % 16, 253 + np.arange(N) // 16 % 3
+    q = np.repeat((code | (code << 4)).astype(np.uint8)[:, None], K // 2, 1)
+    x = np.full((M, K), 2.0 ** -20, np.float32)
+    y = oracle.bf16_bits_to_f64(bf16_bits(w8.mxfp4_gemm(to_dev_bf16(synth.f32_to_bf16_bits(x)), to_dev(q),
+                                                    to_dev(byte.astype(np.uint8)[:, None]))))
+    val = oracle.e2m1_decode(code) * np.exp2(byte - 127.0)
+    with np.errstate(invalid="ignore"):
+        val = np.where(np.abs(val) >= 2.0 ** 128, np.sign(val) * np.inf, val) * K * 2.0 ** -20
+    val[byte == 255] = np.nan
+    assert np.array_equal(y, np.tile(val, (M, 1)), equal_nan=True)

@@ -8,7 +8,9 @@
 //   FP8    dec(E4M3): 4 significant bits. The row's float32 scale stays in
 //          the epilogue.
 //   MXFP4  dec(E2M1) * 2^(e - 127): 2 significant bits, the block exponent
-//          applied by the conversion instruction itself.
+//          applied by the conversion instruction itself. Exact for e = 0 .. 252
+//          (2^-128 is a subnormal BF16; the quantiser writes no larger e); at
+//          253 and 254 a value of 2^128 or more is infinite, as in float32.
 //   NVFP4  dec(E2M1) * dec(E4M3 block scale): 2 + 4 = 6 significant bits at
 //          most, magnitudes 2^-10 .. 2688. The matrix's float32 scale stays
 //          in the epilogue.
