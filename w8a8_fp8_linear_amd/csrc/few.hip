@@ -794,21 +794,23 @@ __device__ inline void codes_f32(v4i w, float scale, float* f) {
 }
 
 // At most 8 tokens and 64 slots: 8 output columns a workgroup, so that a narrow
-// output still fills the GPU. A wave takes every 16th expert, in the order of
-// their first slots; lane s holds slot s's id and weight, so a ballot finds the
-// expert's tokens. Lane (r16, g) works on row r16 % 8 in half r16 / 8 of K and
-// loads 16 code bytes a step; the h rows of the expert's tokens go to LDS by
-// direct loads, 512 values of two tokens at a time, and a token's dot product is
-// float32 FMAs: h keeps its 24 bits, a token that did not pick the expert is not
-// touched, and most experts of so few tokens have one or two, where an MFMA
-// would fill 8 columns. 8 tokens of 64 nvfp4 experts, 2048 x 512: 11.7 us (8 waves:
-// 14.0 us), 1 token 4.7 us; one token's 4 fp8 experts, 1024 x 512: 3.9 us. A wave's
-// experts are a chain of load latencies: with 42 picked experts, three each.
-template <int F>
-__global__ __launch_bounds__(1024) void few_down_small(const FewArgs p) {
+// output still fills the GPU. The picked experts, in the order of their first
+// slots, times their rounds of 512 inputs are dealt to the waves in turn; lane s
+// holds slot s's id and weight, so a ballot finds the expert's tokens. Lane
+// (r16, g) works on row r16 % 8 in half r16 / 8 of K and loads 16 code bytes a
+// step; the h rows of the expert's tokens go to LDS by direct loads, four tokens
+// at a time, and a token's dot product is float32 FMAs: h keeps its 24 bits, a
+// token that did not pick the expert is not touched, and most experts of so few
+// tokens have one or two, where an MFMA would fill 8 columns. 8 tokens of 64
+// nvfp4 experts, 2048 x 512: 11.9 us for 25 MB, the vector units busy 51% of the
+// time and a wave waiting 49% of its own; one token's 4 fp8 experts, 1024 x 512:
+// 4.0 us. Registers are held to 128 for four waves a SIMD; a spill costs 3 us.
+template <int F, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(4, 4)))
+void few_down_small(const FewArgs p) {
   using W = WideFmt<F>;
-  constexpr int WAVES = 16, R = 8, TOK = 8;
-  constexpr int B = 2;                       // tokens staged together
+  constexpr int R = 8, TOK = 8;
+  constexpr int B = 4;                       // tokens staged together
   constexpr int U = F == kFmtFp8 ? 4 : 2;    // steps of a round
   constexpr int kHalf = U * W::kStepK;       // inputs of a round in one half of K
   static_assert(2 * kHalf == 512, "a token's h of a round is two loads of a wave");
@@ -816,7 +818,7 @@ __global__ __launch_bounds__(1024) void few_down_small(const FewArgs p) {
   __shared__ uint32_t first[kFewMaxE];             // the first slot of every expert
   __shared__ __attribute__((aligned(1024))) float hbuf[WAVES][B][512];
   __shared__ __attribute__((aligned(16))) uint8_t slds[WAVES][S::kLds];
-  __shared__ float red[WAVES][TOK][72], sums[WAVES][TOK * R];
+  __shared__ float sums[WAVES][TOK * R];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4, row = r16 % R, half = r16 / R;
@@ -834,124 +836,124 @@ __global__ __launch_bounds__(1024) void few_down_small(const FewArgs p) {
   const int64_t rb = W::row_bytes(p.I), rs = W::row_scales(p.I);
   const int steps = ((p.I + W::kStepK - 1) / W::kStepK + 1) / 2;  // of one half
   const int kbase = half * steps * W::kStepK;
+  const int rounds = (steps + U - 1) / U;
   const auto rX = make_rsrc(p.h, (int64_t)slots * p.I * 4);
   const uint64_t kmask = p.k == 64 ? ~0ull : (1ull << p.k) - 1;
   float y[TOK];
 #pragma unroll
   for (int t = 0; t < TOK; ++t) y[t] = 0.f;
-  for (int i = 0; i < wave; ++i) leaders &= leaders - 1;
-  while (leaders) {
+  int round = wave;  // of the first of the experts that are left
+  while (true) {
+    for (; leaders && round >= rounds; round -= rounds) leaders &= leaders - 1;
+    if (!leaders) break;
     const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(leaders));
     const uint64_t same = __ballot(id == e);
-    for (int i = 0; i < WAVES; ++i) leaders &= leaders - 1;
     const auto rW = make_rsrc(p.w2 + ((int64_t)e * p.H + row0) * rb, R * rb);
     uint32_t skew;
     const auto rS = scale_rsrc(static_cast<const uint8_t*>(p.s2) + ((int64_t)e * p.H + row0) * rs, R * rs, &skew);
     float scale = 1.f;
     if constexpr (F == kFmtFp8) scale = static_cast<const float*>(p.s2)[(int64_t)e * p.H + row0 + row];
     if constexpr (F == kFmtNvfp4) scale = p.g2[e];
-    for (int kt = 0; kt < steps; kt += U) {
-      const int k0 = kbase + kt * W::kStepK;
-      v4i w[U];
-      S sc;
-      sc.load(rS, [&](int) { return k0 < p.I ? skew + (uint32_t)(row * rs) + (uint32_t)(k0 / W::kBlock) : kOutOfRange; });
+    const int kt = round * U;
+    round += WAVES;
+    const int k0 = kbase + kt * W::kStepK;
+    v4i w[U];
+    S sc;
+    sc.load(rS, [&](int) { return k0 < p.I ? skew + (uint32_t)(row * rs) + (uint32_t)(k0 / W::kBlock) : kOutOfRange; });
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * W::kStepK + W::kLaneK * g;
-        w[u] = buffer_load16(rW, kt + u < steps && k < p.I ? (uint32_t)(row * rb) + (uint32_t)W::row_bytes(k) : kOutOfRange);
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * W::kStepK + W::kLaneK * g;
+      w[u] = buffer_load16(rW, kt + u < steps && k < p.I ? (uint32_t)(row * rb) + (uint32_t)W::row_bytes(k) : kOutOfRange);
+    }
+    uint32_t hk[2];  // bytes into an h row of the 4 values that this lane brings to LDS for each half
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = 4 * lane;
+      const int k = (i * steps + kt) * W::kStepK + at;
+      hk[i] = kt + at / W::kStepK < steps && k < p.I ? (uint32_t)k * 4u : kOutOfRange;
+    }
+    float f[U][W::kLaneK], s[U][2];
+    uint64_t rest = same;  // the slots of the tokens that are still to come
+    auto stage = [&]() {   // the next B tokens' h
+      uint64_t left = rest;
+      int n = 0;
+      for (; left && n < B; ++n) {
+        const int slot = __builtin_ctzll(left);
+        left &= ~(kmask << (__builtin_amdgcn_readlane(slot_tok, slot) * p.k));
+        const uint32_t at = (uint32_t)slot * (uint32_t)p.I * 4u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          buffer_load16_lds(rX, &hbuf[wave][n][256 * i], hk[i] == kOutOfRange ? kOutOfRange : at + hk[i]);
       }
-      uint32_t hk[2];  // bytes into an h row of the 4 values that this lane brings to LDS for each half
+      wait_vmem_all();
+      wave_lds_order();
+      return n;
+    };
+    int n = stage();
+    sc.spread(slds[wave], (p.I - k0) / W::kBlock);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = 4 * lane;
-        const int k = (i * steps + kt) * W::kStepK + at;
-        hk[i] = kt + at / W::kStepK < steps && k < p.I ? (uint32_t)k * 4u : kOutOfRange;
+    for (int u = 0; u < U; ++u) {
+      const uint32_t code = S::get(slds[wave], u, 0);
+      codes_f32<F>(w[u], F == kFmtMxfp4 ? mx_scale_value(code) : 1.0f, f[u]);
+      if constexpr (F == kFmtNvfp4) {
+        const auto two = __builtin_amdgcn_cvt_pk_f32_fp8((int)code, false);
+        s[u][0] = two[0], s[u][1] = two[1];
       }
-      float f[U][W::kLaneK], s[U][2];
-      uint64_t rest = same;  // slots of the tokens that are still to come
-      bool begun = false;
-      do {  // B tokens
-        int tok[B], slot[B];
-        float weight[B];
+    }
+    while (true) {
+#pragma nounroll
+      for (int b = 0; b < n; ++b) {
+        const int tok = __builtin_amdgcn_readlane(slot_tok, __builtin_ctzll(rest));
+        const uint64_t all = kmask << (tok * p.k);
+        float weight = 0.f;
+        for (uint64_t m = rest & all; m; m &= m - 1)
+          weight += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(tw), __builtin_ctzll(m)));
+        rest &= ~all;
+        const float* h = &hbuf[wave][b][half * kHalf + W::kLaneK * g];
+        float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-          tok[b] = -1, slot[b] = 0, weight[b] = 0.f;
-          if (rest) {
-            slot[b] = __builtin_ctzll(rest);
-            tok[b] = __builtin_amdgcn_readlane(slot_tok, slot[b]);
-            const uint64_t all = kmask << (tok[b] * p.k);
-            for (uint64_t m = rest & all; m; m &= m - 1)
-              weight[b] += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(tw), __builtin_ctzll(m)));
-            rest &= ~all;
-          }
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): what the batch before reads has arrived
-        wave_lds_order();
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-          if (tok[b] < 0) break;
-          const uint32_t at = (uint32_t)slot[b] * (uint32_t)p.I * 4u;
+          for (int c0 = 0; c0 < W::kLaneK; c0 += 16) {  // 16 values: a block of NVFP4
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            buffer_load16_lds(rX, &hbuf[wave][b][256 * i], hk[i] == kOutOfRange ? kOutOfRange : at + hk[i]);
-        }
-        wait_vmem_all();
-        wave_lds_order();
-        if (!begun) {
-          begun = true;
-          sc.spread(slds[wave], (p.I - k0) / W::kBlock);
+            for (int c = c0; c < c0 + 16; c += 4) {
+              const v4f x = *reinterpret_cast<const v4f*>(h + u * W::kStepK + c);
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const uint32_t code = S::get(slds[wave], u, 0);
-            codes_f32<F>(w[u], F == kFmtMxfp4 ? mx_scale_value(code) : 1.0f, f[u]);
+              for (int i = 0; i < 4; ++i) {
+                if constexpr (F == kFmtNvfp4)
+                  d[i] = __builtin_fmaf(f[u][c + i], x[i], d[i]);
+                else
+                  a[i] = __builtin_fmaf(f[u][c + i], x[i], a[i]);
+              }
+            }
             if constexpr (F == kFmtNvfp4) {
-              const auto two = __builtin_amdgcn_cvt_pk_f32_fp8((int)code, false);
-              s[u][0] = two[0], s[u][1] = two[1];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(d[i], s[u][c0 / 16], a[i]);
             }
           }
         }
+        const float add = ((a[0] + a[1]) + (a[2] + a[3])) * scale * weight;
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-          if (tok[b] < 0) break;
-          const float* h = &hbuf[wave][b][half * kHalf + W::kLaneK * g];
-          float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int c0 = 0; c0 < W::kLaneK; c0 += 16) {  // 16 values: a block of NVFP4
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int c = c0; c < c0 + 16; c += 4) {
-                const v4f x = *reinterpret_cast<const v4f*>(h + u * W::kStepK + c);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  if constexpr (F == kFmtNvfp4)
-                    d[i] = __builtin_fmaf(f[u][c + i], x[i], d[i]);
-                  else
-                    a[i] = __builtin_fmaf(f[u][c + i], x[i], a[i]);
-                }
-              }
-              if constexpr (F == kFmtNvfp4) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(d[i], s[u][c0 / 16], a[i]);
-              }
-            }
-          }
-          const float add = ((a[0] + a[1]) + (a[2] + a[3])) * scale * weight[b];
-#pragma unroll
-          for (int t = 0; t < TOK; ++t) y[t] = tok[b] == t ? y[t] + add : y[t];
-        }
-      } while (rest);
+        for (int t = 0; t < TOK; ++t) y[t] = tok == t ? y[t] + add : y[t];
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): what the tokens were read from is free
+      wave_lds_order();
+      if (!rest) break;
+      n = stage();
     }
   }
-  // the sum over the lanes that have the same row, then over the waves
+  // the sum over the lanes that have the same row, in the place of the wave's h,
+  // then over the waves
+  float* const red = hbuf[wave][0];
+  wave_lds_order();
 #pragma unroll
-  for (int t = 0; t < TOK; ++t) red[wave][t][lane] = y[t];
+  for (int t = 0; t < TOK; ++t) red[t * 72 + lane] = y[t];
   wave_lds_order();
   if (lane < TOK * R) {
     float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 64 / R; ++i) v += red[wave][lane / R][i * R + lane % R];
+    for (int i = 0; i < 64 / R; ++i) v += red[lane / R * 72 + i * R + lane % R];
     sums[wave][lane] = v;
   }
   __syncthreads();
@@ -1031,7 +1033,13 @@ hipError_t launch_few_fmt(const FewArgs& a, const RouterArgs* route, hipStream_t
   hipError_t e = launch_rows<F, false>(a, route, stream);
   if (e != hipSuccess) return e;
   if (few_small(a.T, a.k)) {
-    hipLaunchKernelGGL(few_down_small<F>, dim3(a.H / 8), dim3(1024), 0, stream, a);
+    // 16 waves a workgroup while each has a CU (whole layers, fp8: 8 tokens of 16
+    // experts, 1024 x 2048, 27.8 us against 29.3 us with 8), two workgroups of 8 on a
+    // CU for wider outputs (8192 x 512: 61.7 us against 68.5 us)
+    if (a.H <= 8 * 256)
+      hipLaunchKernelGGL((few_down_small<F, 16>), dim3(a.H / 8), dim3(64 * 16), 0, stream, a);
+    else
+      hipLaunchKernelGGL((few_down_small<F, 8>), dim3(a.H / 8), dim3(64 * 8), 0, stream, a);
     return hipGetLastError();
   }
   e = launch_rows<F, true>(a, nullptr, stream);
