@@ -643,7 +643,7 @@ size_t moe_few_tokens_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E
  *   x_bf16 [T, H]; topk_ids, topk_w [T, topk]; ids outside [0, E) are dropped
  *   format    w13_q        w13_scale               w13_gscale
  *   MOE_FP8   [E, 2I, H]   float32 [E, 2I]         NULL
- *   MOE_MXFP4 [E, 2I, H/2] E8M0 [E, 2I, H/32]      NULL     (bytes as for mxfp4_gemm)
+ *   MOE_MXFP4 [E, 2I, H/2] E8M0 [E, 2I, H/32]      NULL     (bytes up to 252)
  *   MOE_NVFP4 [E, 2I, H/2] E4M3 [E, 2I, H/16]      float32 [E]
  *   w2_q [E, H, I] or [E, H, I/2] with scales likewise (along I)
  *   out_bf16 [T, H]

@@ -316,7 +316,7 @@ struct FewArgs {
   const void* s2;
   const float* g2;
   float* h;               // [T * k, I]: every routed copy's h
-  float* y;               // [T * k, H]: weighted float32 rows (few_down_rows)
+  float* y;               // [T * k, H]: weighted float32 rows of the larger steps
   uint16_t* out;          // [T, H]
   int T, H, I, E, k, by_slot;
 };
@@ -440,8 +440,8 @@ __device__ inline void split3(const float (&h)[8], v4i (&part)[3]) {
 //
 // FP8, 64 tokens of 64 experts, 2048 x 512: gate/up 134 MB in 30 us (4.5
 // TB/s), down 67 MB in 22 us (nvfp4 21 us), of which the third part of h is 1.2
-// us and taking h apart another. 8 tokens, nvfp4: gate/up about 50 MB in 17.5 us, of which some 4 us
-// are the start (ids, then inputs and weights).
+// us and taking h apart 1 us. 8 tokens, nvfp4: gate/up about 50 MB in 17.5 us, of
+// which some 4 us are the start (ids, then inputs and weights).
 //
 // ROUTE (at most kFewWaves tokens, few workgroups): the choice is made here
 // from the logits, a wave per token, by every workgroup for itself, and

@@ -1,5 +1,5 @@
 // Weights of the default maths widened to BF16 in registers, and the
-// weight-streaming dot product that the few-token kernels share.
+// weight-streaming dot product that the products of few rows share.
 //
 // Without the fast-math flag the pages' runtime widens the 8-bit and 4-bit
 // weights to 16 bits as it multiplies (Lernex/Metis-1.6-Logos-FP8, "What
