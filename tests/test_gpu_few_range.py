@@ -71,7 +71,7 @@ def _set(fmt, w, e, row, k, negative=False):
         w[0][e, row, k // 2] |= (0xA if negative else 0x2) << (4 * (k % 2))
 
 
-# tokens that take: the small down projection (4 and 8 columns), the grouped one by copies and by experts with one
+# tokens that take: the small down projection, the grouped one by copies and by experts with one
 # column tile, and with several
 _STEPS = [(1, 5), (5, 40), (12, 60), (14, 3), (40, 2)]
 
