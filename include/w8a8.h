@@ -624,6 +624,54 @@ int moe_router(const uint16_t* x_bf16, const uint16_t* w_router, const float* bi
                int64_t T, int64_t H, int64_t E, int64_t topk, int score, int renormalize, float route_scale,
                void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * moe_router_with_logits — moe_router, and the logits rounded to float32 in
+ * logits_f32 [T, E]: what moe_balance_loss takes. The choice and the weights
+ * are moe_router's, bit for bit.
+ */
+int moe_router_with_logits(const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int32_t* topk_ids,
+                           float* topk_w, float* logits_f32, int64_t T, int64_t H, int64_t E, int64_t topk, int score,
+                           int renormalize, float route_scale, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/* Types of moe_balance_loss's logits. */
+enum { MOE_LOGITS_F32 = 0, MOE_LOGITS_BF16 = 1 };
+
+/*
+ * moe_balance_loss — how evenly a router's choice loads the experts, per
+ * sequence, and the gradient that evens it out: what a router is trained (or,
+ * beside experts that stay as they are, trained on) with to keep the balance
+ * that its bias otherwise has to (Lernex/Metis-1.6-Praxis, "Architecture").
+ * T tokens in S sequences of T / S; ids outside [0, E) are dropped, and a token
+ * without a valid id (the place behind a sequence's end) does not count: its
+ * logits are not used and its gradient is zero. With n[s] the tokens of a
+ * sequence that count:
+ *   counts[s,e] = routed copies of the sequence's tokens that name e
+ *   p[t,e]      = softmax over e of the logits, or sigmoid / sum of sigmoids
+ *                 (all zero where that is 0 / 0: every logit -infinity)
+ *   loss        = coef / S * sum_s sum_e E counts[s,e] / (topk n[s]) * mean_t p[t,e]
+ *   grad_logits = d loss / d logits, the counts held constant
+ * A sequence without a token that counts adds nothing. A logit of -infinity
+ * bars its expert (p = 0); +infinity and NaN in a token that counts are
+ * outside the contract. Scores are float32, the loss is summed in float64 in a
+ * fixed order (the same bits every call), and rounded once. coef may carry a
+ * loss scale.
+ *   logits       [T, E] float32 or BF16 (logits_dtype)
+ *   topk_ids     [T, topk] int32
+ *   loss         [1] float32, 4-byte aligned     counts [S, E] int32
+ *   grad_logits  [T, E] of the logits' type, or NULL: not wanted
+ *   workspace    moe_balance_loss_workspace_bytes bytes; calls that may
+ *                overlap need one each
+ *   E <= 1024, topk <= 64, T <= 2^24, 1 <= S <= 2^20 dividing T. T == 0 gives a
+ *   loss and counts of zero.
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED (also another type or score),
+ *         MISALIGNED, WORKSPACE, DEVICE, LAUNCH.
+ */
+size_t moe_balance_loss_workspace_bytes(int64_t T, int64_t S, int64_t E);
+int moe_balance_loss(int logits_dtype, const void* logits, const int32_t* topk_ids, int64_t T, int64_t S, int64_t E,
+                     int64_t topk, int score, float coef, float* loss, int32_t* counts, void* grad_logits,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Weight formats of the few-token calls. */
 enum { MOE_FP8 = 0, MOE_MXFP4 = 1, MOE_NVFP4 = 2 };
 
@@ -669,6 +717,94 @@ int moe_few_tokens_layer(int format, const uint16_t* x_bf16, const uint16_t* w_r
                          const void* w13_scale, const float* w13_gscale, const uint8_t* w2_q, const void* w2_scale,
                          const float* w2_gscale, uint16_t* out_bf16, int64_t T, int64_t H, int64_t I, int64_t E,
                          int64_t topk, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * FP8 with a scale per block of 128
+ *
+ * The fast-math scheme (a layer's input rounded to FP8 at run time, FP8
+ * weights, products on the FP8 matrix units: Lernex/Metis-1.6-Logos-FP8, "What
+ * --fast-math does") with finer scales than a row's: one per 128 consecutive
+ * values of a row of activations, one per 128 x 128 values of a weight matrix.
+ * Blocks are counted from index 0; the last of a dimension may be shorter.
+ *   activations  codes [M, K], scales [ceil(K/128), M]: the scales of one block
+ *                of K for all rows are contiguous
+ *   weights      codes [N, K], scales [ceil(N/128), ceil(K/128)], stacked [E, ..]
+ *                for experts
+ * A value is dec(code) * scale.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * quantize_blocks — BF16 rows -> E4M3 codes and one scale per 128 values:
+ * quantize_per_token's rule on every block by itself,
+ *   scale = fl32(amax / 448), 1 for an all-zero block; q = E4M3(fl32(x / scale))
+ * quantize_weight_blocks — the same on 128 x 128 blocks of E matrices.
+ * Both are bit-exact and deterministic.
+ *   x_bf16 [M, K]    q_e4m3 [M, K]    scale [ceil(K/128), M]
+ *   w_bf16 [E, N, K] q_e4m3 [E, N, K] scale [E, ceil(N/128), ceil(K/128)]
+ *   K a positive multiple of 16; rows: K <= 2^24, M <= 2^26, fewer than 2^24
+ *   pieces of 16 rows x 512 values; weights: E, N, K <= 2^20, fewer than 2^24 blocks
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, DEVICE, LAUNCH.
+ */
+int quantize_blocks(const uint16_t* x_bf16, int64_t M, int64_t K, uint8_t* q_e4m3, float* scale, hipStream_t stream);
+int quantize_weight_blocks(const uint16_t* w_bf16, int64_t E, int64_t N, int64_t K, uint8_t* q_e4m3, float* scale,
+                           hipStream_t stream);
+
+/*
+ * w8a8_block_gemm — the product of block-scaled operands:
+ *   y[m,n] = bf16( sum_b a_scale[b,m] * w_scale[n/128,b] * sum_{k in block b} dec(a[m,k]) * dec(w[n,k]) )
+ * Products are exact, a block's sum is the FP8 matrix unit's, the product of
+ * two scales is rounded to float32, blocks are added in float32 and the result
+ * is rounded to nearest even. M <= 32 runs a weight-streaming kernel, larger M
+ * tiles that grow with the work.
+ *   a_q [M, K]  a_scale [ceil(K/128), M]  w_q [N, K]  w_scale [ceil(N/128), ceil(K/128)]
+ *   y_bf16 [M, N] (must not overlap the inputs)
+ *   K and N positive multiples of 16, K, N <= 2^20, M <= 2^24, fewer than 2^23
+ *   tiles of 64 x 64 outputs
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, DEVICE, LAUNCH.
+ */
+int w8a8_block_gemm(const uint8_t* a_q, const float* a_scale, const uint8_t* w_q, const float* w_scale,
+                    uint16_t* y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/*
+ * w8a8_block_linear — the layer on BF16 input: quantize_blocks, then
+ * w8a8_block_gemm. Up to 32 rows it is one launch that quantises the input
+ * inside the product and needs no workspace; the result is the same bits.
+ *   x_bf16 [M, K]; workspace w8a8_block_linear_workspace_bytes(M, K) bytes (0 up
+ *   to 32 rows, and for sizes it does not take); other arguments, limits and
+ *   errors as w8a8_block_gemm and quantize_blocks, plus WORKSPACE.
+ */
+size_t w8a8_block_linear_workspace_bytes(int64_t M, int64_t K);
+int w8a8_block_linear(const uint16_t* x_bf16, const uint8_t* w_q, const float* w_scale, uint16_t* y_bf16, int64_t M,
+                      int64_t N, int64_t K, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_w8a8_block_grouped — one routed-expert pass on block-scaled tokens and
+ * weights, the chain of moe_w8a8_grouped with its conventions for ids, slots
+ * and the sum over a token's copies:
+ *   g, u   = gate and up halves of W13[e] . x[t]     (float32, as w8a8_block_gemm)
+ *   h      = silu(g) * u                             (float32)
+ *   h_q    = E4M3 of h with one scale per 128 of its I values (quantize_blocks' rule)
+ *   out[t] = bf16( sum over j with a valid id, in order, of topk_w[t,j] * (W2[e] . h) )
+ * A token without a valid id gets zeros.
+ *   x_q [T, H]  x_scale [ceil(H/128), T]
+ *   w13_q [E, 2I, H] (rows 0..I-1 gate, I..2I-1 up)  w13_scale [E, 2I/128, ceil(H/128)]
+ *   w2_q [E, H, I]  w2_scale [E, ceil(H/128), I/128]
+ *   out_bf16 [T, H]
+ *   out_q [T, H], out_scale [ceil(H/128), T]  optional (both NULL or both set):
+ *             also quantize_blocks(out_bf16), bit for bit, fused into the sum:
+ *             the next pass's input
+ *   workspace  moe_w8a8_block_workspace_bytes bytes; calls that may overlap
+ *              need one each
+ *   Limits as moe_w8a8_grouped (H a multiple of 16, I of 128), and fewer than
+ *   2^22 tiles of 64 copies x 128 columns.
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, WORKSPACE, DEVICE,
+ *         LAUNCH.
+ */
+size_t moe_w8a8_block_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
+int moe_w8a8_block_grouped(const uint8_t* x_q, const float* x_scale, const int32_t* topk_ids, const float* topk_w,
+                           const uint8_t* w13_q, const float* w13_scale, const uint8_t* w2_q, const float* w2_scale,
+                           uint16_t* out_bf16, uint8_t* out_q, float* out_scale, int64_t T, int64_t H, int64_t I,
+                           int64_t E, int64_t topk, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

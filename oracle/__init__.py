@@ -31,6 +31,8 @@ What it defines, and where the pages state it:
   product of BF16 activations with 4-bit weights (same page).
 * The router and the default-maths routed-expert pass of a step with few
   tokens (``few``).
+* FP8 with a scale per block of 128, its product and expert pass, and the
+  router's balance loss (``block``).
 * The routed-expert chain (``moe``): routed experts in FP8 with the same
   scheme, top-k routing, the stack run twice with shared weights
   (Lernex/Metis-1.6-Praxis, "Architecture"; sglang-metis 0.1.0, "How the
@@ -52,6 +54,8 @@ from .mxfp4 import (e2m1_decode, e2m1_encode, e8m0_value, mx_dequant, mx_quantiz
                     moe_mxfp4_pass, moe_mxfp4_two_pass)
 from .nvfp4 import NVFP4_GSCALE_MIN, nvfp4_quantize, nvfp4_scaled, nvfp4_dequant_f32, w4a16_linear
 from .few import router, wide_pass
+from .block import (BLOCK, quantize_row_blocks, quantize_weight_blocks, row_values, weight_values, block_linear,
+                    moe_block_pass, balance_loss)
 
 __all__ = [
     "E4M3_MAX", "decode", "decode_table", "encode", "encode_bits", "finite_codes", "magnitudes",
@@ -60,4 +64,6 @@ __all__ = [
     "swiglu_f32", "bf16_values", "combine_copies", "e2m1_decode", "e2m1_encode", "e8m0_value", "mx_dequant", "mx_quantize_rows", "mx_unpack",
     "mxfp4_linear", "moe_mxfp4_pass", "moe_mxfp4_two_pass", "NVFP4_GSCALE_MIN", "nvfp4_quantize", "nvfp4_scaled",
     "nvfp4_dequant_f32", "w4a16_linear", "router", "wide_pass",
+    "BLOCK", "quantize_row_blocks", "quantize_weight_blocks", "row_values", "weight_values", "block_linear",
+    "moe_block_pass", "balance_loss",
 ]

@@ -22,6 +22,8 @@ __all__ = [
     "w8a8_grouped_gemm", "moe_w8a8_grouped", "moe_workspace", "moe_ffn",
     "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_gemm", "mxfp4_gemm",
     "moe_router", "moe_few_tokens", "moe_few_tokens_layer", "moe_few_tokens_workspace", "moe_few_tokens_ffn",
+    "quantize_blocks", "quantize_weight_blocks", "w8a8_block_gemm", "w8a8_block_linear",
+    "moe_w8a8_block_grouped", "moe_w8a8_block_workspace", "moe_block_ffn", "moe_balance_loss",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -85,6 +87,18 @@ _SIGNATURES = {
     "moe_few_tokens_layer": (ctypes.c_int, [ctypes.c_int] + [_c_ptr] * 3 + [ctypes.c_int, ctypes.c_int,
                                                                            ctypes.c_float]
                              + [_c_ptr] * 9 + [_c_i64] * 5 + [_c_ptr, ctypes.c_size_t, _c_ptr]),
+    "moe_router_with_logits": (ctypes.c_int, [_c_ptr] * 6 + [_c_i64] * 4 + [ctypes.c_int, ctypes.c_int, ctypes.c_float,
+                                                                           _c_ptr, ctypes.c_size_t, _c_ptr]),
+    "moe_balance_loss_workspace_bytes": (ctypes.c_size_t, [_c_i64] * 3),
+    "moe_balance_loss": (ctypes.c_int, [ctypes.c_int] + [_c_ptr] * 2 + [_c_i64] * 4 + [ctypes.c_int, ctypes.c_float]
+                         + [_c_ptr] * 4 + [ctypes.c_size_t, _c_ptr]),
+    "quantize_blocks": (ctypes.c_int, [_c_ptr, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr]),
+    "quantize_weight_blocks": (ctypes.c_int, [_c_ptr, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr]),
+    "w8a8_block_gemm": (ctypes.c_int, [_c_ptr] * 5 + [_c_i64] * 3 + [_c_ptr]),
+    "w8a8_block_linear_workspace_bytes": (ctypes.c_size_t, [_c_i64] * 2),
+    "w8a8_block_linear": (ctypes.c_int, [_c_ptr] * 4 + [_c_i64] * 3 + [_c_ptr, ctypes.c_size_t, _c_ptr]),
+    "moe_w8a8_block_workspace_bytes": (ctypes.c_size_t, [_c_i64] * 5),
+    "moe_w8a8_block_grouped": (ctypes.c_int, [_c_ptr] * 11 + [_c_i64] * 5 + [_c_ptr, ctypes.c_size_t, _c_ptr]),
 }
 
 
@@ -939,13 +953,14 @@ _FP8, _MXFP4, _NVFP4 = 0, 1, 2
 
 
 def moe_router(x, w_router, topk: int, bias=None, score="softmax", renormalize=True, route_scale=1.0, ids=None,
-               weights=None, workspace=None):
+               weights=None, workspace=None, logits=None):
     """The experts of every token: (ids int32 [T, topk], weights float32 [T, topk]).
 
     The score is softmax or sigmoid of x . w_router^T (float64 sums); the
     choice goes by score + bias, larger first, the lower id where they are
     equal; the weights are the scores of the chosen, renormalised to sum to
-    one if asked, times ``route_scale``."""
+    one if asked, times ``route_scale``. ``logits`` (float32 [T, E]), where
+    given, gets the logits, for ``moe_balance_loss``."""
     import torch
 
     T, H = x.shape
@@ -956,11 +971,17 @@ def moe_router(x, w_router, topk: int, bias=None, score="softmax", renormalize=T
         weights = torch.empty((T, topk), dtype=torch.float32, device=x.device)
     dev = _same_device(x, (x, torch.bfloat16, (T, H), "x"), (w_router, torch.bfloat16, (E, H), "w_router"),
                        (ids, torch.int32, (T, topk), "ids"), (weights, torch.float32, (T, topk), "weights"),
-                       *(((bias, torch.float32, (E,), "bias"),) if bias is not None else ()))
+                       *(((bias, torch.float32, (E,), "bias"),) if bias is not None else ()),
+                       *(((logits, torch.float32, (T, E), "logits"),) if logits is not None else ()))
     if score not in _SCORES:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
     if workspace is None:
         workspace = torch.empty(max(T * E * 8, 16), dtype=torch.uint8, device=x.device)
+    if logits is not None:
+        _call(dev, "moe_router_with_logits", x.data_ptr(), w_router.data_ptr(),
+              bias.data_ptr() if bias is not None else None, ids.data_ptr(), weights.data_ptr(), logits.data_ptr(), T, H,
+              E, topk, _SCORES[score], int(renormalize), route_scale, *_workspace_args(workspace, dev))
+        return ids, weights
     _call(dev, "moe_router", x.data_ptr(), w_router.data_ptr(), bias.data_ptr() if bias is not None else None,
           ids.data_ptr(), weights.data_ptr(), T, H, E, topk, _SCORES[score], int(renormalize), route_scale,
           *_workspace_args(workspace, dev))
@@ -1069,3 +1090,192 @@ def moe_few_tokens_ffn(x, routers, w13, w2, topk: int, score="softmax", renormal
                                          route_scale=route_scale, workspace=workspace))
         x = outs[-1][0]
     return outs
+
+
+# ---- FP8 with a scale per block of 128 ------------------------------------------
+#
+# Activations: codes [M, K] uint8, scales [ceil(K/128), M] f32 (the scales of one
+# block of K for all rows are contiguous). Weights: codes [N, K], scales
+# [ceil(N/128), ceil(K/128)], both with a leading [E] for experts.
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def quantize_blocks(x, q=None, scale=None):
+    """BF16 [M, K] -> (E4M3 codes uint8 [M, K], float32 scales [ceil(K/128), M]):
+    quantize_per_token's rule on every 128 values of a row by themselves."""
+    import torch
+
+    M, K = x.shape
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty((_blocks(K), M), dtype=torch.float32, device=x.device)
+    dev = _same_device(x, (x, torch.bfloat16, (M, K), "x"), (q, torch.uint8, (M, K), "q"),
+                       (scale, torch.float32, (_blocks(K), M), "scale"))
+    _call(dev, "quantize_blocks", x.data_ptr(), M, K, q.data_ptr(), scale.data_ptr())
+    return q, scale
+
+
+def quantize_weight_blocks(w, q=None, scale=None):
+    """BF16 [N, K] or [E, N, K] -> (E4M3 codes of the same shape, float32 scales
+    [(E,) ceil(N/128), ceil(K/128)]): one scale per 128 x 128 block."""
+    import torch
+
+    if w.dim() not in (2, 3):
+        raise ValueError("[N, K] or [E, N, K] expected")
+    shape = tuple(w.shape)
+    E, N, K = shape if len(shape) == 3 else (1,) + shape
+    sshape = shape[:-2] + (_blocks(N), _blocks(K))
+    if q is None:
+        q = torch.empty(shape, dtype=torch.uint8, device=w.device)
+    if scale is None:
+        scale = torch.empty(sshape, dtype=torch.float32, device=w.device)
+    dev = _same_device(w, (w, torch.bfloat16, shape, "w"), (q, torch.uint8, shape, "q"),
+                       (scale, torch.float32, sshape, "scale"))
+    _call(dev, "quantize_weight_blocks", w.data_ptr(), E, N, K, q.data_ptr(), scale.data_ptr())
+    return q, scale
+
+
+def w8a8_block_gemm(a_q, a_scale, w_q, w_scale, out=None):
+    """y[m, n] = bf16(sum over blocks b of K of a_scale[b, m] * w_scale[n/128, b] * (a_q . w_q over the block))
+    (E4M3 operands of quantize_blocks and quantize_weight_blocks)."""
+    import torch
+
+    M, K = a_q.shape
+    N = w_q.shape[0]
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device)
+    dev = _same_device(a_q, (a_q, torch.uint8, (M, K), "a_q"), (a_scale, torch.float32, (_blocks(K), M), "a_scale"),
+                       (w_q, torch.uint8, (N, K), "w_q"),
+                       (w_scale, torch.float32, (_blocks(N), _blocks(K)), "w_scale"),
+                       (out, torch.bfloat16, (M, N), "out"))
+    _call(dev, "w8a8_block_gemm", a_q.data_ptr(), a_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(),
+          out.data_ptr(), M, N, K)
+    return out
+
+
+def w8a8_block_linear(x, w_q, w_scale, out=None, workspace=None):
+    """The layer on BF16 input: quantize_blocks, then w8a8_block_gemm (up to 32
+    rows in one launch without a workspace; the same bits)."""
+    import torch
+
+    M, K = x.shape
+    N = w_q.shape[0]
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    dev = _same_device(x, (x, torch.bfloat16, (M, K), "x"), (w_q, torch.uint8, (N, K), "w_q"),
+                       (w_scale, torch.float32, (_blocks(N), _blocks(K)), "w_scale"),
+                       (out, torch.bfloat16, (M, N), "out"))
+    if workspace is None and M > 32:
+        workspace = torch.empty(max(int(lib().w8a8_block_linear_workspace_bytes(M, K)), 16), dtype=torch.uint8,
+                                device=x.device)
+    _call(dev, "w8a8_block_linear", x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), out.data_ptr(), M, N, K,
+          *_workspace_args(workspace, dev))
+    return out
+
+
+def moe_w8a8_block_workspace(T: int, H: int, I: int, E: int, topk: int, device="cuda"):
+    """Scratch buffer sized for moe_w8a8_block_grouped."""
+    import torch
+
+    nbytes = int(lib().moe_w8a8_block_workspace_bytes(T, H, I, E, topk))
+    if nbytes == 0 and T > 0:
+        raise ValueError("unsupported routed-expert sizes")
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
+def moe_w8a8_block_grouped(x_q, x_scale, topk_ids, topk_w, w13_q, w13_scale, w2_q, w2_scale, out=None, workspace=None,
+                           quantize_output=False):
+    """One routed-expert pass on block-scaled FP8 tokens and weights: BF16 [T, H].
+
+    With ``quantize_output`` also quantize_blocks of the output, made in the
+    combine: the input of the next pass. Returns ``out`` or ``(out, out_q,
+    out_scale)``."""
+    import torch
+
+    T, H = x_q.shape
+    k = topk_ids.shape[1]
+    E, twoI = w13_q.shape[:2]
+    I = twoI // 2
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x_q.device)
+    hb = _blocks(H)
+    dev = _same_device(x_q, (x_q, torch.uint8, (T, H), "x_q"), (x_scale, torch.float32, (hb, T), "x_scale"),
+                       (topk_ids, torch.int32, (T, k), "topk_ids"), (topk_w, torch.float32, (T, k), "topk_w"),
+                       (w13_q, torch.uint8, (E, 2 * I, H), "w13_q"),
+                       (w13_scale, torch.float32, (E, _blocks(2 * I), hb), "w13_scale"),
+                       (w2_q, torch.uint8, (E, H, I), "w2_q"), (w2_scale, torch.float32, (E, hb, _blocks(I)), "w2_scale"),
+                       (out, torch.bfloat16, (T, H), "out"))
+    if workspace is None:
+        workspace = moe_w8a8_block_workspace(T, H, I, E, k, device=x_q.device)
+    oq = os_ = None
+    if quantize_output:
+        oq = torch.empty((T, H), dtype=torch.uint8, device=x_q.device)
+        os_ = torch.empty((hb, T), dtype=torch.float32, device=x_q.device)
+    _call(dev, "moe_w8a8_block_grouped", x_q.data_ptr(), x_scale.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
+          w13_q.data_ptr(), w13_scale.data_ptr(), w2_q.data_ptr(), w2_scale.data_ptr(), out.data_ptr(),
+          oq.data_ptr() if quantize_output else None, os_.data_ptr() if quantize_output else None, T, H, I, E, k,
+          *_workspace_args(workspace, dev))
+    return (out, oq, os_) if quantize_output else out
+
+
+def moe_block_ffn(x, routes, w13_q, w13_scale, w2_q, w2_scale, workspace=None):
+    """moe_ffn on block-scaled weights: the routed-expert stage once per entry
+    (topk_ids, topk_w) of ``routes``, each pass on the previous pass's output,
+    which that pass's combine has quantised by blocks. Returns the list of
+    per-pass BF16 outputs."""
+    outs = []
+    q, s = quantize_blocks(x)
+    for i, (ids, tw) in enumerate(routes):
+        last = i + 1 == len(routes)
+        r = moe_w8a8_block_grouped(q, s, ids, tw, w13_q, w13_scale, w2_q, w2_scale, workspace=workspace,
+                                   quantize_output=not last)
+        if last:
+            outs.append(r)
+        else:
+            out, q, s = r
+            outs.append(out)
+    return outs
+
+
+def moe_balance_loss(logits, topk_ids, coef=1.0, sequences=1, score="softmax", with_grad=True, loss=None, counts=None,
+                     grad=None, workspace=None):
+    """How evenly the router's choice loads the experts: (loss float32 [], counts
+    int32 [sequences, E], d loss / d logits).
+
+    loss = coef / S * sum over sequences s and experts e of E * counts[s, e] /
+    (topk * n[s]) * mean over the sequence's tokens of p[t, e], p the softmax of
+    the logits, or their sigmoids divided by their sum. Logits [T, E] are float32
+    or BF16 (``moe_router(..., logits=)``), the sequences equally long. Ids
+    outside [0, E) are dropped; a token without a valid id (padding) does not
+    count and its gradient is zero. The counts are constants of the gradient,
+    which has the logits' type; ``with_grad=False`` leaves it out (None)."""
+    import torch
+
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
+    if sequences < 1 or T % sequences:
+        raise ValueError("sequences must be positive and divide the number of tokens")
+    if loss is None:
+        loss = torch.empty((), dtype=torch.float32, device=logits.device)
+    if counts is None:
+        counts = torch.empty((sequences, E), dtype=torch.int32, device=logits.device)
+    if grad is None and with_grad:
+        grad = torch.empty_like(logits)
+    dev = _same_device(logits, (logits, logits.dtype, (T, E), "logits"), (topk_ids, torch.int32, (T, k), "topk_ids"),
+                       (loss, torch.float32, (), "loss"), (counts, torch.int32, (sequences, E), "counts"),
+                       *(((grad, logits.dtype, (T, E), "grad"),) if grad is not None else ()))
+    if workspace is None:
+        workspace = torch.empty(max(int(lib().moe_balance_loss_workspace_bytes(T, sequences, E)), 16), dtype=torch.uint8,
+                                device=logits.device)
+    _call(dev, "moe_balance_loss", int(logits.dtype is torch.bfloat16), logits.data_ptr(), topk_ids.data_ptr(), T,
+          sequences, E, k, _SCORES[score], coef, loss.data_ptr(), counts.data_ptr(),
+          grad.data_ptr() if grad is not None else None, *_workspace_args(workspace, dev))
+    return loss, counts, grad

@@ -696,20 +696,36 @@ size_t moe_router_workspace_bytes(int64_t T, int64_t E) {
   return w8a8::router_workspace_bytes(T, E);
 }
 
-int moe_router(const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int32_t* topk_ids, float* topk_w,
-               int64_t T, int64_t H, int64_t E, int64_t topk, int score, int renormalize, float route_scale,
-               void* workspace, size_t workspace_bytes, hipStream_t stream) {
+static int router_checked(const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int32_t* topk_ids,
+                          float* topk_w, float* logits, bool with_logits, int64_t T, int64_t H, int64_t E, int64_t topk,
+                          int score, int renormalize, float route_scale, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
   const int c = check_router_shape(T, H, E, topk, score);
   if (c != W8A8_OK) return c;
   if (T == 0) return W8A8_OK;
-  if (any_null({x_bf16, w_router, topk_ids, topk_w, workspace})) return W8A8_ERR_NULL_ARG;
-  if (!all_aligned({x_bf16, w_router, bias, topk_ids, topk_w, workspace})) return W8A8_ERR_MISALIGNED;
+  if (any_null({x_bf16, w_router, topk_ids, topk_w, workspace}) || (with_logits && !logits)) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({x_bf16, w_router, bias, topk_ids, topk_w, logits, workspace})) return W8A8_ERR_MISALIGNED;
   if (workspace_bytes < w8a8::router_workspace_bytes(T, E)) return W8A8_ERR_WORKSPACE;
   const int d = check_device();
   if (d != W8A8_OK) return d;
   const w8a8::Router r{x_bf16,   w_router, bias, topk_ids, topk_w, score == MOE_SCORE_SIGMOID, renormalize != 0,
-                       route_scale};
+                       route_scale, logits};
   return launch_status(w8a8::launch_router(r, T, H, E, topk, workspace, stream));
+}
+
+int moe_router(const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int32_t* topk_ids, float* topk_w,
+               int64_t T, int64_t H, int64_t E, int64_t topk, int score, int renormalize, float route_scale,
+               void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return router_checked(x_bf16, w_router, bias, topk_ids, topk_w, nullptr, false, T, H, E, topk, score, renormalize,
+                        route_scale, workspace, workspace_bytes, stream);
+}
+
+int moe_router_with_logits(const uint16_t* x_bf16, const uint16_t* w_router, const float* bias, int32_t* topk_ids,
+                           float* topk_w, float* logits_f32, int64_t T, int64_t H, int64_t E, int64_t topk, int score,
+                           int renormalize, float route_scale, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream) {
+  return router_checked(x_bf16, w_router, bias, topk_ids, topk_w, logits_f32, true, T, H, E, topk, score, renormalize,
+                        route_scale, workspace, workspace_bytes, stream);
 }
 
 size_t moe_few_tokens_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
@@ -756,9 +772,168 @@ int moe_few_tokens_layer(int format, const uint16_t* x_bf16, const uint16_t* w_r
   const int d = check_device();
   if (d != W8A8_OK) return d;
   const w8a8::Router r{x_bf16,   w_router, bias, topk_ids, topk_w, score == MOE_SCORE_SIGMOID, renormalize != 0,
-                       route_scale};
+                       route_scale, nullptr};
   const w8a8::Few f{format, x_bf16, topk_ids, topk_w, w13_q, w13_scale, w13_gscale, w2_q, w2_scale, w2_gscale, out_bf16};
   return launch_status(w8a8::launch_few(f, &r, T, H, I, E, topk, workspace, stream));
+}
+
+}  // extern "C"
+
+// ---- FP8 with a scale per block of 128 --------------------------------------------
+namespace {
+
+int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+
+int check_quant_blocks(int64_t M, int64_t K) {
+  if (M < 0 || K < 0 || !mul_ok(M, K) || !mul_ok(M * K, 2)) return W8A8_ERR_BAD_SHAPE;
+  // 16 rows x 4 blocks a workgroup; the grid's second extent is 16 bits wide
+  if (K == 0 || K % 16 != 0 || K > (int64_t(1) << 24) || M > (int64_t(1) << 26)) return W8A8_ERR_UNSUPPORTED;
+  if (((M + 15) / 16) * ((blocks128(K) + 3) / 4) >= int64_t(1) << 24) return W8A8_ERR_UNSUPPORTED;
+  return W8A8_OK;
+}
+
+int check_quant_weight_blocks(int64_t E, int64_t N, int64_t K) {
+  if (E < 0 || N < 0 || K < 0 || !mul_ok(N, K) || !mul_ok(E, N * K) || !mul_ok(E * N * K, 2)) return W8A8_ERR_BAD_SHAPE;
+  if (K == 0 || K % 16 != 0 || K > (int64_t(1) << 20) || N > (int64_t(1) << 20) || E > (int64_t(1) << 20))
+    return W8A8_ERR_UNSUPPORTED;
+  if (blocks128(N) * blocks128(K) >= int64_t(1) << 24 || E * (blocks128(N) * blocks128(K)) >= int64_t(1) << 24)
+    return W8A8_ERR_UNSUPPORTED;  // a workgroup of 256 threads a block, fewer than 2^32 threads
+  return W8A8_OK;
+}
+
+// As the other dense products, and the scales' offsets inside a tile fit 32 bits.
+int check_block_dense(int64_t M, int64_t N, int64_t K) {
+  const int c = check_dense_shape(M, N, K);
+  if (c != W8A8_OK) return c;
+  if (((M + 63) / 64) * ((N + 63) / 64) >= int64_t(1) << 23) return W8A8_ERR_UNSUPPORTED;
+  return W8A8_OK;
+}
+
+int check_block_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
+  const int c = check_moe_shape(T, H, I, E, topk);
+  if (c != W8A8_OK) return c;
+  if (I % kFusedIMultiple != 0) return W8A8_ERR_UNSUPPORTED;
+  if (!mul_ok(T * topk, H) || !mul_ok(T * topk * H, 4)) return W8A8_ERR_BAD_SHAPE;
+  // a grid holds fewer than 2^32 threads: 4 waves for 64 rows and 128 columns
+  if ((T * topk / 64 + E + 1) * (blocks128(H) + blocks128(I)) >= int64_t(1) << 22 || T * blocks128(H) >= int64_t(1) << 27)
+    return W8A8_ERR_UNSUPPORTED;
+  return W8A8_OK;
+}
+
+int check_balance(int64_t T, int64_t S, int64_t E, int64_t topk, int dtype, int score) {
+  if (T < 0 || S < 0 || E < 0 || topk < 0) return W8A8_ERR_BAD_SHAPE;
+  if (E < 1 || E > kMaxExperts || topk < 1 || topk > kMaxTopk || T > (int64_t(1) << 24)) return W8A8_ERR_UNSUPPORTED;
+  if (S < 1 || S > (int64_t(1) << 20) || T % S != 0) return W8A8_ERR_UNSUPPORTED;
+  if (dtype != MOE_LOGITS_F32 && dtype != MOE_LOGITS_BF16) return W8A8_ERR_UNSUPPORTED;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return W8A8_ERR_UNSUPPORTED;
+  return W8A8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int quantize_blocks(const uint16_t* x_bf16, int64_t M, int64_t K, uint8_t* q_e4m3, float* scale, hipStream_t stream) {
+  const int c = check_quant_blocks(M, K);
+  if (c != W8A8_OK) return c;
+  if (M == 0) return W8A8_OK;
+  if (any_null({x_bf16, q_e4m3, scale})) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({x_bf16, q_e4m3, scale})) return W8A8_ERR_MISALIGNED;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  return launch_status(w8a8::launch_quantize_blocks(x_bf16, M, K, q_e4m3, scale, stream));
+}
+
+int quantize_weight_blocks(const uint16_t* w_bf16, int64_t E, int64_t N, int64_t K, uint8_t* q_e4m3, float* scale,
+                           hipStream_t stream) {
+  const int c = check_quant_weight_blocks(E, N, K);
+  if (c != W8A8_OK) return c;
+  if (E == 0 || N == 0) return W8A8_OK;
+  if (any_null({w_bf16, q_e4m3, scale})) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({w_bf16, q_e4m3, scale})) return W8A8_ERR_MISALIGNED;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  return launch_status(w8a8::launch_quantize_weight_blocks(w_bf16, E, N, K, q_e4m3, scale, stream));
+}
+
+int w8a8_block_gemm(const uint8_t* a_q, const float* a_scale, const uint8_t* w_q, const float* w_scale,
+                    uint16_t* y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  const int c = check_block_dense(M, N, K);
+  if (c != W8A8_OK) return c;
+  if (M == 0 || N == 0) return W8A8_OK;
+  if (any_null({a_q, a_scale, w_q, w_scale, y_bf16})) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({a_q, a_scale, w_q, w_scale, y_bf16})) return W8A8_ERR_MISALIGNED;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  return launch_status(w8a8::launch_block_gemm(a_q, a_scale, w_q, w_scale, y_bf16, M, N, K, stream));
+}
+
+size_t w8a8_block_linear_workspace_bytes(int64_t M, int64_t K) {
+  if (check_quant_blocks(M, K) != W8A8_OK || K > (int64_t(1) << 20) || M > (int64_t(1) << 24)) return 0;
+  return w8a8::block_linear_workspace_bytes(M, K);
+}
+
+int w8a8_block_linear(const uint16_t* x_bf16, const uint8_t* w_q, const float* w_scale, uint16_t* y_bf16, int64_t M,
+                      int64_t N, int64_t K, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int c = check_block_dense(M, N, K);
+  if (c != W8A8_OK) return c;
+  const int cq = check_quant_blocks(M, K);
+  if (cq != W8A8_OK) return cq;
+  if (M == 0 || N == 0) return W8A8_OK;
+  const size_t need = w8a8::block_linear_workspace_bytes(M, K);
+  if (any_null({x_bf16, w_q, w_scale, y_bf16}) || (need && !workspace)) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({x_bf16, w_q, w_scale, y_bf16}) || (need && !aligned16(workspace))) return W8A8_ERR_MISALIGNED;
+  if (workspace_bytes < need) return W8A8_ERR_WORKSPACE;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  return launch_status(w8a8::launch_block_linear(x_bf16, w_q, w_scale, y_bf16, M, N, K, workspace, stream));
+}
+
+size_t moe_w8a8_block_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
+  if (check_block_moe(T, H, I, E, topk) != W8A8_OK) return 0;
+  return w8a8::block_moe_workspace_bytes(T, H, I, E, topk);
+}
+
+int moe_w8a8_block_grouped(const uint8_t* x_q, const float* x_scale, const int32_t* topk_ids, const float* topk_w,
+                           const uint8_t* w13_q, const float* w13_scale, const uint8_t* w2_q, const float* w2_scale,
+                           uint16_t* out_bf16, uint8_t* out_q, float* out_scale, int64_t T, int64_t H, int64_t I,
+                           int64_t E, int64_t topk, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int c = check_block_moe(T, H, I, E, topk);
+  if (c != W8A8_OK) return c;
+  if (T == 0) return W8A8_OK;
+  if (any_null({x_q, x_scale, topk_ids, topk_w, w13_q, w13_scale, w2_q, w2_scale, out_bf16, workspace}))
+    return W8A8_ERR_NULL_ARG;
+  if ((out_q == nullptr) != (out_scale == nullptr)) return W8A8_ERR_NULL_ARG;
+  if (!all_aligned({x_q, x_scale, topk_ids, topk_w, w13_q, w13_scale, w2_q, w2_scale, out_bf16, out_q, out_scale,
+                    workspace}))
+    return W8A8_ERR_MISALIGNED;
+  if (workspace_bytes < w8a8::block_moe_workspace_bytes(T, H, I, E, topk)) return W8A8_ERR_WORKSPACE;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  return launch_status(w8a8::launch_block_moe(x_q, x_scale, topk_ids, topk_w, w13_q, w13_scale, w2_q, w2_scale,
+                                              out_bf16, out_q, out_scale, T, H, I, E, topk, workspace, stream));
+}
+
+size_t moe_balance_loss_workspace_bytes(int64_t T, int64_t S, int64_t E) {
+  if (check_balance(T, S, E, 1, MOE_LOGITS_F32, MOE_SCORE_SOFTMAX) != W8A8_OK) return 0;
+  return w8a8::balance_workspace_bytes(T, S, E);
+}
+
+int moe_balance_loss(int logits_dtype, const void* logits, const int32_t* topk_ids, int64_t T, int64_t S, int64_t E,
+                     int64_t topk, int score, float coef, float* loss, int32_t* counts, void* grad_logits,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int c = check_balance(T, S, E, topk, logits_dtype, score);
+  if (c != W8A8_OK) return c;
+  if (any_null({loss, counts, workspace}) || (T > 0 && any_null({logits, topk_ids}))) return W8A8_ERR_NULL_ARG;
+  // the loss is one float, often an element of a vector with one per layer
+  if (!all_aligned({logits, topk_ids, counts, grad_logits, workspace}) || (reinterpret_cast<uintptr_t>(loss) & 3u))
+    return W8A8_ERR_MISALIGNED;
+  if (workspace_bytes < w8a8::balance_workspace_bytes(T, S, E)) return W8A8_ERR_WORKSPACE;
+  const int d = check_device();
+  if (d != W8A8_OK) return d;
+  const w8a8::Balance b{logits, topk_ids, loss, counts, grad_logits, logits_dtype == MOE_LOGITS_BF16,
+                        score == MOE_SCORE_SIGMOID, coef};
+  return launch_status(w8a8::launch_balance(b, T, S, E, topk, workspace, stream));
 }
 
 }  // extern "C"

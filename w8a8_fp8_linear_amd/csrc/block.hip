@@ -1,0 +1,696 @@
+// FP8 with a scale per block of 128: quantisers, the dense product, and the
+// routed-expert pass.
+//
+// The pages' FP8 scheme rounds a layer's input to FP8 at run time and
+// multiplies it with FP8 weights on the FP8 matrix units (Lernex/Metis-1.6-
+// Logos-FP8, "What --fast-math does"), with one scale per token and one per
+// output channel. Here a scale covers less: 128 consecutive values of a row of
+// activations, 128 x 128 values of a weight matrix, so that one outlier costs
+// 128 values their small digits and not a whole row. A K step of the
+// 16x16x128 E4M3 MFMA is one block:
+//   y[m,n] = sum_b sa[b,m] * sw[n/128,b] * sum_{k in block b} a[m,k] w[n,k]
+// Every MFMA starts from C = 0 and its four results are added to the float32
+// accumulators times the product of the two scales: four FMAs of the vector
+// unit to an MFMA (16 of its 32 cycles).
+#include <algorithm>
+
+#include "device.h"
+#include "grouped.h"
+#include "launch.h"
+
+namespace w8a8 {
+namespace {
+
+// ---- quantisers ------------------------------------------------------------
+
+// Maximum over each row of 16 lanes, in every lane: swaps inside quads, then
+// mirrored halves and rows, all by DPP.
+__device__ inline uint32_t row16_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+  return v;
+}
+
+// Activations. 16 lanes take a block (16 bytes each), a workgroup 16 rows x 4
+// blocks, whose loads go out together: 1 KB of a row, and the scales of 16 rows
+// are one 64-byte piece of the [blocks, M] array.
+constexpr int kQuantRows = 16, kQuantBlocks = 4;
+
+__global__ __launch_bounds__(256) void quant_row_blocks(const uint16_t* __restrict__ x, int64_t M, int64_t K,
+                                                        uint8_t* __restrict__ q, float* __restrict__ scale) {
+  const int64_t row = (int64_t)blockIdx.x * kQuantRows + (threadIdx.x >> 4);
+  const int l = threadIdx.x & 15;
+  if (row >= M) return;
+  const int64_t k0 = ((int64_t)blockIdx.y * kQuantBlocks << 7) + 8 * l;
+  v4i v[kQuantBlocks];
+#pragma unroll
+  for (int b = 0; b < kQuantBlocks; ++b) {
+    v[b] = v4i{0, 0, 0, 0};
+    if (k0 + 128 * b < K) v[b] = *reinterpret_cast<const v4i*>(x + row * K + k0 + 128 * b);
+  }
+#pragma unroll
+  for (int b = 0; b < kQuantBlocks; ++b) {
+    const uint4 u = make_uint4((uint32_t)v[b].x, (uint32_t)v[b].y, (uint32_t)v[b].z, (uint32_t)v[b].w);
+    const float s = row_scale(row16_max(absmax8(u)));
+    const int64_t k = k0 + 128 * b;
+    if (k < K) *reinterpret_cast<uint2*>(q + row * K + k) = quant8(u, s, 1.0f / s);
+    if (l == 0 && k < K) scale[(k >> 7) * M + row] = s;
+  }
+}
+
+// Weights: a workgroup per 128 x 128 block, held in registers between the
+// maximum and the codes.
+__global__ __launch_bounds__(256) void quant_weight_blocks(const uint16_t* __restrict__ w, int64_t N, int64_t K,
+                                                           int nb, int kb, uint8_t* __restrict__ q,
+                                                           float* __restrict__ scale) {
+  __shared__ uint32_t wmax[4];
+  const int64_t e = blockIdx.x / (uint32_t)(nb * kb);
+  const int rest = (int)(blockIdx.x - e * (nb * kb));
+  const int64_t n0 = (int64_t)(rest / kb) * 128, k = (int64_t)(rest % kb) * 128 + 8 * (threadIdx.x & 15);
+  const int r0 = threadIdx.x >> 4;
+  const uint16_t* src = w + (e * N + n0) * K + k;
+  v4i v[8];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = v4i{0, 0, 0, 0};
+    if (n0 + r0 + 16 * i < N && k < K) v[i] = *reinterpret_cast<const v4i*>(src + (int64_t)(r0 + 16 * i) * K);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    amax = max(amax, absmax8(make_uint4((uint32_t)v[i].x, (uint32_t)v[i].y, (uint32_t)v[i].z, (uint32_t)v[i].w)));
+  amax = wave_max_u32(amax);
+  if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = amax;
+  __syncthreads();
+  const float s = row_scale(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])));
+  const float r = 1.0f / s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (n0 + r0 + 16 * i < N && k < K)
+      *reinterpret_cast<uint2*>(q + (e * N + n0 + r0 + 16 * i) * K + k) =
+          quant8(make_uint4((uint32_t)v[i].x, (uint32_t)v[i].y, (uint32_t)v[i].z, (uint32_t)v[i].w), s, r);
+  if (threadIdx.x == 0) scale[blockIdx.x] = s;
+}
+
+// ---- products of at most 32 rows ---------------------------------------------
+
+// NT tiles of 16 weight rows a workgroup, K split over 4 waves, U steps of
+// loads in flight a wave. Q: x is BF16 and is quantised on the way: a lane
+// group's 16-lane columns hold a row's block between them, so its maximum is
+// two exchanges, and nothing has to wait for another wave.
+template <int MT, int U, int NT, bool Q>
+__global__ __launch_bounds__(256) void block_skinny(const void* __restrict__ X, const float* __restrict__ sA,
+                                                    const uint8_t* __restrict__ W, const float* __restrict__ sW,
+                                                    uint16_t* __restrict__ Y, int M, int N, int K) {
+  __shared__ v4f red[3][NT][MT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 16 * NT;
+  const auto rW = make_rsrc(W + (int64_t)n0 * K, (int64_t)(N - n0) * K);
+  const auto rX = make_rsrc(X, (int64_t)M * K * (Q ? 2 : 1));
+  const int r16 = lane & 15, g = lane >> 4;
+  const int nk = (K + 127) >> 7;
+  const float* sWrow = sW + (int64_t)(n0 >> 7) * nk;  // 16 NT rows of one weight block
+  v4f acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int kt = wave; kt < nk; kt += 4 * U) {
+    v8i wf[U][NT];
+    v4i xb[U][MT][Q ? 4 : 2];
+    float sx[U][MT], sw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = kt + 4 * u;
+      const bool live = kb < nk;
+      const int c0 = (kb << 7) + 16 * g, c1 = c0 + 64;
+      const uint32_t o0 = live && c0 < K ? (uint32_t)c0 : kOutOfRange;
+      const uint32_t o1 = live && c1 < K ? (uint32_t)c1 : kOutOfRange;
+      sw[u] = sWrow[live ? kb : 0];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const uint32_t row = (uint32_t)(t * 16 + r16);
+        if constexpr (Q) {
+          const uint32_t xrow = row * (uint32_t)K * 2u;
+          const uint32_t b0 = o0 == kOutOfRange ? o0 : xrow + 2u * o0, b1 = o1 == kOutOfRange ? o1 : xrow + 2u * o1;
+          xb[u][t][0] = buffer_load16(rX, b0);
+          xb[u][t][1] = buffer_load16(rX, o0 == kOutOfRange ? b0 : b0 + 16u);
+          xb[u][t][2] = buffer_load16(rX, b1);
+          xb[u][t][3] = buffer_load16(rX, o1 == kOutOfRange ? b1 : b1 + 16u);
+        } else {
+          const uint32_t xrow = row * (uint32_t)K;
+          xb[u][t][0] = buffer_load16(rX, o0 == kOutOfRange ? o0 : xrow + o0);
+          xb[u][t][1] = buffer_load16(rX, o1 == kOutOfRange ? o1 : xrow + o1);
+          sx[u][t] = live && (int)row < M ? sA[(int64_t)kb * M + row] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const uint32_t wrow = (uint32_t)(i * 16 + r16) * (uint32_t)K;
+        const v4i lo = buffer_load16(rW, o0 == kOutOfRange ? o0 : wrow + o0);
+        const v4i hi = buffer_load16(rW, o1 == kOutOfRange ? o1 : wrow + o1);
+        wf[u][i] = v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      }
+    }
+    // every load of the round ahead of the first use
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        v8i xf;
+        if constexpr (Q) {
+          uint4 b[4];
+          uint32_t am = 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const v4i v = xb[u][t][c];
+            b[c] = make_uint4((uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w);
+            am = max(am, absmax8(b[c]));
+          }
+          am = max(am, (uint32_t)__shfl_xor((int)am, 16, 64));
+          am = max(am, (uint32_t)__shfl_xor((int)am, 32, 64));
+          const float s = row_scale(am), r = 1.0f / s;
+          sx[u][t] = s;
+          const uint2 q0 = quant8(b[0], s, r), q1 = quant8(b[1], s, r), q2 = quant8(b[2], s, r), q3 = quant8(b[3], s, r);
+          xf = v8i{(int)q0.x, (int)q0.y, (int)q1.x, (int)q1.y, (int)q2.x, (int)q2.y, (int)q3.x, (int)q3.y};
+        } else {
+          const v4i a = xb[u][t][0], b = xb[u][t][1];
+          xf = v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        }
+        const float s = sx[u][t] * sw[u];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const v4f d = mfma_16x16x128_e4m3(wf[u][i], xf, v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][t][r] = __builtin_fmaf(d[r], s, acc[i][t][r]);
+        }
+      }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) red[wave - 1][i][t][lane] = acc[i][t];
+  }
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int n = n0 + i * 16 + 4 * g;
+    if (n >= N) continue;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const v4f a = acc[i][t] + red[0][i][t][lane] + red[1][i][t][lane] + red[2][i][t][lane];
+      const int m = t * 16 + r16;
+      if (m < M) *reinterpret_cast<uint2*>(Y + (int64_t)m * N + n) = make_uint2(bf16x2_rne(a[0], a[1]), bf16x2_rne(a[2], a[3]));
+    }
+  }
+}
+
+// ---- tiled products ------------------------------------------------------------
+
+enum { kDense = 0, kGateUp = 1, kDown = 2 };
+
+struct BlockArgs {
+  const uint8_t* A;        // codes: dense [M, K]; gate/up tokens [T, K]; down sorted h rows [T topk, K]
+  const float* sA;         // their scales [blocks of K, a_rows]
+  int64_t a_rows;
+  const uint8_t* B;        // [E, N, K] codes (dense: E = 1)
+  const float* sB;         // [E, blocks of N, blocks of K]
+  const int32_t* perm;     // sorted row -> slot
+  const int32_t* offsets;  // [E + 1]
+  const float* tw;         // [slots] router weights (down)
+  uint16_t* y;             // dense [M, N]
+  uint8_t* hq;             // gate/up: codes of h [T topk, N / 2]
+  float* hs;               // gate/up: their scales [N / 256, T topk]
+  float* y32;              // down: weighted rows in sorted order [T topk, N]
+  int32_t* slot_row;       // down: slot -> sorted row
+  int E, topk, N, K, tiles_m, tiles_n;
+};
+
+template <int BM, int BN, int WGM, int WGN, int MODE>
+struct BlockTile {
+  static constexpr int kThreads = 64 * WGM * WGN;
+  static constexpr int WM = BM / WGM, WN = BN / WGN;  // a wave's part
+  static constexpr int SM = WM / 16, SN = WN / 16;
+  static constexpr int kRows = BM + BN;
+  static constexpr int kCodes = kRows * 128;                              // bytes of a stage's codes
+  static constexpr int kStage = kCodes + (BM * 4 + 1023) / 1024 * 1024;   // and its row scales
+  static constexpr int kRowsPerPass = kThreads / 8;
+  static constexpr int kLoadsB = BN / kRowsPerPass, kLoadsA = BM / kRowsPerPass;
+  static constexpr int kEpiStride = BN * 2 + 16;  // dense: staged BF16 row
+  static constexpr int kHStride = 128 + 16;       // gate/up: staged row of h codes
+  static constexpr int kEpi = MODE == kDense ? BM * kEpiStride
+                              : MODE == kGateUp ? BM * kHStride + WGN * BM * 4 : WM * BN * 4;
+  static constexpr int kLds = 2 * kStage > kEpi ? 2 * kStage : kEpi;
+  static_assert(BN % kRowsPerPass == 0 && BM % kRowsPerPass == 0 && kRowsPerPass % 8 == 0, "stages split evenly");
+  static_assert(WM % 16 == 0 && WN % 16 == 0 && BM % 64 == 0 && BM / 64 <= WGM * WGN, "wave tiles");
+  static_assert(MODE != kGateUp || (BN == 256 && SN % 2 == 0), "a gate/up tile is one block of 128 h columns");
+};
+
+// One 128-deep K step is one block of scales. Stages are double-buffered in
+// LDS: the codes by direct 16-byte loads (rows of 128 bytes, 16-byte pieces
+// swizzled), the step's row scales by direct 4-byte loads behind them; the
+// weight scale is one value a wave (a wave's columns lie in one block where
+// their number divides 128), read by scalar loads.
+//  kDense   y = bf16(a . w^T)
+//  kGateUp  rows gathered through the sorted order; stage rows alternate 16
+//           gate and the 16 matching up rows, so that g and u of an element meet
+//           in one lane. A tile's 128 columns of h are one block: its row maxima
+//           meet in LDS, and h leaves as codes and scales.
+//  kDown    y32 = router weight * (h . w2^T), a float32 row per sorted row.
+template <int BM, int BN, int WGM, int WGN, int MODE>
+__global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(1, 2)))
+void block_tiled(const BlockArgs p) {
+  using C = BlockTile<BM, BN, WGM, WGN, MODE>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds + (MODE == kDense ? 0 : BM * 8)];
+  int* const row_slot = reinterpret_cast<int*>(smem + C::kLds);                // slot of a tile row, -1: none
+  float* const row_w = reinterpret_cast<float*>(smem + C::kLds + BM * 4);      // its router weight
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int N = p.N, K = p.K;
+  int row0, rows, nt, e = 0;
+  if constexpr (MODE == kDense) {
+    int tm;
+    map_tile<4>(blockIdx.x, p.tiles_m, p.tiles_n, tm, nt);
+    row0 = tm * BM;
+    rows = min(BM, (int)p.a_rows - row0);
+  } else {
+    const int total = p.tiles_m * p.tiles_n, per = total >> 3;
+    int t = blockIdx.x;
+    if ((int)blockIdx.x < (per << 3)) t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    const int mt = t / p.tiles_n;
+    nt = t - mt * p.tiles_n;
+    const int cap = (int)(MODE == kDown ? p.a_rows : p.a_rows * p.topk);
+    if (!find_tile(p.offsets, p.E, BM, mt, cap, e, row0, rows)) return;
+    for (int i = tid; i < BM; i += C::kThreads) {
+      int slot = -1;
+      if (i < rows) slot = p.perm[row0 + i];
+      if (slot >= cap) slot = -1;
+      row_slot[i] = slot;
+      if (MODE == kDown) {
+        row_w[i] = slot >= 0 ? p.tw[slot] : 0.f;
+        if (nt == 0 && slot >= 0) p.slot_row[slot] = row0 + i;
+      }
+    }
+    __syncthreads();
+  }
+  const int n0 = nt * BN;
+  const int nb = (N + 127) >> 7, nk = (K + 127) >> 7;
+  const auto rB = MODE == kGateUp ? make_rsrc(p.B + (int64_t)e * N * K, (int64_t)N * K)
+                                  : make_rsrc(p.B + ((int64_t)e * N + n0) * K, (int64_t)(N - n0) * K);
+  const auto rA = MODE == kGateUp ? make_rsrc(p.A, p.a_rows * K) : make_rsrc(p.A + (int64_t)row0 * K, (int64_t)rows * K);
+
+  const int lchunk = ((tid & 7) ^ ((tid >> 3) & 7)) << 4;
+  const int lrow = tid >> 3;
+  uint32_t boff[C::kLoadsB], aoff[C::kLoadsA];
+#pragma unroll
+  for (int i = 0; i < C::kLoadsB; ++i) {
+    const int r = lrow + C::kRowsPerPass * i;
+    int wr = r;
+    if (MODE == kGateUp) wr = ((r >> 4) & 1 ? N / 2 : 0) + (n0 >> 1) + (r >> 5) * 16 + (r & 15);
+    boff[i] = (uint32_t)wr * (uint32_t)K + (uint32_t)lchunk;
+  }
+#pragma unroll
+  for (int j = 0; j < C::kLoadsA; ++j) {
+    const int r = lrow + C::kRowsPerPass * j;
+    if constexpr (MODE == kGateUp) {
+      const int slot = row_slot[r];
+      aoff[j] = slot < 0 ? kOutOfRange : (uint32_t)(slot / p.topk) * (uint32_t)K + (uint32_t)lchunk;
+    } else {
+      aoff[j] = r < rows ? (uint32_t)r * (uint32_t)K + (uint32_t)lchunk : kOutOfRange;
+    }
+  }
+  // this lane's row scale of a step: lane l of wave w < BM / 64 loads row 64 w + l
+  uint32_t soff = kOutOfRange;
+  if (wave < BM / 64) {
+    const int r = wave * 64 + lane;
+    if constexpr (MODE == kGateUp) {
+      const int slot = row_slot[r];
+      if (slot >= 0) soff = (uint32_t)(slot / p.topk) * 4u;
+    } else if (r < rows) {
+      soff = (uint32_t)r * 4u;
+    }
+  }
+  auto issue = [&](int stage, int kt) {
+    uint8_t* base = smem + stage * C::kStage;
+    const int k0 = kt << 7;
+    const bool kin = k0 + lchunk < K;
+#pragma unroll
+    for (int i = 0; i < C::kLoadsB + C::kLoadsA; ++i) {
+      const int s0 = wave * 64 + C::kThreads * i;
+      if (i < C::kLoadsB) {
+        buffer_load16_lds(rB, base + s0 * 16, kin ? boff[i] + (uint32_t)k0 : kOutOfRange);
+      } else {
+        const uint32_t a = aoff[i - C::kLoadsB];
+        buffer_load16_lds(rA, base + s0 * 16, kin && a != kOutOfRange ? a + (uint32_t)k0 : kOutOfRange);
+      }
+    }
+    if (wave < BM / 64) {
+      const float* s = p.sA + (int64_t)kt * p.a_rows + (MODE == kGateUp ? 0 : row0);
+      const auto rS = make_rsrc(s, (MODE == kGateUp ? p.a_rows : (int64_t)rows) * 4);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rS, (lds_void*)(base + C::kCodes + wave * 256), 4, soff, 0, 0, 0);
+    }
+  };
+
+  const int wm = wave % WGM, wn = wave / WGM;
+  const int r16 = lane & 15, g = lane >> 4;
+  // weight blocks of the wave's column tiles (gate/up: even tiles are gate columns, odd ones up columns)
+  const float* sBe = p.sB + (int64_t)e * nb * nk;
+  constexpr int kBlocks = MODE == kGateUp ? 2 : 128 % C::WN == 0 ? 1 : C::SN;
+  const float* sBp[kBlocks];
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    const int b = MODE == kGateUp ? nt + i * (nb >> 1) : min((n0 + wn * C::WN + i * 16) >> 7, nb - 1);
+    sBp[i] = sBe + (int64_t)b * nk;
+  }
+  v4f acc[C::SN][C::SM];
+#pragma unroll
+  for (int i = 0; i < C::SN; ++i)
+#pragma unroll
+    for (int j = 0; j < C::SM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  issue(0, 0);
+  for (int kt = 0; kt < nk; ++kt) {
+    float sw[kBlocks];
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) sw[i] = sBp[i][kt];
+    wait_vmem_all();
+    __syncthreads();
+    if (kt + 1 < nk) issue((kt + 1) & 1, kt + 1);
+    const uint8_t* st = smem + (kt & 1) * C::kStage;
+    v8i xf[C::SM];
+    float sx[C::SM];
+#pragma unroll
+    for (int j = 0; j < C::SM; ++j) {
+      const int r = wm * C::WM + j * 16 + r16;
+      xf[j] = lds_frag(st, BN + r, g);
+      sx[j] = *reinterpret_cast<const float*>(st + C::kCodes + r * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < C::SN; ++i) {
+      const v8i wf = lds_frag(st, wn * C::WN + i * 16 + r16, g);
+#pragma unroll
+      for (int j = 0; j < C::SM; ++j) {
+        const v4f d = mfma_16x16x128_e4m3(wf, xf[j], v4f{0.f, 0.f, 0.f, 0.f});
+        const float s = sx[j] * sw[i % kBlocks];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s, acc[i][j][r]);
+      }
+    }
+  }
+  __syncthreads();
+
+  // acc[i][j][r]: tile row wm WM + 16 j + lane % 16, stage row wn WN + 16 i + 4 (lane / 16) + r
+  if constexpr (MODE == kDense) {
+#pragma unroll
+    for (int i = 0; i < C::SN; ++i) {
+      const int nl = wn * C::WN + i * 16 + 4 * g;
+#pragma unroll
+      for (int j = 0; j < C::SM; ++j) {
+        const int ml = wm * C::WM + j * 16 + r16;
+        const v4f a = acc[i][j];
+        *reinterpret_cast<uint2*>(smem + ml * C::kEpiStride + nl * 2) =
+            make_uint2(bf16x2_rne(a[0], a[1]), bf16x2_rne(a[2], a[3]));
+      }
+    }
+    __syncthreads();
+    constexpr int kRowChunks = BN / 8;
+    for (int c = tid; c < BM * kRowChunks; c += C::kThreads) {
+      const int row = c / kRowChunks, col = (c % kRowChunks) * 8;
+      if (row < rows && n0 + col < N)
+        store16_nt(p.y + (int64_t)(row0 + row) * N + n0 + col,
+                   *reinterpret_cast<const uint4*>(smem + row * C::kEpiStride + col * 2));
+    }
+  }
+  if constexpr (MODE == kGateUp) {
+    // maxima of |h| on the bits, where infinity and NaN come last and reach the
+    // scale, and through it the token
+    uint32_t* const rmax = reinterpret_cast<uint32_t*>(smem + BM * C::kHStride);  // [WGN][BM]
+    uint32_t am[C::SM];
+#pragma unroll
+    for (int j = 0; j < C::SM; ++j) {
+      am[j] = 0u;
+#pragma unroll
+      for (int i = 0; i < C::SN; i += 2)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float h = silu_f32(acc[i][j][r]) * acc[i + 1][j][r];
+          acc[i][j][r] = h;
+          am[j] = max(am[j], __float_as_uint(h) & 0x7FFFFFFFu);
+        }
+      am[j] = max(am[j], (uint32_t)__shfl_xor((int)am[j], 16, 64));
+      am[j] = max(am[j], (uint32_t)__shfl_xor((int)am[j], 32, 64));
+      if (g == 0) rmax[wn * BM + wm * C::WM + j * 16 + r16] = am[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < C::SM; ++j) {
+      const int ml = wm * C::WM + j * 16 + r16;
+      uint32_t a = 0u;
+#pragma unroll
+      for (int w = 0; w < WGN; ++w) a = max(a, rmax[w * BM + ml]);
+      const float s = a == 0u ? 1.0f : __uint_as_float(a) / 448.0f, inv = 1.0f / s;
+      if (wn == 0 && g == 0 && ml < rows) p.hs[(int64_t)nt * (p.a_rows * p.topk) + row0 + ml] = s;
+#pragma unroll
+      for (int i = 0; i < C::SN; i += 2) {
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          // the quotient by one residual correction (quant8); tiny scales divide
+          const float h = acc[i][j][r], q0 = h * inv;
+          v[r] = clamp448(s >= kQuotientMinScale ? __builtin_fmaf(__builtin_fmaf(-q0, s, h), inv, q0) : h / s);
+        }
+        const int hc = ((wn * C::WN + i * 16) >> 1) + 4 * g;
+        *reinterpret_cast<uint32_t*>(smem + ml * C::kHStride + hc) = e4m3x4(v[0], v[1], v[2], v[3]);
+      }
+    }
+    __syncthreads();
+    for (int c = tid; c < BM * 8; c += C::kThreads) {
+      const int row = c >> 3, col = (c & 7) << 4;
+      if (row < rows)
+        *reinterpret_cast<uint4*>(p.hq + (int64_t)(row0 + row) * (N / 2) + (n0 >> 1) + col) =
+            *reinterpret_cast<const uint4*>(smem + row * C::kHStride + col);
+    }
+  }
+  if constexpr (MODE == kDown) {
+    // a wm's rows at a time through LDS, so that stores are whole row pieces;
+    // 16-byte chunks swizzled by row against bank conflicts
+    constexpr int kChunks = BN / 4;
+    static_assert(kChunks >= 16, "the swizzle exchanges 16 chunks");
+#pragma unroll
+    for (int pw = 0; pw < WGM; ++pw) {
+      if (pw) __syncthreads();
+      if (wm == pw) {
+#pragma unroll
+        for (int j = 0; j < C::SM; ++j) {
+          const int rl = j * 16 + r16;
+          const float w = row_w[pw * C::WM + rl];
+#pragma unroll
+          for (int i = 0; i < C::SN; ++i) {
+            const int chunk = (wn * C::WN + i * 16) / 4 + g;
+            const v4f a = acc[i][j];
+            *reinterpret_cast<float4*>(smem + rl * (BN * 4) + ((chunk ^ (rl & 15)) << 4)) =
+                make_float4(a[0] * w, a[1] * w, a[2] * w, a[3] * w);
+          }
+        }
+      }
+      __syncthreads();
+      for (int c = tid; c < C::WM * kChunks; c += C::kThreads) {
+        const int rl = c / kChunks, ch = c % kChunks, ml = pw * C::WM + rl;
+        if (row_slot[ml] >= 0 && n0 + ch * 4 < N)
+          store16_nt(p.y32 + (int64_t)(row0 + ml) * N + n0 + ch * 4,
+                     *reinterpret_cast<const float4*>(smem + rl * (BN * 4) + ((ch ^ (rl & 15)) << 4)));
+      }
+    }
+  }
+}
+
+// The combine with the next pass's quantisation by blocks: 16 threads sum a
+// block of 128 columns of a token (in the order of combine_slots) and quantise
+// it as quantize_blocks does.
+__global__ __launch_bounds__(256) void combine_block_quant(const float* __restrict__ y, const int32_t* __restrict__ ids,
+                                                           const int32_t* __restrict__ slot_row, int64_t T, int topk,
+                                                           int E, int H, uint16_t* __restrict__ out,
+                                                           uint8_t* __restrict__ q, float* __restrict__ scale) {
+  const int kb = (H + 127) >> 7;
+  const int64_t b = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int64_t t = b / kb;
+  if (t >= T) return;
+  const int blk = (int)(b - t * kb), c = blk * 128 + 8 * (threadIdx.x & 15);
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (c < H) {
+    float4 lo, hi;
+    sum_slots8(y, ids, slot_row, t, topk, E, H, c, lo, hi);
+    v = to_bf16x8(lo, hi);
+    *reinterpret_cast<uint4*>(out + t * H + c) = v;
+  }
+  const float s = row_scale(row16_max(absmax8(v)));
+  if (c < H) *reinterpret_cast<uint2*>(q + t * H + c) = quant8(v, s, 1.0f / s);
+  if ((threadIdx.x & 15) == 0) scale[(int64_t)blk * T + t] = s;
+}
+
+template <int BM, int BN, int WGM, int WGN, int MODE>
+hipError_t run_tiled(BlockArgs a, hipStream_t stream) {
+  a.tiles_n = (a.N + BN - 1) / BN;
+  const int64_t cap = MODE == kGateUp ? a.a_rows * a.topk : a.a_rows;
+  a.tiles_m = (int)((cap + BM - 1) / BM + (MODE == kDense ? 0 : a.E));  // a group adds at most one partial tile
+  hipLaunchKernelGGL((block_tiled<BM, BN, WGM, WGN, MODE>), dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)),
+                     dim3(64 * WGM * WGN), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <bool Q>
+hipError_t run_skinny(const void* x, const float* sa, const uint8_t* w, const float* sw, uint16_t* y, int64_t M,
+                      int64_t N, int64_t K, hipStream_t stream) {
+  if (M <= 16)
+    hipLaunchKernelGGL((block_skinny<1, 4, 1, Q>), dim3((unsigned)((N + 15) / 16)), dim3(256), 0, stream, x, sa, w, sw, y,
+                       (int)M, (int)N, (int)K);
+  else
+    hipLaunchKernelGGL((block_skinny<2, 2, 2, Q>), dim3((unsigned)((N + 31) / 32)), dim3(256), 0, stream, x, sa, w, sw, y,
+                       (int)M, (int)N, (int)K);
+  return hipGetLastError();
+}
+
+int64_t align256(int64_t b) { return (b + 255) & ~int64_t(255); }
+
+}  // namespace
+
+hipError_t launch_quantize_blocks(const uint16_t* x, int64_t M, int64_t K, uint8_t* q, float* scale,
+                                  hipStream_t stream) {
+  const int64_t kb = (K + 127) / 128;
+  hipLaunchKernelGGL(quant_row_blocks,
+                     dim3((unsigned)((M + kQuantRows - 1) / kQuantRows), (unsigned)((kb + kQuantBlocks - 1) / kQuantBlocks)),
+                     dim3(256), 0, stream, x, M, K, q, scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_weight_blocks(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* q, float* scale,
+                                         hipStream_t stream) {
+  const int64_t nb = (N + 127) / 128, kb = (K + 127) / 128;
+  hipLaunchKernelGGL(quant_weight_blocks, dim3((unsigned)(E * nb * kb)), dim3(256), 0, stream, w, N, K, (int)nb, (int)kb, q,
+                     scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, uint16_t* y,
+                             int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  if (M <= kBlockSkinnyM) return run_skinny<false>(a, sa, w, sw, y, M, N, K, stream);
+  BlockArgs p{};
+  p.A = a;
+  p.sA = sa;
+  p.a_rows = M;
+  p.B = w;
+  p.sB = sw;
+  p.y = y;
+  p.E = 1;
+  p.topk = 1;
+  p.N = (int)N;
+  p.K = (int)K;
+  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256), mid = ((M + 127) / 128) * ((N + 127) / 128);
+  if (big >= 256) return run_tiled<256, 256, 2, 4, kDense>(p, stream);
+  if (mid >= 256) return run_tiled<128, 128, 2, 2, kDense>(p, stream);
+  return run_tiled<64, 64, 2, 2, kDense>(p, stream);
+}
+
+hipError_t launch_block_linear(const uint16_t* x, const uint8_t* w, const float* sw, uint16_t* y, int64_t M, int64_t N,
+                               int64_t K, void* ws, hipStream_t stream) {
+  if (M <= kBlockSkinnyM) return run_skinny<true>(x, nullptr, w, sw, y, M, N, K, stream);
+  uint8_t* q = static_cast<uint8_t*>(ws);
+  float* s = reinterpret_cast<float*>(q + align256(M * K));
+  const hipError_t e = launch_quantize_blocks(x, M, K, q, s, stream);
+  if (e != hipSuccess) return e;
+  return launch_block_gemm(q, s, w, sw, y, M, N, K, stream);
+}
+
+size_t block_linear_workspace_bytes(int64_t M, int64_t K) {
+  if (M <= kBlockSkinnyM) return 0;
+  return (size_t)(align256(M * K) + align256((K + 127) / 128 * M * 4));
+}
+
+// counts | offsets | perm | route scratch | codes of h | their scales | slot -> row | y
+struct BlockMoeLayout {
+  int64_t counts, offsets, perm, route, hq, hs, slot_row, y, total;
+};
+
+static BlockMoeLayout block_moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
+  BlockMoeLayout L;
+  const int64_t n = T * topk;
+  int64_t o = 0;
+  L.counts = o, o += align256(E * 4);
+  L.offsets = o, o += align256((E + 1) * 4);
+  L.perm = o, o += align256(n * 4);
+  L.route = o, o += (int64_t)route_workspace_bytes(T, topk, E);
+  L.hq = o, o += align256(n * I);
+  L.hs = o, o += align256(I / 128 * n * 4);
+  L.slot_row = o, o += align256(n * 4);
+  L.y = o, o += align256(n * H * 4);
+  L.total = o;
+  return L;
+}
+
+size_t block_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
+  return (size_t)block_moe_layout(T, H, I, E, topk).total;
+}
+
+hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* ids, const float* tw, const uint8_t* w13,
+                            const float* s13, const uint8_t* w2, const float* s2, uint16_t* out, uint8_t* out_q,
+                            float* out_s, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, void* ws,
+                            hipStream_t stream) {
+  const BlockMoeLayout L = block_moe_layout(T, H, I, E, topk);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  int32_t* const offsets = reinterpret_cast<int32_t*>(b + L.offsets);
+  int32_t* const perm = reinterpret_cast<int32_t*>(b + L.perm);
+  int32_t* const slot_row = reinterpret_cast<int32_t*>(b + L.slot_row);
+  float* const y = reinterpret_cast<float*>(b + L.y);
+  hipError_t err = launch_route(ids, T, topk, E, 0, reinterpret_cast<int32_t*>(b + L.counts), offsets, perm, nullptr,
+                                b + L.route, stream);
+  if (err != hipSuccess) return err;
+  BlockArgs p{};
+  p.A = xq;
+  p.sA = xs;
+  p.a_rows = T;
+  p.B = w13;
+  p.sB = s13;
+  p.perm = perm;
+  p.offsets = offsets;
+  p.hq = b + L.hq;
+  p.hs = reinterpret_cast<float*>(b + L.hs);
+  p.E = (int)E;
+  p.topk = (int)topk;
+  p.N = (int)(2 * I);
+  p.K = (int)H;
+  const int64_t avg = T * topk / E;
+  if (avg < 64)
+    err = run_tiled<64, 256, 1, 4, kGateUp>(p, stream);
+  else
+    err = run_tiled<128, 256, 2, 4, kGateUp>(p, stream);
+  if (err != hipSuccess) return err;
+  BlockArgs d = p;
+  d.A = p.hq;
+  d.sA = p.hs;
+  d.a_rows = T * topk;
+  d.B = w2;
+  d.sB = s2;
+  d.tw = tw;
+  d.y32 = y;
+  d.slot_row = slot_row;
+  d.N = (int)H;
+  d.K = (int)I;
+  if (avg < 64)
+    err = run_tiled<64, 128, 1, 2, kDown>(d, stream);
+  else
+    err = run_tiled<128, 128, 2, 2, kDown>(d, stream);
+  if (err != hipSuccess) return err;
+  if (out_q == nullptr) return launch_combine(y, ids, slot_row, T, topk, E, H, out, stream);
+  const int64_t groups = T * ((H + 127) / 128);
+  hipLaunchKernelGGL(combine_block_quant, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, stream, y, ids, slot_row, T,
+                     (int)topk, (int)E, (int)H, out, out_q, out_s);
+  return hipGetLastError();
+}
+
+}  // namespace w8a8

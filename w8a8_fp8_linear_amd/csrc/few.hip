@@ -111,6 +111,7 @@ struct RouterArgs {
   float* tw;           // [T, k]
   int T, H, E, k, sigmoid, renorm;
   float scale;
+  float* logits32;     // [T, E] or NULL
 };
 
 // Few tokens: a wave per expert, lanes along K, TT tokens. One round of load
@@ -301,6 +302,8 @@ __global__ __launch_bounds__(64) void router_select(const RouterArgs p) {
     p.ids[(int64_t)t * p.k + lane] = id;
     p.tw[(int64_t)t * p.k + lane] = tw;
   }
+  if (p.logits32 != nullptr)
+    for (int e = lane; e < p.E; e += 64) p.logits32[(int64_t)t * p.E + e] = (float)p.logits[(int64_t)t * p.E + e];
 }
 
 // ---- experts -----------------------------------------------------------------
@@ -1079,7 +1082,7 @@ static hipError_t launch_router(const RouterArgs& a, hipStream_t stream) {
 
 hipError_t launch_router(const Router& r, int64_t T, int64_t H, int64_t E, int64_t topk, void* ws, hipStream_t stream) {
   return launch_router(RouterArgs{r.x, r.wr, r.bias, static_cast<double*>(ws), r.ids, r.tw, (int)T, (int)H, (int)E,
-                                  (int)topk, r.sigmoid, r.renorm, r.scale},
+                                  (int)topk, r.sigmoid, r.renorm, r.scale, r.logits},
                        stream);
 }
 
@@ -1106,7 +1109,7 @@ hipError_t launch_few(const Few& f, const Router* r, int64_t T, int64_t H, int64
   const bool fused = r && few_routes(a);
   if (r) {
     route = RouterArgs{r->x, r->wr, r->bias, reinterpret_cast<double*>(rest), r->ids, r->tw, (int)T, (int)H, (int)E,
-                       (int)topk, r->sigmoid, r->renorm, r->scale};
+                       (int)topk, r->sigmoid, r->renorm, r->scale, nullptr};
     const hipError_t e = fused ? launch_logits(route, stream) : launch_router(route, stream);
     if (e != hipSuccess) return e;
   }

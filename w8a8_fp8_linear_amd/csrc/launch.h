@@ -76,6 +76,11 @@ hipError_t launch_gate_up_swiglu_quant(const uint8_t* xq, const float* xs, const
                                        int64_t H, int64_t I, int64_t E, int64_t topk, int order, void* ws,
                                        hipStream_t stream, bool amax_zeroed = false);
 
+// out[t] = bf16(sum over the token's valid slots j = 0, 1, ... of its float32
+// row of y): row t * topk + j, or slot_row's where given.
+hipError_t launch_combine(const float* y, const int32_t* ids, const int32_t* slot_row, int64_t T, int64_t topk, int64_t E,
+                          int64_t H, uint16_t* out, hipStream_t stream);
+
 // y: [T*topk, H] float32 scratch (down_combine_scratch_bytes).
 size_t down_combine_scratch_bytes(int64_t T, int64_t H, int64_t topk);
 // out_q / out_s (both NULL or both set): also quantize_per_token(out).
@@ -149,6 +154,7 @@ struct Router {
   float* tw;               // [T, topk]
   int sigmoid, renorm;
   float scale;
+  float* logits;           // [T, E] or NULL: the logits rounded to float32
 };
 size_t router_workspace_bytes(int64_t T, int64_t E);
 hipError_t launch_router(const Router& r, int64_t T, int64_t H, int64_t E, int64_t topk, void* ws, hipStream_t stream);
@@ -172,5 +178,41 @@ size_t few_layer_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int
 // is then few_layer_workspace_bytes, else few_workspace_bytes.
 hipError_t launch_few(const Few& f, const Router* r, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, void* ws,
                       hipStream_t stream);
+
+// FP8 with a scale per block of 128 (block.hip): rows [M, K] with scales
+// [blocks of K, M], weights [E, N, K] with scales [E, blocks of N, blocks of K].
+hipError_t launch_quantize_blocks(const uint16_t* x, int64_t M, int64_t K, uint8_t* q, float* scale,
+                                  hipStream_t stream);
+hipError_t launch_quantize_weight_blocks(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* q, float* scale,
+                                         hipStream_t stream);
+hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, uint16_t* y,
+                             int64_t M, int64_t N, int64_t K, hipStream_t stream);
+// The layer on BF16 input. ws: block_linear_workspace_bytes bytes (0 up to
+// kBlockSkinnyM rows, which are quantised inside the product).
+constexpr int64_t kBlockSkinnyM = 32;
+size_t block_linear_workspace_bytes(int64_t M, int64_t K);
+hipError_t launch_block_linear(const uint16_t* x, const uint8_t* w, const float* sw, uint16_t* y, int64_t M, int64_t N,
+                               int64_t K, void* ws, hipStream_t stream);
+// The routed-expert pass; out_q / out_s (both NULL or both set): also
+// quantize_blocks(out).
+size_t block_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk);
+hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* ids, const float* tw, const uint8_t* w13,
+                            const float* s13, const uint8_t* w2, const float* s2, uint16_t* out, uint8_t* out_q,
+                            float* out_s, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, void* ws,
+                            hipStream_t stream);
+
+// The balance loss (balance.hip): T tokens in S sequences of one length.
+struct Balance {
+  const void* logits;  // [T, E] float32 or BF16
+  const int32_t* ids;  // [T, topk]
+  float* loss;         // [1]
+  int32_t* counts;     // [S, E]
+  void* grad;          // [T, E] or NULL, the logits' type
+  int bf16, sigmoid;
+  float coef;
+};
+size_t balance_workspace_bytes(int64_t T, int64_t S, int64_t E);
+hipError_t launch_balance(const Balance& b, int64_t T, int64_t S, int64_t E, int64_t topk, void* ws,
+                          hipStream_t stream);
 
 }  // namespace w8a8

@@ -832,6 +832,14 @@ hipError_t launch_gate_up_swiglu_quant(const uint8_t* xq, const float* xs, const
   return hipGetLastError();
 }
 
+hipError_t launch_combine(const float* y, const int32_t* ids, const int32_t* slot_row, int64_t T, int64_t topk, int64_t E,
+                          int64_t H, uint16_t* out, hipStream_t stream) {
+  const int64_t threads = T * (H / 8);
+  hipLaunchKernelGGL(combine_slots, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, y, ids, slot_row, T,
+                     (int)topk, (int)E, (int)H, out);
+  return hipGetLastError();
+}
+
 // Down projection of the sorted rows (any order: every slot's product goes
 // to its own row of y, or with slot_row to its sorted row), then the
 // per-token combine.
@@ -867,12 +875,9 @@ hipError_t launch_down_combine(const uint8_t* qh, const float* sh, const int32_t
       hipLaunchKernelGGL(combine_quant<4>, grid, dim3(256), 0, stream, y, ids, slot_row, (int)topk, (int)E, (int)H, out, out_q, out_s);
     return hipGetLastError();
   }
-  const int64_t threads = T * (H / 8);
-  hipLaunchKernelGGL(combine_slots, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, y, ids, slot_row, T,
-                     (int)topk, (int)E, (int)H, out);
-  if (out_q == nullptr) return hipGetLastError();
-  const hipError_t cerr = hipGetLastError();  // rows longer than the fused kernel holds: quantise separately
-  if (cerr != hipSuccess) return cerr;
+  const hipError_t cerr = launch_combine(y, ids, slot_row, T, topk, E, H, out, stream);
+  if (out_q == nullptr || cerr != hipSuccess) return cerr;
+  // rows longer than the fused kernel holds: quantise separately
   return launch_quantize_rows(out, T, H, out_q, out_s, stream);
 }
 
