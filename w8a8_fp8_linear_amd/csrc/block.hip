@@ -232,15 +232,16 @@ struct BlockArgs {
   int E, topk, N, K, tiles_m, tiles_n;
 };
 
-template <int BM, int BN, int WGM, int WGN, int MODE>
+template <int BM, int BN, int WGM, int WGN, int MODE, bool PP>
 struct BlockTile {
   static constexpr int kThreads = 64 * WGM * WGN;
+  static constexpr int kLoaders = PP ? kThreads / 2 : kThreads;  // threads that issue the loads
   static constexpr int WM = BM / WGM, WN = BN / WGN;  // a wave's part
   static constexpr int SM = WM / 16, SN = WN / 16;
   static constexpr int kRows = BM + BN;
   static constexpr int kCodes = kRows * 128;                              // bytes of a stage's codes
   static constexpr int kStage = kCodes + (BM * 4 + 1023) / 1024 * 1024;   // and its row scales
-  static constexpr int kRowsPerPass = kThreads / 8;
+  static constexpr int kRowsPerPass = kLoaders / 8;
   static constexpr int kLoadsB = BN / kRowsPerPass, kLoadsA = BM / kRowsPerPass;
   static constexpr int kEpiStride = BN * 2 + 16;  // dense: staged BF16 row
   static constexpr int kHStride = 128 + 16;       // gate/up: staged row of h codes
@@ -248,9 +249,51 @@ struct BlockTile {
                               : MODE == kGateUp ? BM * kHStride + WGN * BM * 4 : WM * BN * 4;
   static constexpr int kLds = 2 * kStage > kEpi ? 2 * kStage : kEpi;
   static_assert(BN % kRowsPerPass == 0 && BM % kRowsPerPass == 0 && kRowsPerPass % 8 == 0, "stages split evenly");
-  static_assert(WM % 16 == 0 && WN % 16 == 0 && BM % 64 == 0 && BM / 64 <= WGM * WGN, "wave tiles");
+  static_assert(WM % 16 == 0 && WN % 16 == 0 && BM % 64 == 0 && BM / 64 <= kLoaders / 64, "wave tiles");
+  static_assert(!PP || (WGM == 2 && BM / 64 == kLoaders / 64), "ping-pong: two groups, a scale load for each loading wave");
   static_assert(MODE != kGateUp || (BN == 256 && SN % 2 == 0), "a gate/up tile is one block of 128 h columns");
 };
+
+// acc[i][j] += (w_i . x_j) * (sx[j] * sw[i]): kAhead MFMAs are under way before
+// the first result is added, then every MFMA is followed by the four FMAs of an
+// earlier one, which run while the matrix unit works.
+template <int SN, int SM, int NB>
+__device__ inline void scaled_mfmas(v4f (&acc)[SN][SM], const v8i (&wf)[SN], const v8i (&xf)[SM], const float (&sx)[SM],
+                                    const float (&sw)[NB]) {
+  constexpr int kAhead = 2, kN = SN * SM;
+#pragma unroll
+  for (int i = 0; i < SN; ++i)
+#pragma unroll
+    for (int j = 0; j < SM; ++j) {
+      const v4f d = mfma_16x16x128_e4m3(wf[i], xf[j], v4f{0.f, 0.f, 0.f, 0.f});
+      const float s = sx[j] * sw[i % NB];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s, acc[i][j][r]);
+    }
+  // the order of issue: groups of MFMAs (mask 8) and vector instructions (2)
+  __builtin_amdgcn_sched_group_barrier(8, kAhead, 0);
+#pragma unroll
+  for (int n = kAhead; n < kN; ++n) {
+    __builtin_amdgcn_sched_group_barrier(8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(2, 5, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(2, 5 * kAhead, 0);
+  // every sum is there by here: left free, the compiler holds all results of a step in registers and adds them later
+#pragma unroll
+  for (int i = 0; i < SN; ++i)
+#pragma unroll
+    for (int j = 0; j < SM; ++j) asm volatile("" : "+v"(acc[i][j]));
+}
+
+// Fragment of the 16 staged rows from `row0` on, lds_frag's chunks c and c + 4
+// of this lane's row: lane_off is the lane's own offset (its row lane % 16 and
+// chunk), so that every fragment of a stage is one address and a constant.
+__device__ inline int frag_lane_off(int r16, int g) { return r16 * 128 + ((g ^ (r16 & 7)) << 4); }
+__device__ inline v8i frag_at(const uint8_t* st, int lane_off, int row0) {
+  const v4i lo = *reinterpret_cast<const v4i*>(st + lane_off + row0 * 128);
+  const v4i hi = *reinterpret_cast<const v4i*>(st + (lane_off ^ 64) + row0 * 128);
+  return v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+}
 
 // One 128-deep K step is one block of scales. Stages are double-buffered in
 // LDS: the codes by direct 16-byte loads (rows of 128 bytes, 16-byte pieces
@@ -263,10 +306,13 @@ struct BlockTile {
 //           in one lane. A tile's 128 columns of h are one block: its row maxima
 //           meet in LDS, and h leaves as codes and scales.
 //  kDown    y32 = router weight * (h . w2^T), a float32 row per sorted row.
-template <int BM, int BN, int WGM, int WGN, int MODE>
-__global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(1, 2)))
+// PP: two groups of waves take turns: one reads its fragments of a step from
+// LDS while the other issues the MFMAs of the step that it read before; group
+// 0 issues all loads, a step ahead.
+template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, bool PP>
+__global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(1, OCC)))
 void block_tiled(const BlockArgs p) {
-  using C = BlockTile<BM, BN, WGM, WGN, MODE>;
+  using C = BlockTile<BM, BN, WGM, WGN, MODE, PP>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds + (MODE == kDense ? 0 : BM * 8)];
   int* const row_slot = reinterpret_cast<int*>(smem + C::kLds);                // slot of a tile row, -1: none
   float* const row_w = reinterpret_cast<float*>(smem + C::kLds + BM * 4);      // its router weight
@@ -307,24 +353,33 @@ void block_tiled(const BlockArgs p) {
 
   const int lchunk = ((tid & 7) ^ ((tid >> 3) & 7)) << 4;
   const int lrow = tid >> 3;
-  uint32_t boff[C::kLoadsB], aoff[C::kLoadsA];
+  // Byte offset of a thread's i-th 16-byte piece at K = 0. Rows past the end lie
+  // outside the buffer and read as zeros. A gathered row's offset is kept in a
+  // register, the others follow from the first.
+  const uint32_t lbase = (uint32_t)lrow * (uint32_t)K + (uint32_t)lchunk;
+  uint32_t arow[MODE == kGateUp ? C::kLoadsA : 1];
+  if constexpr (MODE == kGateUp) {
 #pragma unroll
-  for (int i = 0; i < C::kLoadsB; ++i) {
-    const int r = lrow + C::kRowsPerPass * i;
-    int wr = r;
-    if (MODE == kGateUp) wr = ((r >> 4) & 1 ? N / 2 : 0) + (n0 >> 1) + (r >> 5) * 16 + (r & 15);
-    boff[i] = (uint32_t)wr * (uint32_t)K + (uint32_t)lchunk;
-  }
-#pragma unroll
-  for (int j = 0; j < C::kLoadsA; ++j) {
-    const int r = lrow + C::kRowsPerPass * j;
-    if constexpr (MODE == kGateUp) {
-      const int slot = row_slot[r];
-      aoff[j] = slot < 0 ? kOutOfRange : (uint32_t)(slot / p.topk) * (uint32_t)K + (uint32_t)lchunk;
-    } else {
-      aoff[j] = r < rows ? (uint32_t)r * (uint32_t)K + (uint32_t)lchunk : kOutOfRange;
+    for (int j = 0; j < C::kLoadsA; ++j) {
+      const int slot = row_slot[lrow + C::kRowsPerPass * j];
+      arow[j] = slot < 0 ? kOutOfRange : (uint32_t)(slot / p.topk) * (uint32_t)K + (uint32_t)lchunk;
     }
   }
+  auto boff = [&](int i) {
+    if constexpr (MODE == kGateUp) {  // 16-row piece b: even = gate rows, odd = the matching up rows
+      const int r = lrow + C::kRowsPerPass * i;
+      const int wr = ((r >> 4) & 1 ? N / 2 : 0) + (n0 >> 1) + (r >> 5) * 16 + (r & 15);
+      return (uint32_t)wr * (uint32_t)K + (uint32_t)lchunk;
+    } else {
+      return lbase + (uint32_t)(C::kRowsPerPass * i) * (uint32_t)K;
+    }
+  };
+  auto aoff = [&](int j) {
+    if constexpr (MODE == kGateUp)
+      return arow[j];
+    else
+      return lbase + (uint32_t)(C::kRowsPerPass * j) * (uint32_t)K;
+  };
   // this lane's row scale of a step: lane l of wave w < BM / 64 loads row 64 w + l
   uint32_t soff = kOutOfRange;
   if (wave < BM / 64) {
@@ -342,11 +397,11 @@ void block_tiled(const BlockArgs p) {
     const bool kin = k0 + lchunk < K;
 #pragma unroll
     for (int i = 0; i < C::kLoadsB + C::kLoadsA; ++i) {
-      const int s0 = wave * 64 + C::kThreads * i;
+      const int s0 = wave * 64 + C::kLoaders * i;
       if (i < C::kLoadsB) {
-        buffer_load16_lds(rB, base + s0 * 16, kin ? boff[i] + (uint32_t)k0 : kOutOfRange);
+        buffer_load16_lds(rB, base + s0 * 16, kin ? boff(i) + (uint32_t)k0 : kOutOfRange);
       } else {
-        const uint32_t a = aoff[i - C::kLoadsB];
+        const uint32_t a = aoff(i - C::kLoadsB);
         buffer_load16_lds(rA, base + s0 * 16, kin && a != kOutOfRange ? a + (uint32_t)k0 : kOutOfRange);
       }
     }
@@ -357,16 +412,20 @@ void block_tiled(const BlockArgs p) {
     }
   };
 
-  const int wm = wave % WGM, wn = wave / WGM;
+  const int wm = PP ? wave / WGN : wave % WGM, wn = PP ? wave % WGN : wave / WGM;
   const int r16 = lane & 15, g = lane >> 4;
+  const int lane_off = frag_lane_off(r16, g);
+  const int a_base = (BN + wm * C::WM) * 128, b_base = wn * C::WN * 128, s_base = C::kCodes + (wm * C::WM + r16) * 4;
   // weight blocks of the wave's column tiles (gate/up: even tiles are gate columns, odd ones up columns)
   const float* sBe = p.sB + (int64_t)e * nb * nk;
   constexpr int kBlocks = MODE == kGateUp ? 2 : 128 % C::WN == 0 ? 1 : C::SN;
-  const float* sBp[kBlocks];
+  // read through the constant address space: scalar loads, whose counter is not that of the loads into LDS
+  typedef const __attribute__((address_space(4))) float* ScalarPtr;
+  ScalarPtr sBp[kBlocks];
 #pragma unroll
   for (int i = 0; i < kBlocks; ++i) {
     const int b = MODE == kGateUp ? nt + i * (nb >> 1) : min((n0 + wn * C::WN + i * 16) >> 7, nb - 1);
-    sBp[i] = sBe + (int64_t)b * nk;
+    sBp[i] = (ScalarPtr)(sBe + (int64_t)b * nk);
   }
   v4f acc[C::SN][C::SM];
 #pragma unroll
@@ -374,32 +433,68 @@ void block_tiled(const BlockArgs p) {
 #pragma unroll
     for (int j = 0; j < C::SM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  issue(0, 0);
-  for (int kt = 0; kt < nk; ++kt) {
-    float sw[kBlocks];
-#pragma unroll
-    for (int i = 0; i < kBlocks; ++i) sw[i] = sBp[i][kt];
-    wait_vmem_all();
-    __syncthreads();
-    if (kt + 1 < nk) issue((kt + 1) & 1, kt + 1);
-    const uint8_t* st = smem + (kt & 1) * C::kStage;
-    v8i xf[C::SM];
-    float sx[C::SM];
-#pragma unroll
-    for (int j = 0; j < C::SM; ++j) {
-      const int r = wm * C::WM + j * 16 + r16;
-      xf[j] = lds_frag(st, BN + r, g);
-      sx[j] = *reinterpret_cast<const float*>(st + C::kCodes + r * 4);
+  if constexpr (PP) {
+    const bool loader = wm == 0;
+    if (loader) {
+      issue(0, 0);
+      if (nk > 1) {
+        issue(1, 1);
+        wait_vmcnt<C::kLoadsB + C::kLoadsA + 1>();
+      } else {
+        wait_vmem_all();
+      }
     }
+    lds_barrier();
+    if (!loader) lds_barrier();
+    for (int kt = 0; kt < nk; ++kt) {
+      if (loader && kt >= 1 && kt + 1 < nk) issue((kt + 1) & 1, kt + 1);
+      const uint8_t* st = smem + (kt & 1) * C::kStage;
+      v8i xf[C::SM], wf[C::SN];
+      float sx[C::SM], sw[kBlocks];
 #pragma unroll
-    for (int i = 0; i < C::SN; ++i) {
-      const v8i wf = lds_frag(st, wn * C::WN + i * 16 + r16, g);
+      for (int i = 0; i < kBlocks; ++i) sw[i] = sBp[i][kt];
 #pragma unroll
       for (int j = 0; j < C::SM; ++j) {
-        const v4f d = mfma_16x16x128_e4m3(wf, xf[j], v4f{0.f, 0.f, 0.f, 0.f});
-        const float s = sx[j] * sw[i % kBlocks];
+        xf[j] = frag_at(st + a_base, lane_off, j * 16);
+        sx[j] = *reinterpret_cast<const float*>(st + s_base + j * 64);
+      }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s, acc[i][j][r]);
+      for (int i = 0; i < C::SN; ++i) wf[i] = frag_at(st + b_base, lane_off, i * 16);
+      lds_barrier();
+      scaled_mfmas<C::SN, C::SM, kBlocks>(acc, wf, xf, sx, sw);
+      // the wait stays behind the MFMAs (an s_waitcnt is no scheduling barrier)
+      __builtin_amdgcn_sched_barrier(0);
+      if (loader) wait_vmem_all();
+      lds_barrier();
+    }
+    if (loader) lds_barrier();
+  } else {
+    issue(0, 0);
+    for (int kt = 0; kt < nk; ++kt) {
+      float sw[kBlocks];
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) sw[i] = sBp[i][kt];
+      wait_vmem_all();
+      __syncthreads();
+      if (kt + 1 < nk) issue((kt + 1) & 1, kt + 1);
+      const uint8_t* st = smem + (kt & 1) * C::kStage;
+      v8i xf[C::SM];
+      float sx[C::SM];
+#pragma unroll
+      for (int j = 0; j < C::SM; ++j) {
+        xf[j] = frag_at(st + a_base, lane_off, j * 16);
+        sx[j] = *reinterpret_cast<const float*>(st + s_base + j * 64);
+      }
+#pragma unroll
+      for (int i = 0; i < C::SN; ++i) {
+        const v8i wf = frag_at(st + b_base, lane_off, i * 16);
+#pragma unroll
+        for (int j = 0; j < C::SM; ++j) {
+          const v4f d = mfma_16x16x128_e4m3(wf, xf[j], v4f{0.f, 0.f, 0.f, 0.f});
+          const float s = sx[j] * sw[i % kBlocks];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s, acc[i][j][r]);
+        }
       }
     }
   }
@@ -534,12 +629,12 @@ __global__ __launch_bounds__(256) void combine_block_quant(const float* __restri
   if ((threadIdx.x & 15) == 0) scale[(int64_t)blk * T + t] = s;
 }
 
-template <int BM, int BN, int WGM, int WGN, int MODE>
+template <int BM, int BN, int WGM, int WGN, int MODE, int OCC = 2, bool PP = false>
 hipError_t run_tiled(BlockArgs a, hipStream_t stream) {
   a.tiles_n = (a.N + BN - 1) / BN;
   const int64_t cap = MODE == kGateUp ? a.a_rows * a.topk : a.a_rows;
   a.tiles_m = (int)((cap + BM - 1) / BM + (MODE == kDense ? 0 : a.E));  // a group adds at most one partial tile
-  hipLaunchKernelGGL((block_tiled<BM, BN, WGM, WGN, MODE>), dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)),
+  hipLaunchKernelGGL((block_tiled<BM, BN, WGM, WGN, MODE, OCC, PP>), dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)),
                      dim3(64 * WGM * WGN), 0, stream, a);
   return hipGetLastError();
 }
@@ -592,7 +687,7 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
   p.N = (int)N;
   p.K = (int)K;
   const int64_t big = ((M + 255) / 256) * ((N + 255) / 256), mid = ((M + 127) / 128) * ((N + 127) / 128);
-  if (big >= 256) return run_tiled<256, 256, 2, 4, kDense>(p, stream);
+  if (big >= 256) return run_tiled<256, 192, 2, 4, kDense, 2, true>(p, stream);
   if (mid >= 256) return run_tiled<128, 128, 2, 2, kDense>(p, stream);
   return run_tiled<64, 64, 2, 2, kDense>(p, stream);
 }
