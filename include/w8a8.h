@@ -660,8 +660,9 @@ enum { MOE_LOGITS_F32 = 0, MOE_LOGITS_BF16 = 1 };
  *   topk_ids     [T, topk] int32
  *   loss         [1] float32, 4-byte aligned     counts [S, E] int32
  *   grad_logits  [T, E] of the logits' type, or NULL: not wanted
- *   workspace    moe_balance_loss_workspace_bytes bytes; calls that may
- *                overlap need one each
+ *   workspace    moe_balance_loss_workspace_bytes bytes (0, and it may be NULL,
+ *                for a single sequence of few tokens); calls that may overlap
+ *                need one each
  *   E <= 1024, topk <= 64, T <= 2^24, 1 <= S <= 2^20 dividing T. T == 0 gives a
  *   loss and counts of zero.
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED (also another type or score),
@@ -767,10 +768,11 @@ int w8a8_block_gemm(const uint8_t* a_q, const float* a_scale, const uint8_t* w_q
 
 /*
  * w8a8_block_linear — the layer on BF16 input: quantize_blocks, then
- * w8a8_block_gemm. Up to 32 rows it is one launch that quantises the input
- * inside the product and needs no workspace; the result is the same bits.
- *   x_bf16 [M, K]; workspace w8a8_block_linear_workspace_bytes(M, K) bytes (0 up
- *   to 32 rows, and for sizes it does not take); other arguments, limits and
+ * w8a8_block_gemm. For few rows (up to 8, up to 16 where K <= 2048) it is one
+ * launch that quantises the input inside the product and needs no workspace;
+ * the result is the same bits.
+ *   x_bf16 [M, K]; workspace w8a8_block_linear_workspace_bytes(M, K) bytes (0 for
+ *   those, and for sizes it does not take); other arguments, limits and
  *   errors as w8a8_block_gemm and quantize_blocks, plus WORKSPACE.
  */
 size_t w8a8_block_linear_workspace_bytes(int64_t M, int64_t K);
@@ -796,7 +798,7 @@ int w8a8_block_linear(const uint16_t* x_bf16, const uint8_t* w_q, const float* w
  *   workspace  moe_w8a8_block_workspace_bytes bytes; calls that may overlap
  *              need one each
  *   Limits as moe_w8a8_grouped (H a multiple of 16, I of 128), and fewer than
- *   2^22 tiles of 64 copies x 128 columns.
+ *   2^21 tiles of 64 copies x 128 columns.
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, WORKSPACE, DEVICE,
  *         LAUNCH.
  */

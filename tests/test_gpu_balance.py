@@ -198,4 +198,4 @@ def test_refusals():
     with pytest.raises(w8.W8A8Error, match="unsupported"):
         w8.moe_balance_loss(torch.zeros((2, 1025), device="cuda"), torch.zeros((2, 1), dtype=torch.int32, device="cuda"))
     with pytest.raises(w8.W8A8Error, match="workspace"):
-        w8.moe_balance_loss(t, d, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        w8.moe_balance_loss(t, d, sequences=2, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))

@@ -1158,8 +1158,8 @@ def w8a8_block_gemm(a_q, a_scale, w_q, w_scale, out=None):
 
 
 def w8a8_block_linear(x, w_q, w_scale, out=None, workspace=None):
-    """The layer on BF16 input: quantize_blocks, then w8a8_block_gemm (up to 32
-    rows in one launch without a workspace; the same bits)."""
+    """The layer on BF16 input: quantize_blocks, then w8a8_block_gemm (few
+    rows in one launch without a workspace)."""
     import torch
 
     M, K = x.shape
@@ -1169,9 +1169,10 @@ def w8a8_block_linear(x, w_q, w_scale, out=None, workspace=None):
     dev = _same_device(x, (x, torch.bfloat16, (M, K), "x"), (w_q, torch.uint8, (N, K), "w_q"),
                        (w_scale, torch.float32, (_blocks(N), _blocks(K)), "w_scale"),
                        (out, torch.bfloat16, (M, N), "out"))
-    if workspace is None and M > 32:
-        workspace = torch.empty(max(int(lib().w8a8_block_linear_workspace_bytes(M, K)), 16), dtype=torch.uint8,
-                                device=x.device)
+    if workspace is None and M > 8:
+        need = lib().w8a8_block_linear_workspace_bytes(M, K)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     _call(dev, "w8a8_block_linear", x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), out.data_ptr(), M, N, K,
           *_workspace_args(workspace, dev))
     return out
@@ -1273,8 +1274,9 @@ def moe_balance_loss(logits, topk_ids, coef=1.0, sequences=1, score="softmax", w
                        (loss, torch.float32, (), "loss"), (counts, torch.int32, (sequences, E), "counts"),
                        *(((grad, logits.dtype, (T, E), "grad"),) if grad is not None else ()))
     if workspace is None:
-        workspace = torch.empty(max(int(lib().moe_balance_loss_workspace_bytes(T, sequences, E)), 16), dtype=torch.uint8,
-                                device=logits.device)
+        need = lib().moe_balance_loss_workspace_bytes(T, sequences, E)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
     _call(dev, "moe_balance_loss", int(logits.dtype is torch.bfloat16), logits.data_ptr(), topk_ids.data_ptr(), T,
           sequences, E, k, _SCORES[score], coef, loss.data_ptr(), counts.data_ptr(),
           grad.data_ptr() if grad is not None else None, *_workspace_args(workspace, dev))

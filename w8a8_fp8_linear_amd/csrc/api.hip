@@ -814,8 +814,8 @@ int check_block_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
   if (c != W8A8_OK) return c;
   if (I % kFusedIMultiple != 0) return W8A8_ERR_UNSUPPORTED;
   if (!mul_ok(T * topk, H) || !mul_ok(T * topk * H, 4)) return W8A8_ERR_BAD_SHAPE;
-  // a grid holds fewer than 2^32 threads: 4 waves for 64 rows and 128 columns
-  if ((T * topk / 64 + E + 1) * (blocks128(H) + blocks128(I)) >= int64_t(1) << 22 || T * blocks128(H) >= int64_t(1) << 27)
+  // a grid holds fewer than 2^32 threads: at most 8 workgroups of 256 for 64 copies and 128 columns
+  if ((T * topk / 64 + E + 1) * (blocks128(H) + blocks128(I)) >= int64_t(1) << 21 || T * blocks128(H) >= int64_t(1) << 27)
     return W8A8_ERR_UNSUPPORTED;
   return W8A8_OK;
 }
@@ -924,11 +924,12 @@ int moe_balance_loss(int logits_dtype, const void* logits, const int32_t* topk_i
                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
   const int c = check_balance(T, S, E, topk, logits_dtype, score);
   if (c != W8A8_OK) return c;
-  if (any_null({loss, counts, workspace}) || (T > 0 && any_null({logits, topk_ids}))) return W8A8_ERR_NULL_ARG;
+  const size_t need = w8a8::balance_workspace_bytes(T, S, E);
+  if (any_null({loss, counts}) || (T > 0 && any_null({logits, topk_ids})) || (need && !workspace)) return W8A8_ERR_NULL_ARG;
   // the loss is one float, often an element of a vector with one per layer
   if (!all_aligned({logits, topk_ids, counts, grad_logits, workspace}) || (reinterpret_cast<uintptr_t>(loss) & 3u))
     return W8A8_ERR_MISALIGNED;
-  if (workspace_bytes < w8a8::balance_workspace_bytes(T, S, E)) return W8A8_ERR_WORKSPACE;
+  if (workspace_bytes < need) return W8A8_ERR_WORKSPACE;
   const int d = check_device();
   if (d != W8A8_OK) return d;
   const w8a8::Balance b{logits, topk_ids, loss, counts, grad_logits, logits_dtype == MOE_LOGITS_BF16,

@@ -22,7 +22,8 @@
 namespace w8a8 {
 namespace {
 
-constexpr int kCountThreads = 1024;
+constexpr int kThreads = 1024;  // of a workgroup
+constexpr int kMainGroups = 256;  // workgroups of the main pass over all sequences
 constexpr int kMaxChunks = 32;  // of a sequence: every workgroup of the main pass adds them up
 
 struct BalanceArgs {
@@ -39,111 +40,247 @@ struct BalanceArgs {
   float coef;
 };
 
-__global__ __launch_bounds__(kCountThreads) void balance_count(const BalanceArgs p) {
-  extern __shared__ int hist[];  // E + 1
-  const int s = blockIdx.x / p.C, c = blockIdx.x % p.C;
-  for (int e = threadIdx.x; e <= p.E; e += kCountThreads) hist[e] = 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0u;
-  __syncthreads();
-  const int64_t hi = min(p.L, (int64_t)(c + 1) * p.chunk);
-  for (int64_t t = (int64_t)c * p.chunk + threadIdx.x; t < hi; t += kCountThreads) {
-    const int32_t* id = p.ids + ((int64_t)s * p.L + t) * p.k;
-    bool any = false;
-    for (int j = 0; j < p.k; ++j) {
-      const int e = id[j];
-      if (e >= 0 && e < p.E) {
-        atomicAdd(&hist[e], 1);
-        any = true;
-      }
-    }
-    if (any) atomicAdd(&hist[p.E], 1);
+// Sum and maximum over groups of 16, 32 or 64 lanes, in every lane, by vector
+// moves alone: swaps inside quads, mirrored halves and rows, then the rows and
+// halves exchanged.
+template <int CTRL>
+__device__ inline float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+template <int LANES, typename F>
+__device__ inline float group_reduce(float v, F f) {
+  v = f(v, dpp<0xB1>(v));
+  v = f(v, dpp<0x4E>(v));
+  v = f(v, dpp<0x141>(v));
+  v = f(v, dpp<0x140>(v));
+  if constexpr (LANES >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
   }
-  __syncthreads();
-  int32_t* out = p.part + (int64_t)blockIdx.x * (p.E + 1);
-  for (int e = threadIdx.x; e <= p.E; e += kCountThreads) out[e] = hist[e];
-}
-
-// Four consecutive values of a row, at whatever alignment the row has.
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint16_t u16x4_any __attribute__((ext_vector_type(4), aligned(2)));
-
-__device__ inline void load4(const float* p, int left, float* v) {
-  if (left >= 4) {
-    const f32x4_any x = *reinterpret_cast<const f32x4_any*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = x[i];
-  } else {
-    for (int i = 0; i < 4; ++i) v[i] = i < left ? p[i] : -INFINITY;
+  if constexpr (LANES >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
   }
+  return v;
 }
-__device__ inline void load4(const uint16_t* p, int left, float* v) {
-  if (left >= 4) {
-    const u16x4_any x = *reinterpret_cast<const u16x4_any*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float((uint32_t)x[i] << 16);
-  } else {
-    for (int i = 0; i < 4; ++i) v[i] = i < left ? __uint_as_float((uint32_t)p[i] << 16) : -INFINITY;
-  }
-}
-__device__ inline void store4(float* p, int left, const float* v) {
-  if (left >= 4)
-    *reinterpret_cast<f32x4_any*>(p) = f32x4_any{v[0], v[1], v[2], v[3]};
-  else
-    for (int i = 0; i < left; ++i) p[i] = v[i];
-}
-__device__ inline void store4(uint16_t* p, int left, const float* v) {
-  const uint32_t lo = bf16x2_rne(v[0], v[1]), hi = bf16x2_rne(v[2], v[3]);
-  const uint16_t h[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
-  if (left >= 4)
-    *reinterpret_cast<u16x4_any*>(p) = u16x4_any{h[0], h[1], h[2], h[3]};
-  else
-    for (int i = 0; i < left; ++i) p[i] = h[i];
-}
-
 template <int LANES>
 __device__ inline float group_sum(float v) {
-#pragma unroll
-  for (int o = 1; o < LANES; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  return group_reduce<LANES>(v, [](float a, float b) { return a + b; });
 }
 template <int LANES>
 __device__ inline float group_max(float v) {
-#pragma unroll
-  for (int o = 1; o < LANES; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
+  return group_reduce<LANES>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// LANES lanes a token, NC pieces of four values a lane.
-template <typename TL, int LANES, int NC>
-__global__ __launch_bounds__(256) void balance_main(const BalanceArgs p, int sigmoid) {
-  extern __shared__ float up[];  // [E]: (f - 1) * coef / (S n)
-  __shared__ int total;
-  __shared__ double part[4];
+// The tokens that a group of LANES lanes works on together, NC pieces of four
+// values a lane. VEC: E is a multiple of 4, and a piece is one load; otherwise
+// four. Loads have no condition (a lane past the end reads its row's first
+// values): the compiler waits for loads where a branch ends.
+template <typename TL, int LANES, int NC, bool VEC>
+struct Tokens {
+  static constexpr int UT = NC == 1 ? 4 : 1;  // tokens of a group in flight
+  uint32_t raw[UT][NC][4];
+  int id[UT];
+
+  // Token u of the group is t0 + u * step of the sequence whose first row is row0 (L > 0).
+  __device__ inline void load(const BalanceArgs& p, int64_t row0, int64_t t0, int step, int l) {
+    const TL* logits = static_cast<const TL*>(p.logits);
+#pragma unroll
+    for (int u = 0; u < UT; ++u) {
+      const int64_t t = t0 + (int64_t)u * step;
+      const int64_t row = row0 + (t < p.L ? t : 0);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int e = 4 * (l + LANES * i);
+        const TL* src = logits + row * p.E;
+        if constexpr (VEC && sizeof(TL) == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + (e < p.E ? e : 0));
+          raw[u][i][0] = v.x, raw[u][i][1] = v.y, raw[u][i][2] = v.z, raw[u][i][3] = v.w;
+        } else if constexpr (VEC) {
+          const uint2 v = *reinterpret_cast<const uint2*>(src + (e < p.E ? e : 0));
+          raw[u][i][0] = v.x, raw[u][i][1] = v.y;
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const TL v = src[e + r < p.E ? e + r : 0];
+            raw[u][i][r] = sizeof(TL) == 4 ? __builtin_bit_cast(uint32_t, (float)v) : (uint32_t)v;
+          }
+        }
+      }
+      id[u] = p.ids[row * p.k + (l < p.k ? l : 0)];
+    }
+    if (p.k > LANES) {  // more copies than lanes: any valid one will do
+#pragma unroll
+      for (int u = 0; u < UT; ++u) {
+        const int64_t t = t0 + (int64_t)u * step;
+        const int64_t row = row0 + (t < p.L ? t : 0);
+        for (int j = l + LANES; j < p.k; j += LANES) {
+          const int e = p.ids[row * p.k + j];
+          if (e >= 0 && e < p.E) id[u] = e;
+        }
+      }
+    }
+  }
+
+  __device__ inline float value(int u, int i, int r, int e, int E) const {
+    const uint32_t b = sizeof(TL) == 4 ? raw[u][i][r] : !VEC ? raw[u][i][r] << 16
+                       : r & 1 ? raw[u][i][r >> 1] & 0xFFFF0000u : raw[u][i][r >> 1] << 16;
+    return (VEC ? e : e + r) < E ? __uint_as_float(b) : -INFINITY;
+  }
+
+  // Adds the tokens' terms of the loss to sum and writes their gradients. w:
+  // this lane's (f - 1) * base.
+  __device__ inline void work(const BalanceArgs& p, int64_t row0, int64_t t0, int step, int lane, int sigmoid, float base,
+                              const float (&w)[NC][4], double& sum) {
+    TL* grad = static_cast<TL*>(p.grad);
+    const int l = lane % LANES;
+    const uint64_t group = LANES == 64 ? ~0ull : ((1ull << (LANES & 63)) - 1) << (lane - l);
+    float x[UT][NC][4], inv[UT], dot[UT];
+    bool here[UT];
+#pragma unroll
+    for (int u = 0; u < UT; ++u) {
+      here[u] = (__ballot(id[u] >= 0 && id[u] < p.E) & group) != 0 && t0 + (int64_t)u * step < p.L;
+      float m = sigmoid ? 0.f : -INFINITY, z = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          x[u][i][r] = value(u, i, r, 4 * (l + LANES * i), p.E);
+          if (!sigmoid) m = fmaxf(m, x[u][i][r]);
+        }
+      if (!sigmoid) {
+        m = group_max<LANES>(m);
+        m = m == -INFINITY ? 0.f : m;
+      }
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float v = x[u][i][r];
+          x[u][i][r] = sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : __expf(v - m);
+          z += x[u][i][r];
+        }
+      z = group_sum<LANES>(z);
+      inv[u] = z > 0.f ? 1.0f / z : 0.f;
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d = __builtin_fmaf(w[i][r], x[u][i][r], d);
+      dot[u] = group_sum<LANES>(d) * inv[u];
+      if (here[u]) sum += (double)dot[u] + (z > 0.f ? (double)base : 0.0);
+    }
+    if (!grad) return;
+#pragma unroll
+    for (int u = 0; u < UT; ++u) {
+      const int64_t t = t0 + (int64_t)u * step;
+      if (t >= p.L) continue;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int e = 4 * (l + LANES * i);
+        float d[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          // d p_j / d l_j = p_j (1 - sigmoid(l_j)) for sigmoids divided by their sum
+          const float v = x[u][i][r], slope = sigmoid ? 1.0f - v : 1.0f;
+          d[r] = here[u] ? v * inv[u] * slope * (w[i][r] - dot[u]) : 0.f;
+        }
+        TL* dst = grad + (row0 + t) * p.E + e;
+        if constexpr (VEC && sizeof(TL) == 4) {
+          if (e < p.E) *reinterpret_cast<float4*>(dst) = make_float4(d[0], d[1], d[2], d[3]);
+        } else if constexpr (VEC) {
+          if (e < p.E) *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_rne(d[0], d[1]), bf16x2_rne(d[2], d[3]));
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (e + r < p.E) {
+              if constexpr (sizeof(TL) == 4) dst[r] = d[r];
+              else dst[r] = (TL)bf16x2_rne(d[r], 0.f);
+            }
+        }
+      }
+    }
+  }
+};
+
+// The counts of a piece of a sequence's tokens into LDS (cleared here); h[E]:
+// the tokens that count. A wave takes whole tokens, a lane a copy, and the first
+// valid copy of a token counts it. Ends with a barrier.
+__device__ inline void count_tokens(const BalanceArgs& p, int64_t row0, int64_t lo, int64_t hi, int* h) {
+  for (int e = threadIdx.x; e <= p.E; e += kThreads) h[e] = 0;
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per = 64 / p.k, t = lane / p.k, j = lane - t * p.k;  // tokens a wave, this lane's token and copy
+  const uint64_t before = ((1ull << lane) - 1) & ~((1ull << (lane - j)) - 1);  // the token's earlier copies
+  int here = 0;
+  constexpr int U = 4;
+  for (int64_t t0 = lo + (int64_t)wave * per; t0 < hi; t0 += (int64_t)U * (kThreads / 64) * per) {
+    int id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t tok = t0 + (int64_t)u * (kThreads / 64) * per + t;
+      const bool in = t < per && tok < hi;
+      const int v = p.ids[(row0 + (in ? tok : lo)) * p.k + (in ? j : 0)];
+      id[u] = in ? v : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool valid = id[u] >= 0 && id[u] < p.E;
+      const uint64_t m = __ballot(valid);
+      if (valid) atomicAdd(&h[id[u]], 1);
+      here += __builtin_popcountll(__ballot(valid && (m & before) == 0));
+    }
+  }
+  if (lane == 0 && here) atomicAdd(&h[p.E], here);
+  __syncthreads();
+}
+
+__global__ __launch_bounds__(kThreads) void balance_count(const BalanceArgs p) {
+  extern __shared__ int hist[];  // E + 1
+  const int s = blockIdx.x / p.C, c = blockIdx.x % p.C;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0u;
+  count_tokens(p, (int64_t)s * p.L, (int64_t)c * p.chunk, min(p.L, (int64_t)(c + 1) * p.chunk), hist);
+  int32_t* out = p.part + (int64_t)blockIdx.x * (p.E + 1);
+  for (int e = threadIdx.x; e <= p.E; e += kThreads) out[e] = hist[e];
+}
+
+// A sequence is split over G workgroups; each adds up the counts of its chunks
+// first, with the logits of its first tokens on their way. ONE: one workgroup
+// has it all, counts included, and is the only launch.
+template <typename TL, int LANES, int NC, bool VEC, bool ONE>
+__global__ __launch_bounds__(kThreads) void balance_main(const BalanceArgs p, int sigmoid) {
+  constexpr int kWaves = kThreads / 64;
+  extern __shared__ float up[];  // [E]: (f - 1) * coef / (S n), then the counts [E + 1]
+  __shared__ double part[kWaves];
   __shared__ bool last;
-  const int s = blockIdx.x / p.G, gi = blockIdx.x % p.G;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int32_t* cnt = p.part + (int64_t)s * p.C * (p.E + 1);
-  if (tid < 64) {
-    int n = tid < p.C ? cnt[(int64_t)tid * (p.E + 1) + p.E] : 0;
-    for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o, 64);
-    if (tid == 0) total = n;
+  using TK = Tokens<TL, LANES, NC, VEC>;
+  const int s = ONE ? 0 : blockIdx.x / p.G, gi = ONE ? 0 : blockIdx.x % p.G;
+  const int tid = threadIdx.x, lane = tid & 63, l = lane % LANES;
+  constexpr int kGroups = kThreads / LANES, kTokens = kGroups * TK::UT;
+  const int64_t row0 = (int64_t)s * p.L;
+  int64_t t0 = (int64_t)gi * kTokens + tid / LANES;  // the group's tokens: t0, t0 + kGroups, ..
+  TK now;
+  if (p.L > 0) now.load(p, row0, t0, kGroups, l);
+  int* const hist = reinterpret_cast<int*>(up + p.E);
+  if constexpr (ONE) {
+    count_tokens(p, row0, 0, p.L, hist);
+  } else {
+    for (int e = tid; e <= p.E; e += kThreads) hist[e] = 0;
+    __syncthreads();
+    const int all = p.C * (p.E + 1);
+    const int32_t* cnt = p.part + (int64_t)s * all;
+    for (int i = tid; i < all; i += kThreads) atomicAdd(&hist[i % (p.E + 1)], cnt[i]);
+    __syncthreads();
   }
-  __syncthreads();
-  const int n = total;
+  const int n = hist[p.E];
   const float base = n > 0 ? p.coef / ((float)p.S * (float)n) : 0.f;
-  for (int e = tid; e < p.E; e += 256) {
-    int c = 0;
-    for (int i = 0; i < p.C; ++i) c += cnt[(int64_t)i * (p.E + 1) + e];
+  for (int e = tid; e < p.E; e += kThreads) {
+    // (f - 1) * base, f - 1 = (c E - k n) / (k n) from whole numbers
     const double kn = (double)p.k * (double)n;
-    up[e] = n > 0 ? base * (float)(((double)c * (double)p.E - kn) / kn) : 0.f;
-    if (gi == 0) p.counts[(int64_t)s * p.E + e] = c;
+    up[e] = n > 0 ? base * (float)(((double)hist[e] * (double)p.E - kn) / kn) : 0.f;
+    if (gi == 0) p.counts[(int64_t)s * p.E + e] = hist[e];
   }
   __syncthreads();
-  constexpr int kTokens = 256 / LANES;
-  const int l = lane % LANES;
-  const uint64_t group = LANES == 64 ? ~0ull : ((1ull << (LANES & 63)) - 1) << (lane - l);
-  const TL* logits = static_cast<const TL*>(p.logits);
-  TL* grad = static_cast<TL*>(p.grad);
   float w[NC][4];
 #pragma unroll
   for (int i = 0; i < NC; ++i)
@@ -153,98 +290,79 @@ __global__ __launch_bounds__(256) void balance_main(const BalanceArgs p, int sig
       w[i][r] = e < p.E ? up[e] : 0.f;
     }
   double sum = 0.0;
-  for (int64_t t0 = (int64_t)gi * kTokens; t0 < p.L; t0 += (int64_t)p.G * kTokens) {
-    const int64_t t = t0 + tid / LANES;
-    const bool in = t < p.L;
-    const int64_t row = (int64_t)s * p.L + (in ? t : 0);
-    float x[NC][4];
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int e = 4 * (l + LANES * i);
-      load4(logits + row * p.E + e, p.E - e, x[i]);
-    }
-    bool any = false;
-    for (int j = l; j < p.k; j += LANES) {
-      const int e = p.ids[row * p.k + j];
-      any |= e >= 0 && e < p.E;
-    }
-    const bool here = in && (__ballot(any) & group) != 0;
-    float m = -INFINITY;
-    if (!sigmoid) {
-#pragma unroll
-      for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m = fmaxf(m, x[i][r]);
-      m = group_max<LANES>(m);
-      m = m == -INFINITY ? 0.f : m;
-    }
-    float slope[NC][4], z = 0.f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float v = sigmoid ? 1.0f / (1.0f + __expf(-x[i][r])) : __expf(x[i][r] - m);
-        slope[i][r] = sigmoid ? 1.0f - v : 1.0f;
-        x[i][r] = v;
-        z += v;
-      }
-    z = group_sum<LANES>(z);
-    const float inv = z > 0.f ? 1.0f / z : 0.f;
-    float dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[i][r] *= inv;
-        dot = __builtin_fmaf(w[i][r], x[i][r], dot);
-      }
-    dot = group_sum<LANES>(dot);
-    if (here) sum += (double)dot + (z > 0.f ? (double)base : 0.0);
-    if (grad && in) {
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int e = 4 * (l + LANES * i);
-        float d[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) d[r] = here ? x[i][r] * slope[i][r] * (w[i][r] - dot) : 0.f;
-        store4(grad + row * p.E + e, p.E - e, d);
-      }
-    }
+  while (t0 - tid / LANES < p.L) {
+    TK next;
+    const int64_t t1 = t0 + (int64_t)(ONE ? 1 : p.G) * kTokens;
+    next.load(p, row0, t1, kGroups, l);
+    now.work(p, row0, t0, kGroups, lane, sigmoid, base, w, sum);
+    now = next;
+    t0 = t1;
   }
   // the groups of a wave, its waves, then (the last workgroup) all of them, in a fixed order
   double v = l == 0 ? sum : 0.0;
   for (int o = LANES; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
   if (lane == 0) part[tid >> 6] = v;
   __syncthreads();
-  if (tid == 0) {
-    __hip_atomic_store(p.sums + blockIdx.x, (part[0] + part[1]) + (part[2] + part[3]), __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-    last = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  if (tid < 64) {
+    v = lane < kWaves ? part[lane] : 0.0;
+    for (int o = 1; o < kWaves; o <<= 1) v += __shfl_xor(v, o, 64);
   }
-  __syncthreads();
-  if (!last) return;
-  v = 0.0;
-  for (int64_t i = tid; i < (int64_t)gridDim.x; i += 256)
-    v += __hip_atomic_load(p.sums + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  if (lane == 0) part[tid >> 6] = v;
-  __syncthreads();
-  if (tid == 0) *p.loss = (float)((part[0] + part[1]) + (part[2] + part[3]));
+  if (tid == 0) {
+    if constexpr (ONE) {
+      *p.loss = (float)v;
+    } else {
+      // The sum is written through to memory and waited for, then the ticket is
+      // taken; the last workgroup reads past its caches. (A release would write
+      // back the whole L2, the gradient in it: 47 us for 65536 x 128.)
+      __hip_atomic_store(p.sums + blockIdx.x, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      last = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    }
+  }
+  if constexpr (!ONE) {
+    __syncthreads();
+    if (!last) return;
+    v = 0.0;
+    for (int64_t i = tid; i < (int64_t)gridDim.x; i += kThreads)
+      v += __hip_atomic_load(p.sums + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+    if (lane == 0) part[tid >> 6] = v;
+    __syncthreads();
+    if (tid < 64) {
+      v = lane < kWaves ? part[lane] : 0.0;
+      for (int o = 1; o < kWaves; o <<= 1) v += __shfl_xor(v, o, 64);
+      if (tid == 0) *p.loss = (float)v;
+    }
+  }
 }
 
-template <typename TL>
+// Tokens that a workgroup has in flight: lanes a token and tokens a group of
+// lanes as launch_main chooses them.
+int tokens_at_once(int64_t E) {
+  const int lanes = E <= 64 ? 16 : E <= 128 ? 32 : 64;
+  return kThreads / lanes * (E <= 256 ? 4 : 1);
+}
+
+// One workgroup for a single sequence of at most two rounds of its tokens.
+bool balance_one(int64_t L, int64_t S, int64_t E) { return S == 1 && L <= 2 * tokens_at_once(E); }
+
+template <typename TL, int LANES, int NC, bool VEC>
 hipError_t run_main(const BalanceArgs& a, int sigmoid, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.S * a.G));
-  const size_t lds = (size_t)a.E * 4;
-  if (a.E <= 64)
-    hipLaunchKernelGGL((balance_main<TL, 16, 1>), grid, dim3(256), lds, stream, a, sigmoid);
-  else if (a.E <= 128)
-    hipLaunchKernelGGL((balance_main<TL, 32, 1>), grid, dim3(256), lds, stream, a, sigmoid);
-  else if (a.E <= 256)
-    hipLaunchKernelGGL((balance_main<TL, 64, 1>), grid, dim3(256), lds, stream, a, sigmoid);
+  const size_t lds = (size_t)(2 * a.E + 1) * 4;
+  if (balance_one(a.L, a.S, a.E))
+    hipLaunchKernelGGL((balance_main<TL, LANES, NC, VEC, true>), dim3(1), dim3(kThreads), lds, stream, a, sigmoid);
   else
-    hipLaunchKernelGGL((balance_main<TL, 64, 4>), grid, dim3(256), lds, stream, a, sigmoid);
+    hipLaunchKernelGGL((balance_main<TL, LANES, NC, VEC, false>), dim3((unsigned)(a.S * a.G)), dim3(kThreads), lds, stream, a,
+                       sigmoid);
   return hipGetLastError();
+}
+
+template <typename TL, bool VEC>
+hipError_t launch_main(const BalanceArgs& a, int sigmoid, hipStream_t stream) {
+  if (a.E <= 64) return run_main<TL, 16, 1, VEC>(a, sigmoid, stream);
+  if (a.E <= 128) return run_main<TL, 32, 1, VEC>(a, sigmoid, stream);
+  if (a.E <= 256) return run_main<TL, 64, 1, VEC>(a, sigmoid, stream);
+  return run_main<TL, 64, 4, VEC>(a, sigmoid, stream);
 }
 
 int64_t align256(int64_t b) { return (b + 255) & ~int64_t(255); }
@@ -252,14 +370,15 @@ int64_t align256(int64_t b) { return (b + 255) & ~int64_t(255); }
 // chunks of a sequence in the count, workgroups of a sequence in the main pass
 int count_chunks(int64_t L) { return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxChunks, (L + 255) / 256)); }
 int main_groups(int64_t L, int64_t S, int64_t E) {
-  const int tokens = E <= 64 ? 16 : E <= 128 ? 8 : 4;
-  return (int)std::max<int64_t>(1, std::min<int64_t>((L + tokens - 1) / tokens, std::max<int64_t>(1, 1024 / S)));
+  const int tokens = tokens_at_once(E);
+  return (int)std::max<int64_t>(1, std::min<int64_t>((L + tokens - 1) / tokens, std::max<int64_t>(1, kMainGroups / S)));
 }
 
 }  // namespace
 
 size_t balance_workspace_bytes(int64_t T, int64_t S, int64_t E) {
   const int64_t L = T / S;
+  if (balance_one(L, S, E)) return 0;
   return (size_t)(256 + align256(S * main_groups(L, S, E) * 8) + align256(S * count_chunks(L) * (E + 1) * 4));
 }
 
@@ -283,10 +402,13 @@ hipError_t launch_balance(const Balance& b, int64_t T, int64_t S, int64_t E, int
   a.ticket = reinterpret_cast<uint32_t*>(w);
   a.sums = reinterpret_cast<double*>(w + 256);
   a.part = reinterpret_cast<int32_t*>(w + 256 + align256(S * a.G * 8));
-  hipLaunchKernelGGL(balance_count, dim3((unsigned)(S * a.C)), dim3(kCountThreads), (size_t)(E + 1) * 4, stream, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return b.bf16 ? run_main<uint16_t>(a, b.sigmoid, stream) : run_main<float>(a, b.sigmoid, stream);
+  if (!balance_one(a.L, S, E)) {
+    hipLaunchKernelGGL(balance_count, dim3((unsigned)(S * a.C)), dim3(kThreads), (size_t)(E + 1) * 4, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (E % 4 == 0) return b.bf16 ? launch_main<uint16_t, true>(a, b.sigmoid, stream) : launch_main<float, true>(a, b.sigmoid, stream);
+  return b.bf16 ? launch_main<uint16_t, false>(a, b.sigmoid, stream) : launch_main<float, false>(a, b.sigmoid, stream);
 }
 
 }  // namespace w8a8

@@ -187,9 +187,8 @@ hipError_t launch_quantize_weight_blocks(const uint16_t* w, int64_t E, int64_t N
                                          hipStream_t stream);
 hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, uint16_t* y,
                              int64_t M, int64_t N, int64_t K, hipStream_t stream);
-// The layer on BF16 input. ws: block_linear_workspace_bytes bytes (0 up to
-// kBlockSkinnyM rows, which are quantised inside the product).
-constexpr int64_t kBlockSkinnyM = 32;
+// The layer on BF16 input. ws: block_linear_workspace_bytes bytes (0 where the
+// input is quantised inside the product).
 size_t block_linear_workspace_bytes(int64_t M, int64_t K);
 hipError_t launch_block_linear(const uint16_t* x, const uint8_t* w, const float* sw, uint16_t* y, int64_t M, int64_t N,
                                int64_t K, void* ws, hipStream_t stream);
