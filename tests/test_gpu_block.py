@@ -73,7 +73,7 @@ def test_quantize_weights_bit_exact(E, N, K):
 
 SHAPES = [(1, 16, 16), (1, 8192, 256), (2, 48, 144), (5, 144, 1040), (8, 528, 2064), (16, 208, 528), (17, 1040, 2080), (31, 96, 4112),
           (8, 64, 4112), (9, 48, 2064), (12, 96, 4112), (32, 64, 128), (33, 16, 32), (64, 208, 96), (65, 192, 160), (257, 400, 1056), (301, 1040, 1056),
-          (513, 272, 528), (1024, 2064, 400), (700, 6160, 272), (2049, 2320, 272), (4100, 4112, 144)]
+          (513, 272, 528), (600, 1040, 528), (1024, 2064, 400), (700, 6160, 272), (2049, 2320, 272), (3000, 5008, 272), (4100, 4112, 144)]
 
 
 def _operands(M, N, K, seed):

@@ -17,6 +17,7 @@
 #include "device.h"
 #include "grouped.h"
 #include "launch.h"
+#include "widen.h"
 
 namespace w8a8 {
 namespace {
@@ -251,6 +252,75 @@ __global__ __launch_bounds__(256) void block_skinny(const uint8_t* __restrict__ 
   skinny_store<NT, MT>(acc, reinterpret_cast<v4f*>(smem), wave, lane, n0, Y, M, N);
 }
 
+// Some more rows: 16 SM x 16 SN outputs a workgroup, its 4 waves split K, U steps
+// a wave in flight, fragments straight from memory (L2). No barrier until the
+// sums meet: a few hundred rows have too few tiles to fill the GPU, and their time
+// is the chain of loads, which a tile whose waves share K steps walks four times
+// as often.
+template <int SM, int SN, int U>
+__global__ __launch_bounds__(256) void block_ksplit(const uint8_t* __restrict__ X, const float* __restrict__ sA,
+                                                    const uint8_t* __restrict__ W, const float* __restrict__ sW,
+                                                    uint16_t* __restrict__ Y, int M, int N, int K, int tiles_m,
+                                                    int tiles_n) {
+  constexpr int kTiles = SM * SN;
+  static_assert(kTiles % 4 == 0 && 128 % (16 * SN) == 0, "tiles go round the waves; one block of weight rows");
+  __shared__ v4f red[4 * kTiles * 64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tm, tn;
+  map_tile<4>(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int m0 = tm * 16 * SM, n0 = tn * 16 * SN;
+  const auto rW = make_rsrc(W + (int64_t)n0 * K, (int64_t)(N - n0) * K);
+  const auto rX = make_rsrc(X + (int64_t)m0 * K, (int64_t)(M - m0) * K);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int nk = (K + 127) >> 7;
+  const ScalarPtr sWrow[1] = {(ScalarPtr)(sW + (int64_t)(n0 >> 7) * nk)};
+  v4f acc[SN][SM];
+#pragma unroll
+  for (int i = 0; i < SN; ++i)
+#pragma unroll
+    for (int j = 0; j < SM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int kb0 = 0; kb0 < nk; kb0 += 4 * U) {
+    v8i wf[U][SN], xf[U][SM];
+    float sx[U][SM], sw[U][1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = kb0 + wave + 4 * u;
+      const bool live = kb < nk;
+      const int c0 = (kb << 7) + 16 * g, c1 = c0 + 64;
+      const auto rS = make_rsrc(sA + (int64_t)(live ? kb : 0) * M + m0, (int64_t)(M - m0) * 4);
+#pragma unroll
+      for (int j = 0; j < SM; ++j) {
+        const uint32_t row = (uint32_t)(j * 16 + r16);
+        sx[u][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rS, live ? row * 4u : kOutOfRange, 0, 0));
+        const v4i lo = buffer_load16(rX, live && c0 < K ? row * (uint32_t)K + (uint32_t)c0 : kOutOfRange);
+        const v4i hi = buffer_load16(rX, live && c1 < K ? row * (uint32_t)K + (uint32_t)c1 : kOutOfRange);
+        xf[u][j] = v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      }
+    }
+    skinny_weights(rW, 16, sWrow, kb0, nk, K, wave, r16, g, wf, sw);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < SN; ++i)
+#pragma unroll
+        for (int j = 0; j < SM; ++j) scaled_mfma(acc[i][j], wf[u][i], xf[u][j], sx[u][j] * sw[u][0]);
+  }
+#pragma unroll
+  for (int i = 0; i < SN; ++i)
+#pragma unroll
+    for (int j = 0; j < SM; ++j) red[((wave * SN + i) * SM + j) * 64 + lane] = acc[i][j];
+  lds_barrier();
+#pragma unroll
+  for (int o = 0; o < kTiles / 4; ++o) {
+    const int it = wave + 4 * o, n = n0 + it / SM * 16 + 4 * g, m = m0 + it % SM * 16 + r16;
+    const v4f a = add_waves<kTiles>(red, it, lane);
+    if (n < N && m < M)
+      *reinterpret_cast<uint2*>(Y + (int64_t)m * N + n) = make_uint2(bf16x2_rne(a[0], a[1]), bf16x2_rne(a[2], a[3]));
+  }
+}
+
 // On BF16 input of at most 16 rows: the workgroup quantises it into LDS, 8
 // values of a row a thread and 16 lanes a block, every value once a workgroup
 // (in the MFMA's own layout, with its 16 columns for a single row, this took
@@ -380,7 +450,25 @@ __device__ inline int few_group(const BlockFewArgs& p, int grp, int lane, int* l
   return n;
 }
 
-// h of 16 columns: 16 gate and 16 up rows of W13, K split over the waves.
+// 32 E4M3 codes of a lane (an FP8 fragment) -> four BF16 fragments of 8 values,
+// two values an instruction, exactly.
+__device__ inline void widen32(v8i q, v4i (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t c = (uint32_t)q[2 * i + j];
+      w[i][2 * j] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
+      w[i][2 * j + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
+    }
+}
+
+// h of 16 columns: 16 gate and 16 up rows of W13, K split over the waves. The
+// codes of both operands are widened to BF16, whose matrix unit sums near
+// float32 (2^-21.7 of the terms against the FP8 unit's 2^-11.6): h is quantised
+// next, and each of its values that the FP8 unit's sum puts on the other side of
+// an E4M3 border moves every output of the token. With the weight stream as the
+// bound the conversions (48 a step) cost little.
 template <int U>
 __global__ __launch_bounds__(256) void block_few_gate_up(const BlockFewArgs p) {
   __shared__ int list[kFewSlots];
@@ -420,9 +508,21 @@ __global__ __launch_bounds__(256) void block_few_gate_up(const BlockFewArgs p) {
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) {
+        v4i x[4];
+        widen32(xf[u], x);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) scaled_mfma(acc[i], wf[u][i], xf[u], sx[u] * sw[u][i]);
+        for (int i = 0; i < 2; ++i) {
+          v4i w[4];
+          widen32(wf[u][i], w);
+          v4f d = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) d = mfma_16x16x32_bf16(w[c], x[c], d);
+          const float s = sx[u] * sw[u][i];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(d[r], s, acc[i][r]);
+        }
+      }
     }
     if (r0) lds_barrier();  // the tile before has been added
 #pragma unroll
@@ -525,25 +625,23 @@ struct BlockArgs {
   int E, topk, N, K, tiles_m, tiles_n;
 };
 
-template <int BM, int BN, int WGM, int WGN, int MODE, bool PP>
+template <int BM, int BN, int WGM, int WGN, int MODE, int NS>
 struct BlockTile {
   static constexpr int kThreads = 64 * WGM * WGN;
-  static constexpr int kLoaders = PP ? kThreads / 2 : kThreads;  // threads that issue the loads
   static constexpr int WM = BM / WGM, WN = BN / WGN;  // a wave's part
   static constexpr int SM = WM / 16, SN = WN / 16;
   static constexpr int kRows = BM + BN;
   static constexpr int kCodes = kRows * 128;                              // bytes of a stage's codes
   static constexpr int kStage = kCodes + (BM * 4 + 1023) / 1024 * 1024;   // and its row scales
-  static constexpr int kRowsPerPass = kLoaders / 8;
+  static constexpr int kRowsPerPass = kThreads / 8;
   static constexpr int kLoadsB = BN / kRowsPerPass, kLoadsA = BM / kRowsPerPass;
   static constexpr int kEpiStride = BN * 2 + 16;  // dense: staged BF16 row
   static constexpr int kHStride = 128 + 16;       // gate/up: staged row of h codes
   static constexpr int kEpi = MODE == kDense ? BM * kEpiStride
                               : MODE == kGateUp ? BM * kHStride + WGN * BM * 4 : WM * BN * 4;
-  static constexpr int kLds = 2 * kStage > kEpi ? 2 * kStage : kEpi;
+  static constexpr int kLds = NS * kStage > kEpi ? NS * kStage : kEpi;
   static_assert(BN % kRowsPerPass == 0 && BM % kRowsPerPass == 0 && kRowsPerPass % 8 == 0, "stages split evenly");
-  static_assert(WM % 16 == 0 && WN % 16 == 0 && BM % 64 == 0 && BM / 64 <= kLoaders / 64, "wave tiles");
-  static_assert(!PP || (WGM == 2 && BM / 64 == kLoaders / 64), "ping-pong: two groups, a scale load for each loading wave");
+  static_assert(WM % 16 == 0 && WN % 16 == 0 && BM % 64 == 0 && BM <= kThreads, "wave tiles");
   static_assert(MODE != kGateUp || (BN == 256 && SN % 2 == 0), "a gate/up tile is one block of 128 h columns");
 };
 
@@ -599,13 +697,12 @@ __device__ inline v8i frag_at(const uint8_t* st, int lane_off, int row0) {
 //           in one lane. A tile's 128 columns of h are one block: its row maxima
 //           meet in LDS, and h leaves as codes and scales.
 //  kDown    y32 = router weight * (h . w2^T), a float32 row per sorted row.
-// PP: two groups of waves take turns: one reads its fragments of a step from
-// LDS while the other issues the MFMAs of the step that it read before; group
-// 0 issues all loads, a step ahead.
-template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, bool PP>
-__global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(1, OCC)))
+// NS: stages. With one, half the LDS lets more workgroups run on a CU, and they
+// fill each other's waits: every tile of the larger sizes has one.
+template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, int NS>
+__global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 void block_tiled(const BlockArgs p) {
-  using C = BlockTile<BM, BN, WGM, WGN, MODE, PP>;
+  using C = BlockTile<BM, BN, WGM, WGN, MODE, NS>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds + (MODE == kDense ? 0 : BM * 8)];
   int* const row_slot = reinterpret_cast<int*>(smem + C::kLds);                // slot of a tile row, -1: none
   float* const row_w = reinterpret_cast<float*>(smem + C::kLds + BM * 4);      // its router weight
@@ -690,7 +787,7 @@ void block_tiled(const BlockArgs p) {
     const bool kin = k0 + lchunk < K;
 #pragma unroll
     for (int i = 0; i < C::kLoadsB + C::kLoadsA; ++i) {
-      const int s0 = wave * 64 + C::kLoaders * i;
+      const int s0 = wave * 64 + C::kThreads * i;
       if (i < C::kLoadsB) {
         buffer_load16_lds(rB, base + s0 * 16, kin ? boff(i) + (uint32_t)k0 : kOutOfRange);
       } else {
@@ -705,7 +802,7 @@ void block_tiled(const BlockArgs p) {
     }
   };
 
-  const int wm = PP ? wave / WGN : wave % WGM, wn = PP ? wave % WGN : wave / WGM;
+  const int wm = wave % WGM, wn = wave / WGM;
   const int r16 = lane & 15, g = lane >> 4;
   const int lane_off = frag_lane_off(r16, g);
   const int a_base = (BN + wm * C::WM) * 128, b_base = wn * C::WN * 128, s_base = C::kCodes + (wm * C::WM + r16) * 4;
@@ -724,70 +821,32 @@ void block_tiled(const BlockArgs p) {
 #pragma unroll
     for (int j = 0; j < C::SM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  if constexpr (PP) {
-    const bool loader = wm == 0;
-    if (loader) {
-      issue(0, 0);
-      if (nk > 1) {
-        issue(1, 1);
-        wait_vmcnt<C::kLoadsB + C::kLoadsA + 1>();
-      } else {
-        wait_vmem_all();
-      }
-    }
+  issue(0, 0);
+  for (int kt = 0; kt < nk; ++kt) {
+    float sw[kBlocks];
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) sw[i] = sBp[i][kt];
+    wait_vmem_all();
     lds_barrier();
-    if (!loader) lds_barrier();
-    for (int kt = 0; kt < nk; ++kt) {
-      if (loader && kt >= 1 && kt + 1 < nk) issue((kt + 1) & 1, kt + 1);
-      const uint8_t* st = smem + (kt & 1) * C::kStage;
-      v8i xf[C::SM], wf[C::SN];
-      float sx[C::SM], sw[kBlocks];
+    if (NS == 2 && kt + 1 < nk) issue((kt + 1) & 1, kt + 1);
+    const uint8_t* st = smem + (NS == 2 ? (kt & 1) * C::kStage : 0);
+    v8i xf[C::SM], wf[C::SN];
+    float sx[C::SM];
 #pragma unroll
-      for (int i = 0; i < kBlocks; ++i) sw[i] = sBp[i][kt];
+    for (int j = 0; j < C::SM; ++j) {
+      xf[j] = frag_at(st + a_base, lane_off, j * 16);
+      sx[j] = *reinterpret_cast<const float*>(st + s_base + j * 64);
+    }
 #pragma unroll
-      for (int j = 0; j < C::SM; ++j) {
-        xf[j] = frag_at(st + a_base, lane_off, j * 16);
-        sx[j] = *reinterpret_cast<const float*>(st + s_base + j * 64);
-      }
-#pragma unroll
-      for (int i = 0; i < C::SN; ++i) wf[i] = frag_at(st + b_base, lane_off, i * 16);
+    for (int i = 0; i < C::SN; ++i) wf[i] = frag_at(st + b_base, lane_off, i * 16);
+    if (NS == 1) {
+      // one stage: once every wave has its fragments the next step's loads go out, and overlap the MFMAs
       lds_barrier();
-      scaled_mfmas<C::SN, C::SM, kBlocks>(acc, wf, xf, sx, sw);
-      // the wait stays behind the MFMAs (an s_waitcnt is no scheduling barrier)
+      if (kt + 1 < nk) issue(0, kt + 1);
       __builtin_amdgcn_sched_barrier(0);
-      if (loader) wait_vmem_all();
-      lds_barrier();
     }
-    if (loader) lds_barrier();
-  } else {
-    issue(0, 0);
-    for (int kt = 0; kt < nk; ++kt) {
-      float sw[kBlocks];
-#pragma unroll
-      for (int i = 0; i < kBlocks; ++i) sw[i] = sBp[i][kt];
-      wait_vmem_all();
-      __syncthreads();
-      if (kt + 1 < nk) issue((kt + 1) & 1, kt + 1);
-      const uint8_t* st = smem + (kt & 1) * C::kStage;
-      v8i xf[C::SM];
-      float sx[C::SM];
-#pragma unroll
-      for (int j = 0; j < C::SM; ++j) {
-        xf[j] = frag_at(st + a_base, lane_off, j * 16);
-        sx[j] = *reinterpret_cast<const float*>(st + s_base + j * 64);
-      }
-#pragma unroll
-      for (int i = 0; i < C::SN; ++i) {
-        const v8i wf = frag_at(st + b_base, lane_off, i * 16);
-#pragma unroll
-        for (int j = 0; j < C::SM; ++j) {
-          const v4f d = mfma_16x16x128_e4m3(wf, xf[j], v4f{0.f, 0.f, 0.f, 0.f});
-          const float s = sx[j] * sw[i % kBlocks];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[r], s, acc[i][j][r]);
-        }
-      }
-    }
+    scaled_mfmas<C::SN, C::SM, kBlocks>(acc, wf, xf, sx, sw);
+    __builtin_amdgcn_sched_barrier(0);
   }
   __syncthreads();
 
@@ -914,12 +973,12 @@ __global__ __launch_bounds__(256) void combine_block_quant(const float* __restri
   if ((threadIdx.x & 15) == 0) scale[(int64_t)blk * T + t] = s;
 }
 
-template <int BM, int BN, int WGM, int WGN, int MODE, int OCC = 2, bool PP = false>
+template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, int NS>
 hipError_t run_tiled(BlockArgs a, hipStream_t stream) {
   a.tiles_n = (a.N + BN - 1) / BN;
   const int64_t cap = MODE == kGateUp ? a.a_rows * a.topk : a.a_rows;
   a.tiles_m = (int)((cap + BM - 1) / BM + (MODE == kDense ? 0 : a.E));  // a group adds at most one partial tile
-  hipLaunchKernelGGL((block_tiled<BM, BN, WGM, WGN, MODE, OCC, PP>), dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)),
+  hipLaunchKernelGGL((block_tiled<BM, BN, WGM, WGN, MODE, OCC, NS>), dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)),
                      dim3(64 * WGM * WGN), 0, stream, a);
   return hipGetLastError();
 }
@@ -929,6 +988,15 @@ hipError_t run_skinny_bf16(const uint16_t* x, const uint8_t* w, const float* sw,
                            int64_t K, hipStream_t stream) {
   hipLaunchKernelGGL((block_skinny_bf16<XR, NT>), dim3((unsigned)((N + 16 * NT - 1) / (16 * NT))), dim3(256), 0, stream, x, w,
                      sw, y, (int)M, (int)N, (int)K);
+  return hipGetLastError();
+}
+
+template <int SM, int SN, int U>
+hipError_t run_ksplit(const uint8_t* x, const float* sa, const uint8_t* w, const float* sw, uint16_t* y, int64_t M,
+                      int64_t N, int64_t K, hipStream_t stream) {
+  const int tiles_m = (int)((M + 16 * SM - 1) / (16 * SM)), tiles_n = (int)((N + 16 * SN - 1) / (16 * SN));
+  hipLaunchKernelGGL((block_ksplit<SM, SN, U>), dim3((unsigned)((int64_t)tiles_m * tiles_n)), dim3(256), 0, stream, x, sa, w,
+                     sw, y, (int)M, (int)N, (int)K, tiles_m, tiles_n);
   return hipGetLastError();
 }
 
@@ -976,10 +1044,25 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
   p.topk = 1;
   p.N = (int)N;
   p.K = (int)K;
-  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256), mid = ((M + 127) / 128) * ((N + 127) / 128);
-  if (big >= 256) return run_tiled<256, 192, 2, 4, kDense, 2, true>(p, stream);
-  if (mid >= 256) return run_tiled<128, 128, 2, 2, kDense>(p, stream);
-  return run_tiled<64, 64, 2, 2, kDense>(p, stream);
+  // By the number of tiles. One workgroup a CU, waves splitting K, while 32 x 32 or
+  // 64 x 32 tiles are no more than the CUs (301 x 1040 x 1056: 5.9 us against 7.1
+  // for 64 x 64 tiles and 10.3 for 128 x 128); 64 x 64 tiles with two stages up to two
+  // a CU (512 x 2048 x 2048: 10.5; K split 14.6; one stage 11.5), with one up to three
+  // (512 x 6144 x 2048: 13.1; two stages 19.0); 64 x 128 up to three (1024 x 6144 x
+  // 2048: 18.9; 64 x 64 24.0; 128 x 128 19.3). Beyond, rounds of the GPU: 768 tiles of
+  // 128 x 128 or 512 of 128 x 256, whose round takes about 1.45 times as long (4096 x
+  // 6144 x 2048, 2 rounds each: 53.2 against 59.2 us; 8192 x 2048 x 6144, 2 against 1:
+  // 104.8 against 93.9 us). Two groups of waves in turns on 256 x 192 tiles, as the
+  // product with row scales has them, took 54.8 us and 129.9 us.
+  const auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  if (tiles(32, 32) <= 256) return run_ksplit<2, 2, 3>(a, sa, w, sw, y, M, N, K, stream);
+  if (tiles(64, 32) <= 256) return run_ksplit<4, 2, 1>(a, sa, w, sw, y, M, N, K, stream);
+  if (tiles(64, 64) <= 512) return run_tiled<64, 64, 2, 2, kDense, 2, 2>(p, stream);
+  if (tiles(64, 64) <= 768) return run_tiled<64, 64, 2, 2, kDense, 4, 1>(p, stream);
+  if (tiles(64, 128) <= 768) return run_tiled<64, 128, 2, 2, kDense, 4, 1>(p, stream);
+  if (3 * ((tiles(128, 256) + 511) / 512) < 2 * ((tiles(128, 128) + 767) / 768))
+    return run_tiled<128, 256, 2, 2, kDense, 2, 1>(p, stream);
+  return run_tiled<128, 128, 2, 2, kDense, 3, 1>(p, stream);
 }
 
 // Rows that are quantised inside the product, by every workgroup for itself:
@@ -1088,11 +1171,11 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
   p.topk = (int)topk;
   p.N = (int)(2 * I);
   p.K = (int)H;
-  const int64_t avg = T * topk / E;
-  if (avg < 64)
-    err = run_tiled<64, 256, 1, 4, kGateUp>(p, stream);
-  else
-    err = run_tiled<128, 256, 2, 4, kGateUp>(p, stream);
+  // 64 x 256 tiles with one stage, three workgroups a CU, for every group size
+  // (whole passes, 4096 tokens, top-8 of 64: 268 us against 288 for 128 x 256 with
+  // two stages, 267 ping-pong; 16384 tokens: 916 against 1015 and 977; 1024: 105
+  // against 116 and 103)
+  err = run_tiled<64, 256, 1, 4, kGateUp, 3, 1>(p, stream);
   if (err != hipSuccess) return err;
   BlockArgs d = p;
   d.A = p.hq;
@@ -1105,10 +1188,10 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
   d.slot_row = slot_row;
   d.N = (int)H;
   d.K = (int)I;
-  if (avg < 64)
-    err = run_tiled<64, 128, 1, 2, kDown>(d, stream);
-  else
-    err = run_tiled<128, 128, 2, 2, kDown>(d, stream);
+  // 64 x 128 tiles, four workgroups a CU, 128 x 256 for large groups (4096 tokens,
+  // top-8 of 64: 250 against 255 us for the pass; 16384 tokens: 878 against 864)
+  err = T * topk / E < 1000 ? run_tiled<64, 128, 2, 2, kDown, 4, 1>(d, stream)
+                            : run_tiled<128, 256, 2, 2, kDown, 2, 1>(d, stream);
   if (err != hipSuccess) return err;
   return combine(y, slot_row);
 }
