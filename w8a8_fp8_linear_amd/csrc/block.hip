@@ -676,6 +676,37 @@ __device__ inline void scaled_mfmas(v4f (&acc)[SN][SM], const v8i (&wf)[SN], con
     for (int j = 0; j < SM; ++j) asm volatile("" : "+v"(acc[i][j]));
 }
 
+// The same on BF16 matrix cores: the codes are widened, the sums near float32.
+template <int SN, int SM, int NB>
+__device__ inline void wide_mfmas(v4f (&acc)[SN][SM], const v8i (&wf)[SN], const v8i (&xf)[SM], const float (&sx)[SM],
+                                  const float (&sw)[NB]) {
+  v4i x[SM][4];
+#pragma unroll
+  for (int j = 0; j < SM; ++j) widen32(xf[j], x[j]);
+#pragma unroll
+  for (int i = 0; i < SN; ++i) {
+    v4i w[4];
+    widen32(wf[i], w);
+    v4f d[SM];
+#pragma unroll
+    for (int j = 0; j < SM; ++j) d[j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < SM; ++j) d[j] = mfma_16x16x32_bf16(w[c], x[j][c], d[j]);
+#pragma unroll
+    for (int j = 0; j < SM; ++j) {
+      const float s = sx[j] * sw[i % NB];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[j][r], s, acc[i][j][r]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < SN; ++i)
+#pragma unroll
+    for (int j = 0; j < SM; ++j) asm volatile("" : "+v"(acc[i][j]));
+}
+
 // Fragment of the 16 staged rows from `row0` on, lds_frag's chunks c and c + 4
 // of this lane's row: lane_off is the lane's own offset (its row lane % 16 and
 // chunk), so that every fragment of a stage is one address and a constant.
@@ -699,7 +730,7 @@ __device__ inline v8i frag_at(const uint8_t* st, int lane_off, int row0) {
 //  kDown    y32 = router weight * (h . w2^T), a float32 row per sorted row.
 // NS: stages. With one, half the LDS lets more workgroups run on a CU, and they
 // fill each other's waits: every tile of the larger sizes has one.
-template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, int NS>
+template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, int NS, bool WIDE>
 __global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 void block_tiled(const BlockArgs p) {
   using C = BlockTile<BM, BN, WGM, WGN, MODE, NS>;
@@ -845,7 +876,10 @@ void block_tiled(const BlockArgs p) {
       if (kt + 1 < nk) issue(0, kt + 1);
       __builtin_amdgcn_sched_barrier(0);
     }
-    scaled_mfmas<C::SN, C::SM, kBlocks>(acc, wf, xf, sx, sw);
+    if constexpr (WIDE)
+      wide_mfmas<C::SN, C::SM, kBlocks>(acc, wf, xf, sx, sw);
+    else
+      scaled_mfmas<C::SN, C::SM, kBlocks>(acc, wf, xf, sx, sw);
     __builtin_amdgcn_sched_barrier(0);
   }
   __syncthreads();
@@ -973,12 +1007,12 @@ __global__ __launch_bounds__(256) void combine_block_quant(const float* __restri
   if ((threadIdx.x & 15) == 0) scale[(int64_t)blk * T + t] = s;
 }
 
-template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, int NS>
+template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, int NS, bool WIDE = false>
 hipError_t run_tiled(BlockArgs a, hipStream_t stream) {
   a.tiles_n = (a.N + BN - 1) / BN;
   const int64_t cap = MODE == kGateUp ? a.a_rows * a.topk : a.a_rows;
   a.tiles_m = (int)((cap + BM - 1) / BM + (MODE == kDense ? 0 : a.E));  // a group adds at most one partial tile
-  hipLaunchKernelGGL((block_tiled<BM, BN, WGM, WGN, MODE, OCC, NS>), dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)),
+  hipLaunchKernelGGL((block_tiled<BM, BN, WGM, WGN, MODE, OCC, NS, WIDE>), dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)),
                      dim3(64 * WGM * WGN), 0, stream, a);
   return hipGetLastError();
 }
@@ -1089,8 +1123,10 @@ size_t block_linear_workspace_bytes(int64_t M, int64_t K) {
   return (size_t)(align256(M * K) + align256((K + 127) / 128 * M * 4));
 }
 
-// Whether the pass takes the kernels for groups of few rows.
-static bool block_few(int64_t T, int64_t E, int64_t topk) { return T * topk <= kFewSlots && T * topk <= 16 * E; }
+// Whether the pass takes the kernels for groups of few rows: up to 8 on average
+// (H 2048, I 512, 64 experts, top-8: 64 tokens 63 us against 74 in tiles, 128
+// tokens 103 against 77; 192 experts, top-4, H 1024: 128 tokens 62 against 85).
+static bool block_few(int64_t T, int64_t E, int64_t topk) { return T * topk <= kFewSlots && T * topk <= 8 * E; }
 
 static hipError_t launch_block_few(const BlockFewArgs& a, hipStream_t stream) {
   const int groups = a.by_slot ? a.n : a.E;
@@ -1171,11 +1207,14 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
   p.topk = (int)topk;
   p.N = (int)(2 * I);
   p.K = (int)H;
-  // 64 x 256 tiles with one stage, three workgroups a CU, for every group size
-  // (whole passes, 4096 tokens, top-8 of 64: 268 us against 288 for 128 x 256 with
-  // two stages, 267 ping-pong; 16384 tokens: 916 against 1015 and 977; 1024: 105
-  // against 116 and 103)
-  err = run_tiled<64, 256, 1, 4, kGateUp, 3, 1>(p, stream);
+  // 64 x 256 tiles with one stage for every group size, on FP8 three workgroups a
+  // CU (whole passes, 4096 tokens, top-8 of 64: 268 us against 288 for 128 x 256
+  // with two stages; 16384 tokens: 916 against 1015; 1024: 105 against 116). Groups of
+  // up to 64 rows on average wait for their weights more than for the matrix unit,
+  // and take the exact sums of the widened codes for 6 to 8% of the pass (512 tokens
+  // 86 against 80 us; at 4096 it would be 310 against 250).
+  err = T * topk <= 64 * E ? run_tiled<64, 256, 1, 4, kGateUp, 2, 1, true>(p, stream)
+                           : run_tiled<64, 256, 1, 4, kGateUp, 3, 1>(p, stream);
   if (err != hipSuccess) return err;
   BlockArgs d = p;
   d.A = p.hq;
