@@ -786,8 +786,9 @@ int w8a8_block_linear(const uint16_t* x_bf16, const uint8_t* w_q, const float* w
  *   g, u   = gate and up halves of W13[e] . x[t]     (float32, as w8a8_block_gemm)
  *   h      = silu(g) * u                             (float32)
  *   h_q    = E4M3 of h with one scale per 128 of its I values (quantize_blocks' rule)
- *   out[t] = bf16( sum over j with a valid id, in order, of topk_w[t,j] * (W2[e] . h) )
- * A token without a valid id gets zeros.
+ *   out[t] = bf16( sum over j with a valid id of topk_w[t,j] * (W2[e] . h) )
+ * The sum is float32, in an order that the ids fix. A token without a valid id
+ * gets zeros.
  *   x_q [T, H]  x_scale [ceil(H/128), T]
  *   w13_q [E, 2I, H] (rows 0..I-1 gate, I..2I-1 up)  w13_scale [E, 2I/128, ceil(H/128)]
  *   w2_q [E, H, I]  w2_scale [E, ceil(H/128), I/128]

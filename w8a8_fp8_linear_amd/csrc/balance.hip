@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kThreads = 1024;  // of a workgroup
 constexpr int kMainGroups = 256;  // workgroups of the main pass over all sequences
+constexpr int kTicketStride = 16;  // words
 constexpr int kMaxChunks = 32;  // of a sequence: every workgroup of the main pass adds them up
 
 struct BalanceArgs {
@@ -31,12 +32,12 @@ struct BalanceArgs {
   const int32_t* ids;   // [S L, k]
   int32_t* part;        // [S, C, E + 1]: copies of a chunk's tokens by expert, its tokens that count
   double* sums;         // [S G]
-  uint32_t* ticket;
+  uint32_t* tickets;    // [1 + ceil(S G / round)] a cache line each
   float* loss;          // [1]
   int32_t* counts;      // [S, E]
   void* grad;           // [S L, E] or NULL
   int64_t L;
-  int S, E, k, C, G, chunk;
+  int S, E, k, C, G, chunk, round;
   float coef;
 };
 
@@ -238,7 +239,8 @@ __device__ inline void count_tokens(const BalanceArgs& p, int64_t row0, int64_t 
 __global__ __launch_bounds__(kThreads) void balance_count(const BalanceArgs p) {
   extern __shared__ int hist[];  // E + 1
   const int s = blockIdx.x / p.C, c = blockIdx.x % p.C;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0u;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= (p.S * p.G - 1) / p.round + 1; i += kThreads) p.tickets[i * kTicketStride] = 0u;
   count_tokens(p, (int64_t)s * p.L, (int64_t)c * p.chunk, min(p.L, (int64_t)(c + 1) * p.chunk), hist);
   int32_t* out = p.part + (int64_t)blockIdx.x * (p.E + 1);
   for (int e = threadIdx.x; e <= p.E; e += kThreads) out[e] = hist[e];
@@ -259,6 +261,13 @@ __global__ __launch_bounds__(kThreads) void balance_main(const BalanceArgs p, in
   constexpr int kGroups = kThreads / LANES, kTokens = kGroups * TK::UT;
   const int64_t row0 = (int64_t)s * p.L;
   int64_t t0 = (int64_t)gi * kTokens + tid / LANES;  // the group's tokens: t0, t0 + kGroups, ..
+  // the counts' loads go out first (loads return in order), then the tokens'
+  constexpr int kAhead = 4;
+  const int all = ONE ? 0 : p.C * (p.E + 1);
+  const int32_t* cnt = p.part + (int64_t)s * all;
+  int c[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) c[i] = tid + i * kThreads < all ? cnt[tid + i * kThreads] : 0;
   TK now;
   if (p.L > 0) now.load(p, row0, t0, kGroups, l);
   int* const hist = reinterpret_cast<int*>(up + p.E);
@@ -267,17 +276,18 @@ __global__ __launch_bounds__(kThreads) void balance_main(const BalanceArgs p, in
   } else {
     for (int e = tid; e <= p.E; e += kThreads) hist[e] = 0;
     __syncthreads();
-    const int all = p.C * (p.E + 1);
-    const int32_t* cnt = p.part + (int64_t)s * all;
-    for (int i = tid; i < all; i += kThreads) atomicAdd(&hist[i % (p.E + 1)], cnt[i]);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (tid + i * kThreads < all) atomicAdd(&hist[(tid + i * kThreads) % (p.E + 1)], c[i]);
+    for (int i = tid + kAhead * kThreads; i < all; i += kThreads) atomicAdd(&hist[i % (p.E + 1)], cnt[i]);
     __syncthreads();
   }
   const int n = hist[p.E];
   const float base = n > 0 ? p.coef / ((float)p.S * (float)n) : 0.f;
   for (int e = tid; e < p.E; e += kThreads) {
-    // (f - 1) * base, f - 1 = (c E - k n) / (k n) from whole numbers
+    // (f - 1) * base, f - 1 = (c E - k n) / (k n), the difference from whole numbers
     const double kn = (double)p.k * (double)n;
-    up[e] = n > 0 ? base * (float)(((double)hist[e] * (double)p.E - kn) / kn) : 0.f;
+    up[e] = n > 0 ? base * ((float)((double)hist[e] * (double)p.E - kn) / (float)kn) : 0.f;
     if (gi == 0) p.counts[(int64_t)s * p.E + e] = hist[e];
   }
   __syncthreads();
@@ -311,12 +321,18 @@ __global__ __launch_bounds__(kThreads) void balance_main(const BalanceArgs p, in
     if constexpr (ONE) {
       *p.loss = (float)v;
     } else {
-      // The sum is written through to memory and waited for, then the ticket is
+      // The sum is written through to memory and waited for, then a ticket is
       // taken; the last workgroup reads past its caches. (A release would write
-      // back the whole L2, the gradient in it: 47 us for 65536 x 128.)
+      // back the whole L2, the gradient in it: 47 us for 65536 x 128.) Tickets of one
+      // word are served one after another, some 11 ns each: every `round` workgroups
+      // have one of their own, and the last of each takes one of all rounds.
+      const uint32_t r = blockIdx.x / p.round, rounds = (gridDim.x - 1) / p.round + 1;
+      const uint32_t mine = min((uint32_t)p.round, gridDim.x - r * p.round);
       __hip_atomic_store(p.sums + blockIdx.x, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      last = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+      last = __hip_atomic_fetch_add(p.tickets + (1 + r) * kTicketStride, 1u, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT) == mine - 1 &&
+             __hip_atomic_fetch_add(p.tickets, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == rounds - 1;
     }
   }
   if constexpr (!ONE) {
@@ -374,12 +390,21 @@ int main_groups(int64_t L, int64_t S, int64_t E) {
   return (int)std::max<int64_t>(1, std::min<int64_t>((L + tokens - 1) / tokens, std::max<int64_t>(1, kMainGroups / S)));
 }
 
+// Workgroups that share a ticket: about as many as there are tickets.
+int ticket_round(int64_t n) {
+  int r = 16;
+  while ((int64_t)r * r < n) r *= 2;
+  return r;
+}
+int64_t tickets_bytes(int64_t n) { return align256((1 + (n - 1) / ticket_round(n) + 1) * kTicketStride * 4); }
+
 }  // namespace
 
 size_t balance_workspace_bytes(int64_t T, int64_t S, int64_t E) {
   const int64_t L = T / S;
   if (balance_one(L, S, E)) return 0;
-  return (size_t)(256 + align256(S * main_groups(L, S, E) * 8) + align256(S * count_chunks(L) * (E + 1) * 4));
+  const int64_t n = S * main_groups(L, S, E);
+  return (size_t)(tickets_bytes(n) + align256(n * 8) + align256(S * count_chunks(L) * (E + 1) * 4));
 }
 
 hipError_t launch_balance(const Balance& b, int64_t T, int64_t S, int64_t E, int64_t topk, void* ws,
@@ -399,9 +424,11 @@ hipError_t launch_balance(const Balance& b, int64_t T, int64_t S, int64_t E, int
   a.counts = b.counts;
   a.grad = b.grad;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  a.ticket = reinterpret_cast<uint32_t*>(w);
-  a.sums = reinterpret_cast<double*>(w + 256);
-  a.part = reinterpret_cast<int32_t*>(w + 256 + align256(S * a.G * 8));
+  const int64_t n = S * a.G;
+  a.round = ticket_round(n);
+  a.tickets = reinterpret_cast<uint32_t*>(w);
+  a.sums = reinterpret_cast<double*>(w + tickets_bytes(n));
+  a.part = reinterpret_cast<int32_t*>(w + tickets_bytes(n) + align256(n * 8));
   if (!balance_one(a.L, S, E)) {
     hipLaunchKernelGGL(balance_count, dim3((unsigned)(S * a.C)), dim3(kThreads), (size_t)(E + 1) * 4, stream, a);
     const hipError_t e = hipGetLastError();

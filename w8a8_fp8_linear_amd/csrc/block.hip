@@ -604,6 +604,109 @@ __global__ __launch_bounds__(256) void block_few_down(const BlockFewArgs p) {
   }
 }
 
+// The smallest steps: the down projection with the sum over a token's copies,
+// one launch instead of two. A workgroup has 16 columns and quantises all
+// slots' h into LDS; its 16 waves take the steps of 128 of the picked experts
+// in turn, the step's columns being the tokens.
+constexpr int kSmallSlots = 16, kSmallCodes = 16384;  // most slots, codes of h
+
+__global__ __launch_bounds__(1024) void block_small_down(const BlockFewArgs p, uint16_t* __restrict__ out) {
+  constexpr int U = 4, kWaves = 16;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // codes [I/128][slots][128]; then the waves' sums
+  __shared__ float hs[kSmallCodes / 128];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int H = p.H, I = p.I, nk = I >> 7, n = p.n, n0 = blockIdx.x * 16;
+  const int r16 = lane & 15, g = lane >> 4;
+  const int nb = (H + 127) >> 7;
+  // h's loads first, then the ids and the first steps' weights
+  const int per = I >> 3, chunks = n * per;  // pieces of 8 values
+  float4 ha, hb;
+  auto load_h = [&](int c) {
+    const float* src = p.h + (int64_t)c * 8;
+    ha = *reinterpret_cast<const float4*>(src);
+    hb = *reinterpret_cast<const float4*>(src + 4);
+  };
+  if (tid < chunks) load_h(tid);
+  int id = -1;
+  float tw = 0.f;
+  if (lane < n) {
+    id = p.ids[lane];
+    tw = p.tw[lane];
+    if (id >= p.E) id = -1;
+  }
+  v8i wf[U];
+  auto load_w = [&](int u0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int unit = u0 + kWaves * u, slot = unit / nk, kb = unit - slot * nk;
+      const int e = slot < n ? __builtin_amdgcn_readlane(id, slot) : -1;
+      // an expert's first slot works for all of its tokens
+      const bool mine = e >= 0 && (__ballot(id == e) & ((1ull << slot) - 1)) == 0;
+      const auto rW = make_rsrc(p.w2 + ((int64_t)(mine ? e : 0) * H + n0) * I, mine ? (int64_t)(H - n0) * I : 0);
+      const uint32_t at = (uint32_t)r16 * (uint32_t)I + (uint32_t)(kb << 7) + 16u * (uint32_t)g;
+      const v4i lo = buffer_load16(rW, at), hi = buffer_load16(rW, at + 64u);
+      wf[u] = v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    }
+  };
+  const int units = n * nk;
+  load_w(wave);
+  __builtin_amdgcn_sched_barrier(0);
+  for (int c = tid; c < chunks; c += 1024) {
+    if (c != tid) load_h(c);
+    const float v[8] = {ha.x, ha.y, ha.z, ha.w, hb.x, hb.y, hb.z, hb.w};
+    uint32_t am = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    const float s = block_scale_f32(row16_max(am)), inv = 1.0f / s;
+    const int slot = c / per, col = c - slot * per, kb = col >> 4, piece = (col & 15) >> 1;
+    *reinterpret_cast<uint2*>(smem + (kb * n + slot) * 128 + ((piece ^ (slot & 7)) << 4) + (col & 1) * 8) =
+        make_uint2(codes4(v, s, inv), codes4(v + 4, s, inv));
+    if ((col & 15) == 0) hs[kb * n + slot] = s;
+  }
+  lds_barrier();
+  v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int u0 = wave; u0 < units; u0 += kWaves * U) {
+    if (u0 != wave) load_w(u0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int unit = u0 + kWaves * u, slot = unit / nk, kb = unit - slot * nk;
+      if (slot >= n) break;
+      const int e = __builtin_amdgcn_readlane(id, slot);
+      const uint64_t all = __ballot(id == e);
+      if (e < 0 || (all & ((1ull << slot) - 1)) != 0) continue;
+      const float sw = ((ScalarPtr)(p.s2 + ((int64_t)e * nb + (n0 >> 7)) * nk))[kb];
+      // this lane's token: its copies for the expert, one row of h, their weights added
+      const uint64_t own = r16 < p.T ? (all >> (r16 * p.topk)) & (~0ull >> (64 - p.topk)) : 0ull;
+      const int row = own ? r16 * p.topk + __builtin_ctzll(own) : 0;
+      float w = 0.f;
+      for (int j = 0; j < p.topk; ++j) {
+        const float x = __uint_as_float(__builtin_amdgcn_ds_bpermute(((r16 * p.topk + j) & 63) << 2, (int)__float_as_uint(tw)));
+        w += (own >> j) & 1 ? x : 0.f;
+      }
+      const uint8_t* at = smem + (kb * n + row) * 128;
+      const v4i lo = *reinterpret_cast<const v4i*>(at + ((g ^ (row & 7)) << 4));
+      const v4i hi = *reinterpret_cast<const v4i*>(at + (((g + 4) ^ (row & 7)) << 4));
+      const v4f d = mfma_16x16x128_e4m3(wf[u], v8i{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}, v4f{0.f, 0.f, 0.f, 0.f});
+      const float s = hs[kb * n + row] * sw * w;
+      // a token without this expert keeps its sum, whatever the expert's weights hold
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r] = own ? __builtin_fmaf(d[r], s, acc[r]) : acc[r];
+    }
+  }
+  lds_barrier();
+  v4f* const red = reinterpret_cast<v4f*>(smem);
+  red[wave * 64 + lane] = acc;
+  lds_barrier();
+  if (wave != 0) return;
+  v4f sum = red[lane];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) sum += red[w * 64 + lane];
+  if (r16 < p.T)
+    *reinterpret_cast<uint2*>(out + (int64_t)r16 * H + n0 + 4 * g) =
+        make_uint2(bf16x2_rne(sum[0], sum[1]), bf16x2_rne(sum[2], sum[3]));
+}
+
 // ---- tiled products ------------------------------------------------------------
 
 enum { kDense = 0, kGateUp = 1, kDown = 2 };
@@ -620,7 +723,8 @@ struct BlockArgs {
   uint16_t* y;             // dense [M, N]
   uint8_t* hq;             // gate/up: codes of h [T topk, N / 2]
   float* hs;               // gate/up: their scales [N / 256, T topk]
-  float* y32;              // down: weighted rows in sorted order [T topk, N]
+  uint16_t* y16;           // down: weighted rows in sorted order [T topk, N], float16 times ys
+  float* ys;               // down: [blocks of N, T topk]
   int32_t* slot_row;       // down: slot -> sorted row
   int E, topk, N, K, tiles_m, tiles_n;
 };
@@ -635,15 +739,46 @@ struct BlockTile {
   static constexpr int kStage = kCodes + (BM * 4 + 1023) / 1024 * 1024;   // and its row scales
   static constexpr int kRowsPerPass = kThreads / 8;
   static constexpr int kLoadsB = BN / kRowsPerPass, kLoadsA = BM / kRowsPerPass;
-  static constexpr int kEpiStride = BN * 2 + 16;  // dense: staged BF16 row
+  static constexpr int kEpiStride = BN * 2 + 16;  // dense, down: staged 16-bit row
   static constexpr int kHStride = 128 + 16;       // gate/up: staged row of h codes
-  static constexpr int kEpi = MODE == kDense ? BM * kEpiStride
-                              : MODE == kGateUp ? BM * kHStride + WGN * BM * 4 : WM * BN * 4;
+  static constexpr int kEpi = MODE == kGateUp ? BM * kHStride + WGN * BM * 4 : BM * kEpiStride;
   static constexpr int kLds = NS * kStage > kEpi ? NS * kStage : kEpi;
   static_assert(BN % kRowsPerPass == 0 && BM % kRowsPerPass == 0 && kRowsPerPass % 8 == 0, "stages split evenly");
   static_assert(WM % 16 == 0 && WN % 16 == 0 && BM % 64 == 0 && BM <= kThreads, "wave tiles");
   static_assert(MODE != kGateUp || (BN == 256 && SN % 2 == 0), "a gate/up tile is one block of 128 h columns");
 };
+
+// find_tile of grouped.h with its prefix sum by DPP: every workgroup starts with
+// it, and 6 exchanges through LDS were a quarter of a microsecond of each.
+__device__ inline bool find_block_tile(const int32_t* __restrict__ offsets, int E, int BM, int mt, int cap, int lane,
+                                       int& e_out, int& row0, int& rows) {
+  int before = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    const int start = offsets[min(e, E)], cnt = offsets[min(e + 1, E)] - start;
+    const int tiles = (cnt + BM - 1) / BM;
+    int incl = tiles;
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xF, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xF, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xA, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, false);
+    const uint64_t hit = __ballot(mt >= before + incl - tiles && mt < before + incl);
+    if (hit) {
+      const int src = __builtin_ctzll(hit);
+      const int local = mt - before - __builtin_amdgcn_readlane(incl - tiles, src);
+      e_out = e0 + src;
+      row0 = __builtin_amdgcn_readlane(start, src) + local * BM;
+      rows = min(BM, __builtin_amdgcn_readlane(cnt, src) - local * BM);
+      if (row0 < 0 || row0 >= cap) return false;
+      rows = min(rows, cap - row0);
+      return rows > 0;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
 
 // acc[i][j] += (w_i . x_j) * (sx[j] * sw[i]): kAhead MFMAs are under way before
 // the first result is added, then every MFMA is followed by the four FMAs of an
@@ -727,16 +862,22 @@ __device__ inline v8i frag_at(const uint8_t* st, int lane_off, int row0) {
 //           gate and the 16 matching up rows, so that g and u of an element meet
 //           in one lane. A tile's 128 columns of h are one block: its row maxima
 //           meet in LDS, and h leaves as codes and scales.
-//  kDown    y32 = router weight * (h . w2^T), a float32 row per sorted row.
+//  kDown    y = router weight * (h . w2^T), a row per sorted row, written in 16
+//           bits: float16 times a power of two for each 128 columns of a row, which
+//           rounds a copy by at most 2^-11 of its value where the sum over the copies
+//           is rounded to BF16 by up to 2^-8. In float32 these rows, written here and
+//           read once by the combine, were 536 MB of a pass of 4096 tokens, top-8, H
+//           2048. The power comes from a bound on the row's sums, |h| <= 448 hs and
+//           |w| <= 448 sw, so that no value can overflow and no maximum has to be
+//           found: what is 2^-29 of the bound and more keeps all 11 bits.
 // NS: stages. With one, half the LDS lets more workgroups run on a CU, and they
 // fill each other's waits: every tile of the larger sizes has one.
 template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, int NS, bool WIDE>
 __global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 void block_tiled(const BlockArgs p) {
   using C = BlockTile<BM, BN, WGM, WGN, MODE, NS>;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds + (MODE == kDense ? 0 : BM * 8)];
-  int* const row_slot = reinterpret_cast<int*>(smem + C::kLds);                // slot of a tile row, -1: none
-  float* const row_w = reinterpret_cast<float*>(smem + C::kLds + BM * 4);      // its router weight
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::kLds + (MODE == kDown ? BM * 4 : 0)];
+  float* const row_w = reinterpret_cast<float*>(smem + C::kLds);  // down: router weight of a tile row
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int N = p.N, K = p.K;
@@ -752,19 +893,8 @@ void block_tiled(const BlockArgs p) {
     if ((int)blockIdx.x < (per << 3)) t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     const int mt = t / p.tiles_n;
     nt = t - mt * p.tiles_n;
-    const int cap = (int)(MODE == kDown ? p.a_rows : p.a_rows * p.topk);
-    if (!find_tile(p.offsets, p.E, BM, mt, cap, e, row0, rows)) return;
-    for (int i = tid; i < BM; i += C::kThreads) {
-      int slot = -1;
-      if (i < rows) slot = p.perm[row0 + i];
-      if (slot >= cap) slot = -1;
-      row_slot[i] = slot;
-      if (MODE == kDown) {
-        row_w[i] = slot >= 0 ? p.tw[slot] : 0.f;
-        if (nt == 0 && slot >= 0) p.slot_row[slot] = row0 + i;
-      }
-    }
-    __syncthreads();
+    const int cap = (int)(MODE == kDown ? p.a_rows : p.a_rows * p.topk);  // sorted rows
+    if (!find_block_tile(p.offsets, p.E, BM, mt, cap, lane, e, row0, rows)) return;
   }
   const int n0 = nt * BN;
   const int nb = (N + 127) >> 7, nk = (K + 127) >> 7;
@@ -779,12 +909,27 @@ void block_tiled(const BlockArgs p) {
   // register, the others follow from the first.
   const uint32_t lbase = (uint32_t)lrow * (uint32_t)K + (uint32_t)lchunk;
   uint32_t arow[MODE == kGateUp ? C::kLoadsA : 1];
+  uint32_t soff = kOutOfRange;  // of this lane's row scale of a step: lane l of wave w < BM / 64 loads row 64 w + l
   if constexpr (MODE == kGateUp) {
+    const auto rP = make_rsrc(p.perm + row0, (int64_t)rows * 4);  // slots of the tile's rows
+    int slot[C::kLoadsA + 1];
 #pragma unroll
-    for (int j = 0; j < C::kLoadsA; ++j) {
-      const int slot = row_slot[lrow + C::kRowsPerPass * j];
-      arow[j] = slot < 0 ? kOutOfRange : (uint32_t)(slot / p.topk) * (uint32_t)K + (uint32_t)lchunk;
+    for (int j = 0; j < C::kLoadsA; ++j)
+      slot[j] = (int)__builtin_amdgcn_raw_buffer_load_b32(rP, (uint32_t)(lrow + C::kRowsPerPass * j) * 4u, 0, 0);
+    slot[C::kLoadsA] = (int)__builtin_amdgcn_raw_buffer_load_b32(rP, (uint32_t)tid * 4u, 0, 0);
+    const int cap = (int)(p.a_rows * p.topk);
+#pragma unroll
+    for (int j = 0; j <= C::kLoadsA; ++j) {
+      const int row = j < C::kLoadsA ? lrow + C::kRowsPerPass * j : tid;
+      const bool ok = row < rows && slot[j] >= 0 && slot[j] < cap;
+      const uint32_t tok = ok ? (uint32_t)slot[j] / (uint32_t)p.topk : 0u;
+      if (j < C::kLoadsA)
+        arow[j] = ok ? tok * (uint32_t)K + (uint32_t)lchunk : kOutOfRange;
+      else if (ok)
+        soff = tok * 4u;
     }
+  } else if (tid < rows) {
+    soff = (uint32_t)tid * 4u;
   }
   auto boff = [&](int i) {
     if constexpr (MODE == kGateUp) {  // 16-row piece b: even = gate rows, odd = the matching up rows
@@ -801,17 +946,6 @@ void block_tiled(const BlockArgs p) {
     else
       return lbase + (uint32_t)(C::kRowsPerPass * j) * (uint32_t)K;
   };
-  // this lane's row scale of a step: lane l of wave w < BM / 64 loads row 64 w + l
-  uint32_t soff = kOutOfRange;
-  if (wave < BM / 64) {
-    const int r = wave * 64 + lane;
-    if constexpr (MODE == kGateUp) {
-      const int slot = row_slot[r];
-      if (slot >= 0) soff = (uint32_t)(slot / p.topk) * 4u;
-    } else if (r < rows) {
-      soff = (uint32_t)r * 4u;
-    }
-  }
   auto issue = [&](int stage, int kt) {
     uint8_t* base = smem + stage * C::kStage;
     const int k0 = kt << 7;
@@ -847,12 +981,24 @@ void block_tiled(const BlockArgs p) {
     sBp[i] = (ScalarPtr)(sBe + (int64_t)b * nk);
   }
   v4f acc[C::SN][C::SM];
+  float size[C::SM];  // down: sum over the steps of the products of the scales
+#pragma unroll
+  for (int j = 0; j < C::SM; ++j) size[j] = 0.f;
 #pragma unroll
   for (int i = 0; i < C::SN; ++i)
 #pragma unroll
     for (int j = 0; j < C::SM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
   issue(0, 0);
+  if constexpr (MODE == kDown) {
+    // the rows' weights, used after the K loop, whose barriers order them
+    if (tid < BM) {
+      const int slot = tid < rows ? p.perm[row0 + tid] : -1;
+      const bool ok = slot >= 0 && slot < (int)p.a_rows;
+      row_w[tid] = ok ? p.tw[slot] : 0.f;
+      if (nt == 0 && ok) p.slot_row[slot] = row0 + tid;
+    }
+  }
   for (int kt = 0; kt < nk; ++kt) {
     float sw[kBlocks];
 #pragma unroll
@@ -875,6 +1021,11 @@ void block_tiled(const BlockArgs p) {
       lds_barrier();
       if (kt + 1 < nk) issue(0, kt + 1);
       __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (MODE == kDown) {
+      static_assert(MODE != kDown || kBlocks == 1, "a wave's columns lie in one block");
+#pragma unroll
+      for (int j = 0; j < C::SM; ++j) size[j] = __builtin_fmaf(sx[j], sw[0], size[j]);
     }
     if constexpr (WIDE)
       wide_mfmas<C::SN, C::SM, kBlocks>(acc, wf, xf, sx, sw);
@@ -951,44 +1102,94 @@ void block_tiled(const BlockArgs p) {
     }
   }
   if constexpr (MODE == kDown) {
-    // a wm's rows at a time through LDS, so that stores are whole row pieces;
-    // 16-byte chunks swizzled by row against bank conflicts
-    constexpr int kChunks = BN / 4;
-    static_assert(kChunks >= 16, "the swizzle exchanges 16 chunks");
 #pragma unroll
-    for (int pw = 0; pw < WGM; ++pw) {
-      if (pw) __syncthreads();
-      if (wm == pw) {
+    for (int j = 0; j < C::SM; ++j) {
+      const int ml = wm * C::WM + j * 16 + r16;
+      const float w = row_w[ml];
+      // the exponent of the bound, twice as large for the roundings of the sums and of itself
+      const float bound = size[j] * fabsf(w) * (2.0f * 128.0f * 448.0f * 448.0f);
+      const int e = (int)((__float_as_uint(bound) >> 23) & 0xFF) - 126;  // bound < 2^e
+      // 2^(15 - e) and back; infinite and NaN bounds make nothing smaller, nor do zeros
+      const int up = bound > 0.f && e < 129 ? min(15 - e, 126) : 0;
+      const float to = __uint_as_float((uint32_t)(127 + up) << 23), from = __uint_as_float((uint32_t)(127 - up) << 23);
+      const int col = n0 + wn * C::WN;
+      if (g == 0 && (col & 127) == 0 && ml < rows && col < N) p.ys[(int64_t)(col >> 7) * p.a_rows + row0 + ml] = from;
+      const float f = w * to;
 #pragma unroll
-        for (int j = 0; j < C::SM; ++j) {
-          const int rl = j * 16 + r16;
-          const float w = row_w[pw * C::WM + rl];
-#pragma unroll
-          for (int i = 0; i < C::SN; ++i) {
-            const int chunk = (wn * C::WN + i * 16) / 4 + g;
-            const v4f a = acc[i][j];
-            *reinterpret_cast<float4*>(smem + rl * (BN * 4) + ((chunk ^ (rl & 15)) << 4)) =
-                make_float4(a[0] * w, a[1] * w, a[2] * w, a[3] * w);
-          }
-        }
+      for (int i = 0; i < C::SN; ++i) {
+        const int nl = wn * C::WN + i * 16 + 4 * g;
+        const v4f a = acc[i][j];
+        typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+        const half2_t lo = {(_Float16)(a[0] * f), (_Float16)(a[1] * f)}, hi = {(_Float16)(a[2] * f), (_Float16)(a[3] * f)};
+        *reinterpret_cast<uint2*>(smem + ml * C::kEpiStride + nl * 2) =
+            make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
       }
-      __syncthreads();
-      for (int c = tid; c < C::WM * kChunks; c += C::kThreads) {
-        const int rl = c / kChunks, ch = c % kChunks, ml = pw * C::WM + rl;
-        if (row_slot[ml] >= 0 && n0 + ch * 4 < N)
-          store16_nt(p.y32 + (int64_t)(row0 + ml) * N + n0 + ch * 4,
-                     *reinterpret_cast<const float4*>(smem + rl * (BN * 4) + ((ch ^ (rl & 15)) << 4)));
-      }
+    }
+    __syncthreads();
+    constexpr int kRowChunks = BN / 8;
+    for (int c = tid; c < BM * kRowChunks; c += C::kThreads) {
+      const int row = c / kRowChunks, col = (c % kRowChunks) * 8;
+      if (row < rows && n0 + col < N)
+        store16_nt(p.y16 + (int64_t)(row0 + row) * N + n0 + col,
+                   *reinterpret_cast<const uint4*>(smem + row * C::kEpiStride + col * 2));
     }
   }
 }
 
-// The combine with the next pass's quantisation by blocks: 16 threads sum a
-// block of 128 columns of a token (in the order of combine_slots) and quantise
-// it as quantize_blocks does.
+// out[t] = bf16(sum over the token's valid slots, in order, of their rows of y16
+// times their scales), 8 columns a thread, 16 threads a block; with q also the
+// next pass's quantisation, as quantize_blocks does it. The rows are loaded
+// before any is added; a dropped slot's is not used.
+__global__ __launch_bounds__(256) void combine_half(const uint16_t* __restrict__ y, const float* __restrict__ ys,
+                                                    const int32_t* __restrict__ ids, const int32_t* __restrict__ slot_row,
+                                                    int64_t T, int topk, int E, int H, uint16_t* __restrict__ out,
+                                                    uint8_t* __restrict__ q, float* __restrict__ scale) {
+  const int kb = (H + 127) >> 7;
+  const int64_t b = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int64_t t = b / kb;
+  if (t >= T) return;
+  const int blk = (int)(b - t * kb), c = blk * 128 + 8 * (threadIdx.x & 15), at = c < H ? c : 0;
+  const int64_t cap = T * topk;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  constexpr int kBatch = 8;
+  for (int j0 = 0; j0 < topk; j0 += kBatch) {
+    v4i v[kBatch];
+    float f[kBatch];
+    bool ok[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t slot = t * topk + (j0 + i < topk ? j0 + i : 0);
+      const int id = ids[slot];
+      ok[i] = j0 + i < topk && id >= 0 && id < E;
+      const int64_t row = ok[i] ? slot_row[slot] : 0;
+      v[i] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(y + row * H + at));
+      f[i] = ys[(int64_t)blk * cap + row];
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (!ok[i]) continue;
+      typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+      const half8_t h = __builtin_bit_cast(half8_t, v[i]);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) sum[r] = __builtin_fmaf((float)h[r], f[i], sum[r]);
+    }
+  }
+  uint4 o = to_bf16x8(make_float4(sum[0], sum[1], sum[2], sum[3]), make_float4(sum[4], sum[5], sum[6], sum[7]));
+  if (c < H)
+    *reinterpret_cast<uint4*>(out + t * H + c) = o;
+  else
+    o = make_uint4(0u, 0u, 0u, 0u);
+  if (q == nullptr) return;
+  const float s = row_scale(row16_max(absmax8(o)));
+  if (c < H) *reinterpret_cast<uint2*>(q + t * H + c) = quant8(o, s, 1.0f / s);
+  if ((threadIdx.x & 15) == 0) scale[(int64_t)blk * T + t] = s;
+}
+
+// The combine of float32 rows (few tokens) with the next pass's quantisation by
+// blocks: 16 threads sum a block of 128 columns of a token (in the order of
+// combine_slots) and quantise it as quantize_blocks does.
 __global__ __launch_bounds__(256) void combine_block_quant(const float* __restrict__ y, const int32_t* __restrict__ ids,
-                                                           const int32_t* __restrict__ slot_row, int64_t T, int topk,
-                                                           int E, int H, uint16_t* __restrict__ out,
+                                                           int64_t T, int topk, int E, int H, uint16_t* __restrict__ out,
                                                            uint8_t* __restrict__ q, float* __restrict__ scale) {
   const int kb = (H + 127) >> 7;
   const int64_t b = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
@@ -998,7 +1199,7 @@ __global__ __launch_bounds__(256) void combine_block_quant(const float* __restri
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
   if (c < H) {
     float4 lo, hi;
-    sum_slots8(y, ids, slot_row, t, topk, E, H, c, lo, hi);
+    sum_slots8(y, ids, nullptr, t, topk, E, H, c, lo, hi);
     v = to_bf16x8(lo, hi);
     *reinterpret_cast<uint4*>(out + t * H + c) = v;
   }
@@ -1128,20 +1329,32 @@ size_t block_linear_workspace_bytes(int64_t M, int64_t K) {
 // tokens 103 against 77; 192 experts, top-4, H 1024: 128 tokens 62 against 85).
 static bool block_few(int64_t T, int64_t E, int64_t topk) { return T * topk <= kFewSlots && T * topk <= 8 * E; }
 
-static hipError_t launch_block_few(const BlockFewArgs& a, hipStream_t stream) {
+// And of those, the ones whose down projection makes the sum too (H 1024, I 512,
+// top-4 of 128: 1 token 10.9 us against 13.4 us, 3 tokens 14.7 against 15.2, 6 tokens
+// 20.6 against 18.1; with a launch less the host takes 3 us less).
+static bool block_small(int64_t T, int64_t I, int64_t topk) {
+  return T * topk <= kSmallSlots && T * topk * I <= kSmallCodes;
+}
+
+// small: where the sum goes, or NULL: y is left for the combine.
+static hipError_t launch_block_few(const BlockFewArgs& a, uint16_t* small, hipStream_t stream) {
   const int groups = a.by_slot ? a.n : a.E;
-  const dim3 gate((unsigned)(groups * (a.I / 16))), down((unsigned)(groups * ((a.H + 63) / 64)));
+  const dim3 gate((unsigned)(groups * (a.I / 16)));
   if (a.H <= 1024)
     hipLaunchKernelGGL(block_few_gate_up<2>, gate, dim3(256), 0, stream, a);
   else
     hipLaunchKernelGGL(block_few_gate_up<4>, gate, dim3(256), 0, stream, a);
-  hipLaunchKernelGGL(block_few_down, down, dim3(256), 0, stream, a);
+  if (small)
+    hipLaunchKernelGGL(block_small_down, dim3((unsigned)(a.H / 16)), dim3(1024), (size_t)std::max(a.n * a.I, 16 * 64 * 16),
+                       stream, a, small);
+  else
+    hipLaunchKernelGGL(block_few_down, dim3((unsigned)(groups * ((a.H + 63) / 64))), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
-// counts | offsets | perm | route scratch | codes of h | their scales | slot -> row | y
+// counts | offsets | perm | route scratch | codes of h | their scales | slot -> row | y | its scales
 struct BlockMoeLayout {
-  int64_t counts, offsets, perm, route, hq, hs, slot_row, y, total;
+  int64_t counts, offsets, perm, route, hq, hs, slot_row, y, ys, total;
 };
 
 static BlockMoeLayout block_moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
@@ -1155,7 +1368,8 @@ static BlockMoeLayout block_moe_layout(int64_t T, int64_t H, int64_t I, int64_t 
   L.hq = o, o += align256(n * I);
   L.hs = o, o += align256(I / 128 * n * 4);
   L.slot_row = o, o += align256(n * 4);
-  L.y = o, o += align256(n * H * 4);
+  L.y = o, o += align256(n * H * 2);
+  L.ys = o, o += align256((H + 127) / 128 * n * 4);
   L.total = o;
   return L;
 }
@@ -1169,27 +1383,30 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
                             const float* s13, const uint8_t* w2, const float* s2, uint16_t* out, uint8_t* out_q,
                             float* out_s, int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, void* ws,
                             hipStream_t stream) {
-  const auto combine = [&](const float* y, const int32_t* slot_row) {
-    if (out_q == nullptr) return launch_combine(y, ids, slot_row, T, topk, E, H, out, stream);
-    const int64_t groups = T * ((H + 127) / 128);
-    hipLaunchKernelGGL(combine_block_quant, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, stream, y, ids, slot_row, T,
-                       (int)topk, (int)E, (int)H, out, out_q, out_s);
-    return hipGetLastError();
-  };
+  const dim3 blocks((unsigned)((T * ((H + 127) / 128) + 15) / 16));  // of 16 blocks of the output
   if (block_few(T, E, topk)) {
     float* const h = static_cast<float*>(ws);
     float* const y = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256(T * topk * I * 4));
     const BlockFewArgs f{xq, xs, ids, tw, w13, w2, s13, s2, h, y, (int)T, (int)H, (int)I, (int)E, (int)topk,
                          (int)(T * topk), T * topk <= E ? 1 : 0};
-    const hipError_t e = launch_block_few(f, stream);
-    return e != hipSuccess ? e : combine(y, nullptr);
+    if (block_small(T, I, topk)) {
+      const hipError_t e = launch_block_few(f, out, stream);
+      return e != hipSuccess || out_q == nullptr ? e : launch_quantize_blocks(out, T, H, out_q, out_s, stream);
+    }
+    const hipError_t e = launch_block_few(f, nullptr, stream);
+    if (e != hipSuccess) return e;
+    if (out_q == nullptr) return launch_combine(y, ids, nullptr, T, topk, E, H, out, stream);
+    hipLaunchKernelGGL(combine_block_quant, blocks, dim3(256), 0, stream, y, ids, T, (int)topk, (int)E, (int)H, out, out_q,
+                       out_s);
+    return hipGetLastError();
   }
   const BlockMoeLayout L = block_moe_layout(T, H, I, E, topk);
   uint8_t* b = static_cast<uint8_t*>(ws);
   int32_t* const offsets = reinterpret_cast<int32_t*>(b + L.offsets);
   int32_t* const perm = reinterpret_cast<int32_t*>(b + L.perm);
   int32_t* const slot_row = reinterpret_cast<int32_t*>(b + L.slot_row);
-  float* const y = reinterpret_cast<float*>(b + L.y);
+  uint16_t* const y = reinterpret_cast<uint16_t*>(b + L.y);
+  float* const ys = reinterpret_cast<float*>(b + L.ys);
   hipError_t err = launch_route(ids, T, topk, E, 0, reinterpret_cast<int32_t*>(b + L.counts), offsets, perm, nullptr,
                                 b + L.route, stream);
   if (err != hipSuccess) return err;
@@ -1223,7 +1440,8 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
   d.B = w2;
   d.sB = s2;
   d.tw = tw;
-  d.y32 = y;
+  d.y16 = y;
+  d.ys = ys;
   d.slot_row = slot_row;
   d.N = (int)H;
   d.K = (int)I;
@@ -1232,7 +1450,9 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
   err = T * topk / E < 1000 ? run_tiled<64, 128, 2, 2, kDown, 4, 1>(d, stream)
                             : run_tiled<128, 256, 2, 2, kDown, 2, 1>(d, stream);
   if (err != hipSuccess) return err;
-  return combine(y, slot_row);
+  hipLaunchKernelGGL(combine_half, blocks, dim3(256), 0, stream, y, ys, ids, slot_row, T, (int)topk, (int)E, (int)H, out,
+                     out_q, out_s);
+  return hipGetLastError();
 }
 
 }  // namespace w8a8
