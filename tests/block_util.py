@@ -34,7 +34,7 @@ def violations(got_bits, ref64, err):
 
 
 def hidden_bound(h32, dh):
-    """The oracle's quantised h (values) and how far a GPU's may be off, given |h_gpu - h32| <= dh: the block's scale
+    """The oracle's quantised h (values), how far a GPU's may be off, given |h_gpu - h32| <= dh, and its scales [rows, blocks]: a block's scale
     moves by at most max dh / 448 and a rounding, and a code lies between those of the ends of its value's range."""
     q, s = oracle.quantize_row_blocks(h32)
     s_el = np.repeat(s.astype(np.float64).T, 128, axis=1)[:, :h32.shape[1]]
@@ -46,7 +46,7 @@ def hidden_bound(h32, dh):
     lo = oracle.decode(oracle.encode((v - dv).astype(np.float32)))
     hi = oracle.decode(oracle.encode((v + dv).astype(np.float32)))
     off = np.maximum(np.abs(lo - ref), np.abs(hi - ref)) * s_el + np.maximum(np.abs(lo), np.abs(hi)) * ds
-    return ref * s_el, off
+    return ref * s_el, off, s.T.astype(np.float64)
 
 
 def moe_ref(qx, sx, ids, tw, q13, s13, q2, s2, tokens=None):
@@ -63,12 +63,18 @@ def moe_ref(qx, sx, ids, tw, q13, s13, q2, s2, tokens=None):
         w13, w2 = oracle.weight_values(q13[e], s13[e]), oracle.weight_values(q2[e], s2[e])
         gu = x[t] @ w13.T
         h32, dh = swiglu_bound(gu, product_err(H, np.abs(x[t]) @ np.abs(w13).T))
-        h, off = hidden_bound(h32, dh)
+        h, off, hs = hidden_bound(h32, dh)
         w = np.asarray(tw, np.float64)[t, j][:, None]
         y, ymag = h @ w2.T, (np.abs(h) + off) @ np.abs(w2).T
         np.add.at(out, t, y * w)
         np.add.at(err, t, (off @ np.abs(w2).T + product_err(I, ymag)) * np.abs(w))
         np.add.at(mag, t, np.abs(y * w))
+        if T * k > min(512, 8 * E):
+            # beyond the few-row kernels a copy is float16 times a power of two: off by half a step, 2^-11 of its value,
+            # or half of float16's smallest step, 2^-25, times that power, which is at most 2^-14 of the bound it is
+            # taken from (256 * 448^2 * sum of the blocks' scale products); 1.01 for the bound on what is rounded
+            size = np.repeat(1.01 * hs @ s2[e].astype(np.float64).T, 128, axis=1)[:, :H] * np.abs(w)
+            np.add.at(err, t, 2.0 ** -11 * (np.abs(y * w) + off @ np.abs(w2).T * np.abs(w)) * 1.01 + 2.0 ** -39 * 256 * 448.0 ** 2 * size)
     return out[tokens], (err + (k + 3) * U32 * 1.01 * mag)[tokens]
 
 

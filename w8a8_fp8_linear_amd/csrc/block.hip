@@ -409,7 +409,7 @@ __device__ inline float block_scale_f32(uint32_t amax) { return amax == 0u ? 1.0
 // each workgroup itself, without the launches that sort them. With no more
 // routed copies (slots) than experts a group is a slot, and the first slot of
 // an expert works for all of them; otherwise a group is an expert.
-constexpr int kFewSlots = 1024;
+constexpr int kFewSlots = 512;
 
 struct BlockFewArgs {
   const uint8_t* x;    // [T, H] codes
@@ -744,7 +744,7 @@ struct BlockTile {
   static constexpr int kEpi = MODE == kGateUp ? BM * kHStride + WGN * BM * 4 : BM * kEpiStride;
   static constexpr int kLds = NS * kStage > kEpi ? NS * kStage : kEpi;
   static_assert(BN % kRowsPerPass == 0 && BM % kRowsPerPass == 0 && kRowsPerPass % 8 == 0, "stages split evenly");
-  static_assert(WM % 16 == 0 && WN % 16 == 0 && BM % 64 == 0 && BM <= kThreads, "wave tiles");
+  static_assert(WM % 16 == 0 && WN % 16 == 0 && BM <= kThreads, "wave tiles");
   static_assert(MODE != kGateUp || (BN == 256 && SN % 2 == 0), "a gate/up tile is one block of 128 h columns");
 };
 
@@ -909,7 +909,7 @@ void block_tiled(const BlockArgs p) {
   // register, the others follow from the first.
   const uint32_t lbase = (uint32_t)lrow * (uint32_t)K + (uint32_t)lchunk;
   uint32_t arow[MODE == kGateUp ? C::kLoadsA : 1];
-  uint32_t soff = kOutOfRange;  // of this lane's row scale of a step: lane l of wave w < BM / 64 loads row 64 w + l
+  uint32_t soff = kOutOfRange;  // of this lane's row scale of a step: lane l of the first waves loads row 64 w + l
   if constexpr (MODE == kGateUp) {
     const auto rP = make_rsrc(p.perm + row0, (int64_t)rows * 4);  // slots of the tile's rows
     int slot[C::kLoadsA + 1];
@@ -960,7 +960,7 @@ void block_tiled(const BlockArgs p) {
         buffer_load16_lds(rA, base + s0 * 16, kin && a != kOutOfRange ? a + (uint32_t)k0 : kOutOfRange);
       }
     }
-    if (wave < BM / 64) {
+    if (wave < (BM + 63) / 64) {
       const float* s = p.sA + (int64_t)kt * p.a_rows + (MODE == kGateUp ? 0 : row0);
       const auto rS = make_rsrc(s, (MODE == kGateUp ? p.a_rows : (int64_t)rows) * 4);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rS, (lds_void*)(base + C::kCodes + wave * 256), 4, soff, 0, 0, 0);
@@ -1324,9 +1324,10 @@ size_t block_linear_workspace_bytes(int64_t M, int64_t K) {
   return (size_t)(align256(M * K) + align256((K + 127) / 128 * M * 4));
 }
 
-// Whether the pass takes the kernels for groups of few rows: up to 8 on average
-// (H 2048, I 512, 64 experts, top-8: 64 tokens 63 us against 74 in tiles, 128
-// tokens 103 against 77; 192 experts, top-4, H 1024: 128 tokens 62 against 85).
+// Whether the pass takes the kernels for groups of few rows: up to 8 on average,
+// and few ids for every workgroup to look through (whole passes in tiles and here:
+// H 2048, I 512, top-8 of 64, 32 tokens 57.9 and 47.7 us, 64 tokens 60.6 and 62.6; H
+// 1024, top-4 of 192, 128 tokens 72.6 and 61.3, 256 tokens 75.9 and 88.4).
 static bool block_few(int64_t T, int64_t E, int64_t topk) { return T * topk <= kFewSlots && T * topk <= 8 * E; }
 
 // And of those, the ones whose down projection makes the sum too (H 1024, I 512,
@@ -1424,14 +1425,15 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
   p.topk = (int)topk;
   p.N = (int)(2 * I);
   p.K = (int)H;
-  // 64 x 256 tiles with one stage for every group size, on FP8 three workgroups a
-  // CU (whole passes, 4096 tokens, top-8 of 64: 268 us against 288 for 128 x 256
-  // with two stages; 16384 tokens: 916 against 1015; 1024: 105 against 116). Groups of
-  // up to 64 rows on average wait for their weights more than for the matrix unit,
-  // and take the exact sums of the widened codes for 6 to 8% of the pass (512 tokens
-  // 86 against 80 us; at 4096 it would be 310 against 250).
-  err = T * topk <= 64 * E ? run_tiled<64, 256, 1, 4, kGateUp, 2, 1, true>(p, stream)
-                           : run_tiled<64, 256, 1, 4, kGateUp, 3, 1>(p, stream);
+  // One stage, three workgroups a CU. Groups of up to 64 rows on average wait for
+  // their weights more than for the matrix unit: 32 rows a tile, and the exact sums
+  // of the widened codes (whole passes, H 2048, I 512, top-8 of 64: 256 tokens 66 us,
+  // on FP8 66, with 64 rows a tile 75 and 67; 512 tokens 77, 73, 81 and 73). Larger
+  // groups 64 rows on FP8 (1024 tokens 86 us, widened 103; 4096: 207 and 272; 128 rows
+  // and two stages 288 where 64 took 268, of which the copies in float32 were some 60).
+  const bool few = T * topk <= 64 * E;
+  err = few ? run_tiled<32, 256, 1, 4, kGateUp, 3, 1, true>(p, stream)
+            : run_tiled<64, 256, 1, 4, kGateUp, 3, 1>(p, stream);
   if (err != hipSuccess) return err;
   BlockArgs d = p;
   d.A = p.hq;
@@ -1445,10 +1447,11 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
   d.slot_row = slot_row;
   d.N = (int)H;
   d.K = (int)I;
-  // 64 x 128 tiles, four workgroups a CU, 128 x 256 for large groups (4096 tokens,
-  // top-8 of 64: 250 against 255 us for the pass; 16384 tokens: 878 against 864)
-  err = T * topk / E < 1000 ? run_tiled<64, 128, 2, 2, kDown, 4, 1>(d, stream)
-                            : run_tiled<128, 256, 2, 2, kDown, 2, 1>(d, stream);
+  // Whole passes with 32 x 256, 64 x 128 and 128 x 128 tiles: 256 tokens 72.8, 75.0 and
+  // 77.4 us, 1024 85.8, 86.2 and 89.5, 4096 213, 208 and 204, 16384 725, 698 and 672.
+  err = few                       ? run_tiled<32, 256, 1, 4, kDown, 4, 1>(d, stream)
+        : T * topk / E < 400 ? run_tiled<64, 128, 2, 2, kDown, 4, 1>(d, stream)
+                             : run_tiled<128, 128, 2, 2, kDown, 3, 1>(d, stream);
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(combine_half, blocks, dim3(256), 0, stream, y, ys, ids, slot_row, T, (int)topk, (int)E, (int)H, out,
                      out_q, out_s);
