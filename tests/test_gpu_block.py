@@ -167,7 +167,8 @@ def _moe_run(d, **kw):
 
 MOE_SHAPES = [(1, 16, 128, 1, 1), (1, 1024, 512, 128, 4), (3, 144, 256, 5, 2), (17, 272, 384, 9, 4), (37, 1024, 512, 192, 4),
               (64, 400, 128, 3, 3), (200, 528, 256, 6, 2), (301, 1040, 384, 40, 8), (900, 272, 256, 4, 3), (1500, 528, 128, 2, 2),
-              (4, 400, 512, 16, 4), (16, 272, 1024, 20, 1), (9, 144, 128, 3, 64), (130, 2064, 128, 8, 4), (70, 144, 1152, 40, 7)]
+              (4, 400, 512, 16, 4), (16, 272, 1024, 20, 1), (9, 144, 128, 3, 64), (130, 2064, 128, 8, 4), (70, 144, 1152, 40, 7),
+              (300, 144, 128, 600, 2), (33000, 128, 128, 16, 2)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", MOE_SHAPES)

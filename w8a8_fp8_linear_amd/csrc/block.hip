@@ -1129,9 +1129,18 @@ void block_tiled(const BlockArgs p) {
     constexpr int kRowChunks = BN / 8;
     for (int c = tid; c < BM * kRowChunks; c += C::kThreads) {
       const int row = c / kRowChunks, col = (c % kRowChunks) * 8;
-      if (row < rows && n0 + col < N)
-        store16_nt(p.y16 + (int64_t)(row0 + row) * N + n0 + col,
-                   *reinterpret_cast<const uint4*>(smem + row * C::kEpiStride + col * 2));
+      if (row < rows && n0 + col < N) {
+        const uint4 v = *reinterpret_cast<const uint4*>(smem + row * C::kEpiStride + col * 2);
+        uint4* const to = reinterpret_cast<uint4*>(p.y16 + (int64_t)(row0 + row) * N + n0 + col);
+        // Rows that the caches may keep for the combine, unless a group's rows outweigh its
+        // weights (tiles of 128 rows) and would drive these out (whole passes, kept and
+        // streamed: 4096 tokens, top-4 of 192, H 1024 120 and 125 us; top-8 of 64, H 2048
+        // 217 and 202).
+        if constexpr (BM >= 128)
+          store16_nt(to, v);
+        else
+          *to = v;
+      }
     }
   }
 }
@@ -1206,6 +1215,115 @@ __global__ __launch_bounds__(256) void combine_block_quant(const float* __restri
   const float s = row_scale(row16_max(absmax8(v)));
   if (c < H) *reinterpret_cast<uint2*>(q + t * H + c) = quant8(v, s, 1.0f / s);
   if ((threadIdx.x & 15) == 0) scale[(int64_t)blk * T + t] = s;
+}
+
+// The slots of 1024 consecutive ids a workgroup, grouped by expert in a stable
+// order (route_count and route_scatter of the other expert formats): every
+// workgroup counts all ids for itself, those before its own and the others, so
+// that one launch does for up to kRouteOneSlots slots. A counter has kRouteCopies
+// copies in LDS, for the lanes that meet at one expert.
+constexpr int kRouteThreads = 1024, kRouteWaves = 16, kRouteCopies = 8;
+
+__global__ __launch_bounds__(kRouteThreads) void block_route(const int32_t* __restrict__ ids, int n, int E,
+                                                             int32_t* __restrict__ offsets, int32_t* __restrict__ perm) {
+  extern __shared__ int route_lds[];
+  int* const before = route_lds;         // [E] ids of the chunks before, then the expert's next row
+  int* const total = route_lds + E;      // [E]
+  int* const hist = route_lds + 2 * E;   // [2][E][kRouteCopies], then [waves][E]
+  static_assert(kRouteWaves == 2 * kRouteCopies, "both take the same room");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lo = blockIdx.x * kRouteThreads, s = lo + tid;
+  const auto rI = make_rsrc(ids, (int64_t)n * 4);
+  const int own = (int)__builtin_amdgcn_raw_buffer_load_b32(rI, (uint32_t)s * 4u, 0, 0);
+  for (int e = tid; e < 2 * E * kRouteCopies; e += kRouteThreads) hist[e] = 0;
+  __syncthreads();
+  constexpr int kBatch = 8;
+  for (int i0 = 0; i0 < n; i0 += kBatch * 4 * kRouteThreads) {
+    v4i v[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) v[b] = buffer_load16(rI, (uint32_t)(i0 + 4 * (b * kRouteThreads + tid)) * 4u);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + 4 * (b * kRouteThreads + tid);
+      int* const h = hist + (i < lo ? 0 : E * kRouteCopies) + (lane & (kRouteCopies - 1));
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (i + r < n && v[b][r] >= 0 && v[b][r] < E) atomicAdd(h + v[b][r] * kRouteCopies, 1);
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += kRouteThreads) {
+    int b = 0, a = 0;
+#pragma unroll
+    for (int c = 0; c < kRouteCopies; ++c) {
+      b += hist[e * kRouteCopies + c];
+      a += hist[(E + e) * kRouteCopies + c];
+    }
+    before[e] = b;
+    total[e] = a + b;
+  }
+  __syncthreads();
+  for (int e = tid; e < kRouteWaves * E; e += kRouteThreads) hist[e] = 0;
+  __syncthreads();
+  int kept = 0;
+  if (wave == 0) {
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const int e = e0 + lane, t = e < E ? total[e] : 0;
+      int incl = t;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(incl, d, 64);
+        if (lane >= d) incl += u;
+      }
+      if (e < E) {
+        before[e] += kept + incl - t;
+        if (blockIdx.x == 0) offsets[e] = kept + incl - t;
+      }
+      kept += __shfl(incl, 63, 64);
+    }
+    if (lane == 0) {
+      total[0] = kept;
+      if (blockIdx.x == 0) offsets[E] = kept;
+    }
+  }
+  // the lanes of the wave that share this lane's expert (dropped ids share E)
+  const int key = s < n && own >= 0 && own < E ? own : E;
+  uint64_t peers = ~0ull;
+  for (int b = 0; (E >> b) != 0; ++b) {
+    const bool bit = (key >> b) & 1;
+    const uint64_t m = __ballot(bit);
+    peers &= bit ? m : ~m;
+  }
+  const int rank = __popcll(peers & ((1ull << lane) - 1));
+  if (rank == 0 && key < E) hist[wave * E + key] = __popcll(peers);
+  __syncthreads();
+  for (int e = tid; e < E; e += kRouteThreads) {
+    int row = before[e];
+#pragma unroll
+    for (int w = 0; w < kRouteWaves; ++w) {
+      const int c = hist[w * E + e];
+      hist[w * E + e] = row;
+      row += c;
+    }
+  }
+  __syncthreads();
+  if (key < E) perm[hist[wave * E + key] + rank] = s;
+  if (s < n && s >= total[0]) perm[s] = -1;  // rows behind the last group
+}
+
+// One launch up to here, where LDS holds the counters, and in two of the other
+// formats' kernels beyond (whole passes, H 256, I 128, one launch and two: 8192 slots,
+// 64 experts 24.8 and 28.5 us, 65536 slots 48.8 and 53.1, of 8 experts 59.7 and 62.1).
+constexpr int64_t kRouteOneSlots = 65536, kRouteOneExperts = 512;
+
+hipError_t run_route(const int32_t* ids, int64_t T, int64_t E, int64_t topk, int32_t* counts, int32_t* offsets,
+                     int32_t* perm, void* scratch, hipStream_t stream) {
+  const int64_t n = T * topk;
+  if (n > kRouteOneSlots || E > kRouteOneExperts)
+    return launch_route(ids, T, topk, E, 0, counts, offsets, perm, nullptr, scratch, stream);
+  hipLaunchKernelGGL(block_route, dim3((unsigned)((n + kRouteThreads - 1) / kRouteThreads)), dim3(kRouteThreads),
+                     (size_t)E * (2 + kRouteWaves) * 4, stream, ids, (int)n, (int)E, offsets, perm);
+  return hipGetLastError();
 }
 
 template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, int NS, bool WIDE = false>
@@ -1408,8 +1526,8 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
   int32_t* const slot_row = reinterpret_cast<int32_t*>(b + L.slot_row);
   uint16_t* const y = reinterpret_cast<uint16_t*>(b + L.y);
   float* const ys = reinterpret_cast<float*>(b + L.ys);
-  hipError_t err = launch_route(ids, T, topk, E, 0, reinterpret_cast<int32_t*>(b + L.counts), offsets, perm, nullptr,
-                                b + L.route, stream);
+  hipError_t err =
+      run_route(ids, T, E, topk, reinterpret_cast<int32_t*>(b + L.counts), offsets, perm, b + L.route, stream);
   if (err != hipSuccess) return err;
   BlockArgs p{};
   p.A = xq;
