@@ -717,16 +717,15 @@ struct BlockArgs {
   int64_t a_rows;
   const uint8_t* B;        // [E, N, K] codes (dense: E = 1)
   const float* sB;         // [E, blocks of N, blocks of K]
-  const int32_t* perm;     // sorted row -> slot
-  const int32_t* offsets;  // [E + 1]
-  const float* tw;         // [slots] router weights (down)
+  const int4* tiles;       // grouped: {their number}, then each one's expert, first sorted row and rows
+  const int32_t* tok;      // gate/up: token of a sorted row
+  const float* tw;         // down: router weight of a sorted row
   uint16_t* y;             // dense [M, N]
   uint8_t* hq;             // gate/up: codes of h [T topk, N / 2]
   float* hs;               // gate/up: their scales [N / 256, T topk]
   uint16_t* y16;           // down: weighted rows in sorted order [T topk, N], float16 times ys
   float* ys;               // down: [blocks of N, T topk]
-  int32_t* slot_row;       // down: slot -> sorted row
-  int E, topk, N, K, tiles_m, tiles_n;
+  int topk, N, K, tiles_m, tiles_n;
 };
 
 template <int BM, int BN, int WGM, int WGN, int MODE, int NS>
@@ -747,38 +746,6 @@ struct BlockTile {
   static_assert(WM % 16 == 0 && WN % 16 == 0 && BM <= kThreads, "wave tiles");
   static_assert(MODE != kGateUp || (BN == 256 && SN % 2 == 0), "a gate/up tile is one block of 128 h columns");
 };
-
-// find_tile of grouped.h with its prefix sum by DPP: every workgroup starts with
-// it, and 6 exchanges through LDS were a quarter of a microsecond of each.
-__device__ inline bool find_block_tile(const int32_t* __restrict__ offsets, int E, int BM, int mt, int cap, int lane,
-                                       int& e_out, int& row0, int& rows) {
-  int before = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    const int start = offsets[min(e, E)], cnt = offsets[min(e + 1, E)] - start;
-    const int tiles = (cnt + BM - 1) / BM;
-    int incl = tiles;
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, false);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, false);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xF, 0xF, false);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xF, 0xF, false);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xA, 0xF, false);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, false);
-    const uint64_t hit = __ballot(mt >= before + incl - tiles && mt < before + incl);
-    if (hit) {
-      const int src = __builtin_ctzll(hit);
-      const int local = mt - before - __builtin_amdgcn_readlane(incl - tiles, src);
-      e_out = e0 + src;
-      row0 = __builtin_amdgcn_readlane(start, src) + local * BM;
-      rows = min(BM, __builtin_amdgcn_readlane(cnt, src) - local * BM);
-      if (row0 < 0 || row0 >= cap) return false;
-      rows = min(rows, cap - row0);
-      return rows > 0;
-    }
-    before += __builtin_amdgcn_readlane(incl, 63);
-  }
-  return false;
-}
 
 // acc[i][j] += (w_i . x_j) * (sx[j] * sw[i]): kAhead MFMAs are under way before
 // the first result is added, then every MFMA is followed by the four FMAs of an
@@ -888,13 +855,18 @@ void block_tiled(const BlockArgs p) {
     row0 = tm * BM;
     rows = min(BM, (int)p.a_rows - row0);
   } else {
-    const int total = p.tiles_m * p.tiles_n, per = total >> 3;
-    int t = blockIdx.x;
-    if ((int)blockIdx.x < (per << 3)) t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    // the tiles there are, an eighth of them, consecutive, on each XCD
+    typedef const __attribute__((address_space(4))) int* ScalarInt;
+    const ScalarInt table = (ScalarInt)p.tiles;
+    const int64_t total = (int64_t)table[0] * p.tiles_n;
+    const int xcd = blockIdx.x & 7;
+    const int t = (int)(total * xcd / 8) + (int)(blockIdx.x >> 3);
+    if (t >= (int)(total * (xcd + 1) / 8)) return;
     const int mt = t / p.tiles_n;
     nt = t - mt * p.tiles_n;
-    const int cap = (int)(MODE == kDown ? p.a_rows : p.a_rows * p.topk);  // sorted rows
-    if (!find_block_tile(p.offsets, p.E, BM, mt, cap, lane, e, row0, rows)) return;
+    e = table[4 * mt + 4];
+    row0 = table[4 * mt + 5];
+    rows = table[4 * mt + 6];
   }
   const int n0 = nt * BN;
   const int nb = (N + 127) >> 7, nk = (K + 127) >> 7;
@@ -911,23 +883,16 @@ void block_tiled(const BlockArgs p) {
   uint32_t arow[MODE == kGateUp ? C::kLoadsA : 1];
   uint32_t soff = kOutOfRange;  // of this lane's row scale of a step: lane l of the first waves loads row 64 w + l
   if constexpr (MODE == kGateUp) {
-    const auto rP = make_rsrc(p.perm + row0, (int64_t)rows * 4);  // slots of the tile's rows
-    int slot[C::kLoadsA + 1];
+    const auto rT = make_rsrc(p.tok + row0, (int64_t)rows * 4);  // tokens of the tile's rows
+    uint32_t tok[C::kLoadsA + 1];
 #pragma unroll
     for (int j = 0; j < C::kLoadsA; ++j)
-      slot[j] = (int)__builtin_amdgcn_raw_buffer_load_b32(rP, (uint32_t)(lrow + C::kRowsPerPass * j) * 4u, 0, 0);
-    slot[C::kLoadsA] = (int)__builtin_amdgcn_raw_buffer_load_b32(rP, (uint32_t)tid * 4u, 0, 0);
-    const int cap = (int)(p.a_rows * p.topk);
+      tok[j] = __builtin_amdgcn_raw_buffer_load_b32(rT, (uint32_t)(lrow + C::kRowsPerPass * j) * 4u, 0, 0);
+    tok[C::kLoadsA] = __builtin_amdgcn_raw_buffer_load_b32(rT, (uint32_t)tid * 4u, 0, 0);
 #pragma unroll
-    for (int j = 0; j <= C::kLoadsA; ++j) {
-      const int row = j < C::kLoadsA ? lrow + C::kRowsPerPass * j : tid;
-      const bool ok = row < rows && slot[j] >= 0 && slot[j] < cap;
-      const uint32_t tok = ok ? (uint32_t)slot[j] / (uint32_t)p.topk : 0u;
-      if (j < C::kLoadsA)
-        arow[j] = ok ? tok * (uint32_t)K + (uint32_t)lchunk : kOutOfRange;
-      else if (ok)
-        soff = tok * 4u;
-    }
+    for (int j = 0; j < C::kLoadsA; ++j)
+      arow[j] = lrow + C::kRowsPerPass * j < rows ? tok[j] * (uint32_t)K + (uint32_t)lchunk : kOutOfRange;
+    if (tid < rows) soff = tok[C::kLoadsA] * 4u;
   } else if (tid < rows) {
     soff = (uint32_t)tid * 4u;
   }
@@ -992,12 +957,7 @@ void block_tiled(const BlockArgs p) {
   issue(0, 0);
   if constexpr (MODE == kDown) {
     // the rows' weights, used after the K loop, whose barriers order them
-    if (tid < BM) {
-      const int slot = tid < rows ? p.perm[row0 + tid] : -1;
-      const bool ok = slot >= 0 && slot < (int)p.a_rows;
-      row_w[tid] = ok ? p.tw[slot] : 0.f;
-      if (nt == 0 && ok) p.slot_row[slot] = row0 + tid;
-    }
+    if (tid < BM) row_w[tid] = tid < rows ? p.tw[row0 + tid] : 0.f;
   }
   for (int kt = 0; kt < nk; ++kt) {
     float sw[kBlocks];
@@ -1217,24 +1177,73 @@ __global__ __launch_bounds__(256) void combine_block_quant(const float* __restri
   if ((threadIdx.x & 15) == 0) scale[(int64_t)blk * T + t] = s;
 }
 
+// ---- the sorted order of the routed slots and its tiles
+
+struct RouteArgs {
+  const int32_t* ids;
+  const float* tw;
+  int32_t* tok;       // token of a sorted row
+  float* w;           // its router weight
+  int32_t* slot_row;  // slot -> sorted row
+  int4* tiles[2];     // of bm[0] and bm[1] rows (one table where these are equal), see BlockArgs
+  int n, E, topk, bm[2];
+};
+
+// Exclusive prefix sums of value(e) over the experts into out, by one wave; their total.
+template <class F>
+__device__ inline int expert_prefix(int E, int lane, F value, int* out) {
+  int before = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane, v = e < E ? value(e) : 0;
+    int incl = v;
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xF, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xF, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xA, 0xF, false);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, false);
+    if (e < E) out[e] = before + incl - v;
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return before;
+}
+
+// Tile i of a table, whose experts' first tiles are first[e], of `total`: its expert is
+// the last whose first tile is not behind it.
+__device__ inline void write_tile(int4* tiles, int bm, int i, int total, int E, const int* first, const int* start,
+                                  const int* count) {
+  if (i == 0) tiles[0] = make_int4(total, 0, 0, 0);
+  if (i >= total) return;
+  int e = 0;
+  for (int half = 512; half > 0; half >>= 1)
+    if (e + half < E && first[e + half] <= i) e += half;
+  const int r = (i - first[e]) * bm;
+  tiles[i + 1] = make_int4(e, start[e] + r, min(bm, count[e] - r), 0);
+}
+
 // The slots of 1024 consecutive ids a workgroup, grouped by expert in a stable
-// order (route_count and route_scatter of the other expert formats): every
+// order (as route_count and route_scatter of the other expert formats): every
 // workgroup counts all ids for itself, those before its own and the others, so
 // that one launch does for up to kRouteOneSlots slots. A counter has kRouteCopies
-// copies in LDS, for the lanes that meet at one expert.
+// copies in LDS, for the lanes that meet at one expert. There are no more tiles
+// than slots: each thread writes at most one of each table.
 constexpr int kRouteThreads = 1024, kRouteWaves = 16, kRouteCopies = 8;
 
-__global__ __launch_bounds__(kRouteThreads) void block_route(const int32_t* __restrict__ ids, int n, int E,
-                                                             int32_t* __restrict__ offsets, int32_t* __restrict__ perm) {
+__global__ __launch_bounds__(kRouteThreads) void block_route(const RouteArgs p) {
   extern __shared__ int route_lds[];
-  int* const before = route_lds;         // [E] ids of the chunks before, then the expert's next row
-  int* const total = route_lds + E;      // [E]
-  int* const hist = route_lds + 2 * E;   // [2][E][kRouteCopies], then [waves][E]
+  const int n = p.n, E = p.E;
+  int* const before = route_lds;          // [E] ids of the chunks before, then the expert's next row
+  int* const count = route_lds + E;       // [E]
+  int* const start = route_lds + 2 * E;   // [E]
+  int* const first = route_lds + 3 * E;   // [2][E]
+  int* const hist = route_lds + 5 * E;    // [2][E][kRouteCopies], then [waves][E]
+  __shared__ int totals[2];
   static_assert(kRouteWaves == 2 * kRouteCopies, "both take the same room");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lo = blockIdx.x * kRouteThreads, s = lo + tid;
-  const auto rI = make_rsrc(ids, (int64_t)n * 4);
+  const auto rI = make_rsrc(p.ids, (int64_t)n * 4);
   const int own = (int)__builtin_amdgcn_raw_buffer_load_b32(rI, (uint32_t)s * 4u, 0, 0);
+  const float own_w = s < n ? p.tw[s] : 0.f;
   for (int e = tid; e < 2 * E * kRouteCopies; e += kRouteThreads) hist[e] = 0;
   __syncthreads();
   constexpr int kBatch = 8;
@@ -1260,32 +1269,17 @@ __global__ __launch_bounds__(kRouteThreads) void block_route(const int32_t* __re
       a += hist[(E + e) * kRouteCopies + c];
     }
     before[e] = b;
-    total[e] = a + b;
+    count[e] = a + b;
   }
   __syncthreads();
   for (int e = tid; e < kRouteWaves * E; e += kRouteThreads) hist[e] = 0;
-  __syncthreads();
-  int kept = 0;
-  if (wave == 0) {
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      const int e = e0 + lane, t = e < E ? total[e] : 0;
-      int incl = t;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(incl, d, 64);
-        if (lane >= d) incl += u;
-      }
-      if (e < E) {
-        before[e] += kept + incl - t;
-        if (blockIdx.x == 0) offsets[e] = kept + incl - t;
-      }
-      kept += __shfl(incl, 63, 64);
-    }
-    if (lane == 0) {
-      total[0] = kept;
-      if (blockIdx.x == 0) offsets[E] = kept;
-    }
+  if (wave == 0) expert_prefix(E, lane, [&](int e) { return count[e]; }, start);
+  if (wave == 1 || wave == 2) {
+    const int bm = p.bm[wave - 1];
+    const int t = expert_prefix(E, lane, [&](int e) { return (count[e] + bm - 1) / bm; }, first + (wave - 1) * E);
+    if (lane == 0) totals[wave - 1] = t;
   }
+  __syncthreads();
   // the lanes of the wave that share this lane's expert (dropped ids share E)
   const int key = s < n && own >= 0 && own < E ? own : E;
   uint64_t peers = ~0ull;
@@ -1296,9 +1290,11 @@ __global__ __launch_bounds__(kRouteThreads) void block_route(const int32_t* __re
   }
   const int rank = __popcll(peers & ((1ull << lane) - 1));
   if (rank == 0 && key < E) hist[wave * E + key] = __popcll(peers);
+  write_tile(p.tiles[0], p.bm[0], s, totals[0], E, first, start, count);
+  if (p.tiles[1] != p.tiles[0]) write_tile(p.tiles[1], p.bm[1], s, totals[1], E, first + E, start, count);
   __syncthreads();
   for (int e = tid; e < E; e += kRouteThreads) {
-    int row = before[e];
+    int row = start[e] + before[e];
 #pragma unroll
     for (int w = 0; w < kRouteWaves; ++w) {
       const int c = hist[w * E + e];
@@ -1307,32 +1303,56 @@ __global__ __launch_bounds__(kRouteThreads) void block_route(const int32_t* __re
     }
   }
   __syncthreads();
-  if (key < E) perm[hist[wave * E + key] + rank] = s;
-  if (s < n && s >= total[0]) perm[s] = -1;  // rows behind the last group
+  if (key < E) {
+    const int row = hist[wave * E + key] + rank;
+    p.tok[row] = (int)((uint32_t)s / (uint32_t)p.topk);
+    p.w[row] = own_w;
+    p.slot_row[s] = row;
+  }
 }
 
-// One launch up to here, where LDS holds the counters, and in two of the other
-// formats' kernels beyond (whole passes, H 256, I 128, one launch and two: 8192 slots,
+// What block_route writes, from the order of route_scatter.
+__global__ __launch_bounds__(kRouteThreads) void block_route_rest(const RouteArgs p, const int32_t* __restrict__ offsets,
+                                                                  const int32_t* __restrict__ perm) {
+  __shared__ int start[1024], count[1024], first[2][1024], totals[2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t i = (int64_t)blockIdx.x * kRouteThreads + tid;
+  const int slot = i < p.n ? perm[i] : -1;
+  if (tid < p.E) {
+    start[tid] = offsets[tid];
+    count[tid] = offsets[tid + 1] - offsets[tid];
+  }
+  __syncthreads();
+  if (wave < 2) {
+    const int bm = p.bm[wave];
+    const int t = expert_prefix(p.E, lane, [&](int e) { return (count[e] + bm - 1) / bm; }, first[wave]);
+    if (lane == 0) totals[wave] = t;
+  }
+  if (slot >= 0) {
+    p.tok[i] = (int)((uint32_t)slot / (uint32_t)p.topk);
+    p.w[i] = p.tw[slot];
+  }
+  __syncthreads();
+  if (i >= p.n) return;
+  write_tile(p.tiles[0], p.bm[0], (int)i, totals[0], p.E, first[0], start, count);
+  if (p.tiles[1] != p.tiles[0]) write_tile(p.tiles[1], p.bm[1], (int)i, totals[1], p.E, first[1], start, count);
+}
+
+// One launch up to here, where LDS holds the counters, and three beyond, two of them
+// the other formats' (whole passes, H 256, I 128, one launch and two: 8192 slots,
 // 64 experts 24.8 and 28.5 us, 65536 slots 48.8 and 53.1, of 8 experts 59.7 and 62.1).
 constexpr int64_t kRouteOneSlots = 65536, kRouteOneExperts = 512;
 
-hipError_t run_route(const int32_t* ids, int64_t T, int64_t E, int64_t topk, int32_t* counts, int32_t* offsets,
-                     int32_t* perm, void* scratch, hipStream_t stream) {
-  const int64_t n = T * topk;
-  if (n > kRouteOneSlots || E > kRouteOneExperts)
-    return launch_route(ids, T, topk, E, 0, counts, offsets, perm, nullptr, scratch, stream);
-  hipLaunchKernelGGL(block_route, dim3((unsigned)((n + kRouteThreads - 1) / kRouteThreads)), dim3(kRouteThreads),
-                     (size_t)E * (2 + kRouteWaves) * 4, stream, ids, (int)n, (int)E, offsets, perm);
-  return hipGetLastError();
-}
+bool route_one(int64_t n, int64_t E) { return n <= kRouteOneSlots && E <= kRouteOneExperts; }
 
 template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, int NS, bool WIDE = false>
-hipError_t run_tiled(BlockArgs a, hipStream_t stream) {
+hipError_t run_tiled(BlockArgs a, int64_t tiles_m, hipStream_t stream) {
   a.tiles_n = (a.N + BN - 1) / BN;
-  const int64_t cap = MODE == kGateUp ? a.a_rows * a.topk : a.a_rows;
-  a.tiles_m = (int)((cap + BM - 1) / BM + (MODE == kDense ? 0 : a.E));  // a group adds at most one partial tile
-  hipLaunchKernelGGL((block_tiled<BM, BN, WGM, WGN, MODE, OCC, NS, WIDE>), dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)),
-                     dim3(64 * WGM * WGN), 0, stream, a);
+  a.tiles_m = (int)tiles_m;
+  // the same number of workgroups on each XCD, which takes an eighth of the tiles
+  const int64_t grid = MODE == kDense ? tiles_m * a.tiles_n : (tiles_m * a.tiles_n + 7) / 8 * 8;
+  hipLaunchKernelGGL((block_tiled<BM, BN, WGM, WGN, MODE, OCC, NS, WIDE>), dim3((unsigned)grid), dim3(64 * WGM * WGN), 0,
+                     stream, a);
   return hipGetLastError();
 }
 
@@ -1393,7 +1413,6 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
   p.B = w;
   p.sB = sw;
   p.y = y;
-  p.E = 1;
   p.topk = 1;
   p.N = (int)N;
   p.K = (int)K;
@@ -1410,12 +1429,12 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
   const auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
   if (tiles(32, 32) <= 256) return run_ksplit<2, 2, 3>(a, sa, w, sw, y, M, N, K, stream);
   if (tiles(64, 32) <= 256) return run_ksplit<4, 2, 1>(a, sa, w, sw, y, M, N, K, stream);
-  if (tiles(64, 64) <= 512) return run_tiled<64, 64, 2, 2, kDense, 2, 2>(p, stream);
-  if (tiles(64, 64) <= 768) return run_tiled<64, 64, 2, 2, kDense, 4, 1>(p, stream);
-  if (tiles(64, 128) <= 768) return run_tiled<64, 128, 2, 2, kDense, 4, 1>(p, stream);
+  if (tiles(64, 64) <= 512) return run_tiled<64, 64, 2, 2, kDense, 2, 2>(p, (M + 63) / 64, stream);
+  if (tiles(64, 64) <= 768) return run_tiled<64, 64, 2, 2, kDense, 4, 1>(p, (M + 63) / 64, stream);
+  if (tiles(64, 128) <= 768) return run_tiled<64, 128, 2, 2, kDense, 4, 1>(p, (M + 63) / 64, stream);
   if (3 * ((tiles(128, 256) + 511) / 512) < 2 * ((tiles(128, 128) + 767) / 768))
-    return run_tiled<128, 256, 2, 2, kDense, 2, 1>(p, stream);
-  return run_tiled<128, 128, 2, 2, kDense, 3, 1>(p, stream);
+    return run_tiled<128, 256, 2, 2, kDense, 2, 1>(p, (M + 127) / 128, stream);
+  return run_tiled<128, 128, 2, 2, kDense, 3, 1>(p, (M + 127) / 128, stream);
 }
 
 // Rows that are quantised inside the product, by every workgroup for itself:
@@ -1472,23 +1491,49 @@ static hipError_t launch_block_few(const BlockFewArgs& a, uint16_t* small, hipSt
 }
 
 // counts | offsets | perm | route scratch | codes of h | their scales | slot -> row | y | its scales
+// Rows of the gate/up and the down tiles. One stage, three workgroups a CU. Groups of
+// up to 64 rows on average wait for their weights more than for the matrix unit: 32
+// rows a tile, and the exact sums of the widened codes (whole passes, H 2048, I 512,
+// top-8 of 64: 256 tokens 66 us, on FP8 66, with 64 rows a tile 75 and 67; 512 tokens
+// 77, 73, 81 and 73). Larger groups 64 rows on FP8 (1024 tokens 86 us, widened 103;
+// 4096: 207 and 272).
+static bool block_narrow(int64_t T, int64_t E, int64_t topk) { return T * topk <= 64 * E; }
+static int gate_rows(int64_t T, int64_t E, int64_t topk) { return block_narrow(T, E, topk) ? 32 : 64; }
+// Whole passes with 32 x 256, 64 x 128 and 128 x 128 tiles: 256 tokens 72.8, 75.0 and
+// 77.4 us, 1024 85.8, 86.2 and 89.5, 4096 213, 208 and 204, 16384 725, 698 and 672.
+static int down_rows(int64_t T, int64_t E, int64_t topk) {
+  return block_narrow(T, E, topk) ? 32 : T * topk / E < 400 ? 64 : 128;
+}
+// A group adds at most one partial tile, and no tile is empty.
+static int64_t max_tiles(int64_t n, int64_t E, int64_t bm) { return std::min(n, n / bm + E); }
+
 struct BlockMoeLayout {
-  int64_t counts, offsets, perm, route, hq, hs, slot_row, y, ys, total;
+  int64_t tok, w, slot_row, tiles[2], hq, hs, y, ys, route, total;
 };
 
 static BlockMoeLayout block_moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
   BlockMoeLayout L;
   const int64_t n = T * topk;
   int64_t o = 0;
-  L.counts = o, o += align256(E * 4);
-  L.offsets = o, o += align256((E + 1) * 4);
-  L.perm = o, o += align256(n * 4);
-  L.route = o, o += (int64_t)route_workspace_bytes(T, topk, E);
+  const int64_t bm[2] = {gate_rows(T, E, topk), down_rows(T, E, topk)};
+  L.tok = o, o += align256(n * 4);
+  L.w = o, o += align256(n * 4);
+  L.slot_row = o, o += align256(n * 4);
+  for (int i = 0; i < 2; ++i) {
+    L.tiles[i] = o;
+    if (i == 0 || bm[1] != bm[0])
+      o += align256((1 + max_tiles(n, E, bm[i])) * 16);
+    else
+      L.tiles[1] = L.tiles[0];
+  }
   L.hq = o, o += align256(n * I);
   L.hs = o, o += align256(I / 128 * n * 4);
-  L.slot_row = o, o += align256(n * 4);
   L.y = o, o += align256(n * H * 2);
   L.ys = o, o += align256((H + 127) / 128 * n * 4);
+  // where the order takes three launches: route_scatter's part
+  L.route = o;
+  if (!route_one(n, E))
+    o += align256(E * 4) + align256((E + 1) * 4) + align256(n * 4) + (int64_t)route_workspace_bytes(T, topk, E);
   L.total = o;
   return L;
 }
@@ -1521,13 +1566,38 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
   }
   const BlockMoeLayout L = block_moe_layout(T, H, I, E, topk);
   uint8_t* b = static_cast<uint8_t*>(ws);
-  int32_t* const offsets = reinterpret_cast<int32_t*>(b + L.offsets);
-  int32_t* const perm = reinterpret_cast<int32_t*>(b + L.perm);
+  const int64_t n = T * topk;
   int32_t* const slot_row = reinterpret_cast<int32_t*>(b + L.slot_row);
   uint16_t* const y = reinterpret_cast<uint16_t*>(b + L.y);
   float* const ys = reinterpret_cast<float*>(b + L.ys);
-  hipError_t err =
-      run_route(ids, T, E, topk, reinterpret_cast<int32_t*>(b + L.counts), offsets, perm, b + L.route, stream);
+  RouteArgs r{};
+  r.ids = ids;
+  r.tw = tw;
+  r.tok = reinterpret_cast<int32_t*>(b + L.tok);
+  r.w = reinterpret_cast<float*>(b + L.w);
+  r.slot_row = slot_row;
+  for (int i = 0; i < 2; ++i) r.tiles[i] = reinterpret_cast<int4*>(b + L.tiles[i]);
+  r.n = (int)n;
+  r.E = (int)E;
+  r.topk = (int)topk;
+  r.bm[0] = gate_rows(T, E, topk);
+  r.bm[1] = down_rows(T, E, topk);
+  const dim3 chunks((unsigned)((n + kRouteThreads - 1) / kRouteThreads));
+  hipError_t err = hipSuccess;
+  if (route_one(n, E)) {
+    hipLaunchKernelGGL(block_route, chunks, dim3(kRouteThreads), (size_t)E * (5 + kRouteWaves) * 4, stream, r);
+    err = hipGetLastError();
+  } else {
+    uint8_t* at = b + L.route;
+    int32_t* const counts = reinterpret_cast<int32_t*>(at);
+    int32_t* const offsets = reinterpret_cast<int32_t*>(at += align256(E * 4));
+    int32_t* const perm = reinterpret_cast<int32_t*>(at += align256((E + 1) * 4));
+    err = launch_route(ids, T, topk, E, 0, counts, offsets, perm, slot_row, at + align256(n * 4), stream);
+    if (err == hipSuccess) {
+      hipLaunchKernelGGL(block_route_rest, chunks, dim3(kRouteThreads), 0, stream, r, offsets, perm);
+      err = hipGetLastError();
+    }
+  }
   if (err != hipSuccess) return err;
   BlockArgs p{};
   p.A = xq;
@@ -1535,41 +1605,34 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
   p.a_rows = T;
   p.B = w13;
   p.sB = s13;
-  p.perm = perm;
-  p.offsets = offsets;
+  p.tiles = r.tiles[0];
+  p.tok = r.tok;
   p.hq = b + L.hq;
   p.hs = reinterpret_cast<float*>(b + L.hs);
-  p.E = (int)E;
   p.topk = (int)topk;
   p.N = (int)(2 * I);
   p.K = (int)H;
-  // One stage, three workgroups a CU. Groups of up to 64 rows on average wait for
-  // their weights more than for the matrix unit: 32 rows a tile, and the exact sums
-  // of the widened codes (whole passes, H 2048, I 512, top-8 of 64: 256 tokens 66 us,
-  // on FP8 66, with 64 rows a tile 75 and 67; 512 tokens 77, 73, 81 and 73). Larger
-  // groups 64 rows on FP8 (1024 tokens 86 us, widened 103; 4096: 207 and 272; 128 rows
-  // and two stages 288 where 64 took 268, of which the copies in float32 were some 60).
-  const bool few = T * topk <= 64 * E;
-  err = few ? run_tiled<32, 256, 1, 4, kGateUp, 3, 1, true>(p, stream)
-            : run_tiled<64, 256, 1, 4, kGateUp, 3, 1>(p, stream);
+  int64_t tiles = max_tiles(n, E, r.bm[0]);
+  err = r.bm[0] == 32 ? run_tiled<32, 256, 1, 4, kGateUp, 3, 1, true>(p, tiles, stream)
+                      : run_tiled<64, 256, 1, 4, kGateUp, 3, 1>(p, tiles, stream);
   if (err != hipSuccess) return err;
-  BlockArgs d = p;
+  BlockArgs d{};
   d.A = p.hq;
   d.sA = p.hs;
-  d.a_rows = T * topk;
+  d.a_rows = n;
   d.B = w2;
   d.sB = s2;
-  d.tw = tw;
+  d.tiles = r.tiles[1];
+  d.tw = r.w;
   d.y16 = y;
   d.ys = ys;
-  d.slot_row = slot_row;
+  d.topk = (int)topk;
   d.N = (int)H;
   d.K = (int)I;
-  // Whole passes with 32 x 256, 64 x 128 and 128 x 128 tiles: 256 tokens 72.8, 75.0 and
-  // 77.4 us, 1024 85.8, 86.2 and 89.5, 4096 213, 208 and 204, 16384 725, 698 and 672.
-  err = few                       ? run_tiled<32, 256, 1, 4, kDown, 4, 1>(d, stream)
-        : T * topk / E < 400 ? run_tiled<64, 128, 2, 2, kDown, 4, 1>(d, stream)
-                             : run_tiled<128, 128, 2, 2, kDown, 3, 1>(d, stream);
+  tiles = max_tiles(n, E, r.bm[1]);
+  err = r.bm[1] == 32   ? run_tiled<32, 256, 1, 4, kDown, 4, 1>(d, tiles, stream)
+        : r.bm[1] == 64 ? run_tiled<64, 128, 2, 2, kDown, 4, 1>(d, tiles, stream)
+                        : run_tiled<128, 128, 2, 2, kDown, 3, 1>(d, tiles, stream);
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(combine_half, blocks, dim3(256), 0, stream, y, ys, ids, slot_row, T, (int)topk, (int)E, (int)H, out,
                      out_q, out_s);
