@@ -69,7 +69,7 @@ def moe_ref(qx, sx, ids, tw, q13, s13, q2, s2, tokens=None):
         np.add.at(out, t, y * w)
         np.add.at(err, t, (off @ np.abs(w2).T + product_err(I, ymag)) * np.abs(w))
         np.add.at(mag, t, np.abs(y * w))
-        if T * k > min(512, 8 * E):
+        if T * k > min(256, 8 * E):
             # beyond the few-row kernels a copy is float16 times a power of two: off by half a step, 2^-11 of its value,
             # or half of float16's smallest step, 2^-25, times that power, which is at most 2^-14 of the bound it is
             # taken from (256 * 448^2 * sum of the blocks' scale products); 1.01 for the bound on what is rounded

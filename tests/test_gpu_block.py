@@ -202,7 +202,7 @@ def test_experts_nothing_routed():
     assert not bf16_bits(_moe_run(d)).any()
 
 
-@pytest.mark.parametrize("T,H", [(5, 144), (70, 512), (300, 1040)])
+@pytest.mark.parametrize("T,H", [(5, 144), (10, 144), (70, 512), (300, 1040)])
 def test_experts_quantised_output(T, H):
     d = _moe(T, H, 256, 6, 3, T)
     out, q, s = _moe_run(d, quantize_output=True)

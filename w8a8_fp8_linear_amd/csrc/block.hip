@@ -409,7 +409,7 @@ __device__ inline float block_scale_f32(uint32_t amax) { return amax == 0u ? 1.0
 // each workgroup itself, without the launches that sort them. With no more
 // routed copies (slots) than experts a group is a slot, and the first slot of
 // an expert works for all of them; otherwise a group is an expert.
-constexpr int kFewSlots = 512;
+constexpr int kFewSlots = 256;
 
 struct BlockFewArgs {
   const uint8_t* x;    // [T, H] codes
@@ -1462,9 +1462,10 @@ size_t block_linear_workspace_bytes(int64_t M, int64_t K) {
 }
 
 // Whether the pass takes the kernels for groups of few rows: up to 8 on average,
-// and few ids for every workgroup to look through (whole passes in tiles and here:
-// H 2048, I 512, top-8 of 64, 32 tokens 57.9 and 47.7 us, 64 tokens 60.6 and 62.6; H
-// 1024, top-4 of 192, 128 tokens 72.6 and 61.3, 256 tokens 75.9 and 88.4).
+// and few ids for every workgroup to look through (whole passes in tiles and here, I
+// 512: top-8 of 64, H 2048, 16 tokens 49.4 and 43.3 us, 32 tokens 52.4 and 50.7, 48
+// tokens 53.2 and 57.0; top-4 of 192, H 1024, 37 tokens 44.4 and 42.7, 64 tokens 49.0
+// and 50.7, 96 tokens 53.4 and 63.0; top-2 of 8, H 1024, 32 tokens 27.6 and 17.2).
 static bool block_few(int64_t T, int64_t E, int64_t topk) { return T * topk <= kFewSlots && T * topk <= 8 * E; }
 
 // And of those, the ones whose down projection makes the sum too (H 1024, I 512,
