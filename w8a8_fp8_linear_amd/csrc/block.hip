@@ -1493,17 +1493,18 @@ static hipError_t launch_block_few(const BlockFewArgs& a, uint16_t* small, hipSt
 
 // counts | offsets | perm | route scratch | codes of h | their scales | slot -> row | y | its scales
 // Rows of the gate/up and the down tiles. One stage, three workgroups a CU. Groups of
-// up to 64 rows on average wait for their weights more than for the matrix unit: 32
-// rows a tile, and the exact sums of the widened codes (whole passes, H 2048, I 512,
-// top-8 of 64: 256 tokens 66 us, on FP8 66, with 64 rows a tile 75 and 67; 512 tokens
-// 77, 73, 81 and 73). Larger groups 64 rows on FP8 (1024 tokens 86 us, widened 103;
-// 4096: 207 and 272).
-static bool block_narrow(int64_t T, int64_t E, int64_t topk) { return T * topk <= 64 * E; }
+// up to 48 rows on average wait for their weights more than for the matrix unit: 32
+// rows a tile, and the exact sums of the widened codes; larger ones 64 rows on FP8
+// (whole passes, I 512, 32 rows and 64: top-8 of 64, H 2048, 384 tokens 56.7 and 58.8
+// us, 512 tokens 65.4 and 60.6, 1024 tokens 90.7 and 74.4; top-4 of 192, H 1024, 1024
+// tokens 71.2 and 71.3, 2048 tokens 86.1 and 83.4, 3000 tokens 101 and 92).
+static bool block_narrow(int64_t T, int64_t E, int64_t topk) { return T * topk <= 48 * E; }
 static int gate_rows(int64_t T, int64_t E, int64_t topk) { return block_narrow(T, E, topk) ? 32 : 64; }
-// Whole passes with 32 x 256, 64 x 128 and 128 x 128 tiles: 256 tokens 72.8, 75.0 and
-// 77.4 us, 1024 85.8, 86.2 and 89.5, 4096 213, 208 and 204, 16384 725, 698 and 672.
+// 64 x 128 and 128 x 128 tiles: top-8 of 64, 2048 tokens 116.9 and 115.7 us, 3000
+// tokens 158.8 and 148.8, 4096 tokens 209 and 188; top-4 of 192, 16384 tokens 240 and
+// 246 (the larger stream their rows out).
 static int down_rows(int64_t T, int64_t E, int64_t topk) {
-  return block_narrow(T, E, topk) ? 32 : T * topk / E < 400 ? 64 : 128;
+  return block_narrow(T, E, topk) ? 32 : T * topk / E < 350 ? 64 : 128;
 }
 // A group adds at most one partial tile, and no tile is empty.
 static int64_t max_tiles(int64_t n, int64_t E, int64_t bm) { return std::min(n, n / bm + E); }
