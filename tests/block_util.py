@@ -70,11 +70,12 @@ def moe_ref(qx, sx, ids, tw, q13, s13, q2, s2, tokens=None):
         np.add.at(err, t, (off @ np.abs(w2).T + product_err(I, ymag)) * np.abs(w))
         np.add.at(mag, t, np.abs(y * w))
         if T * k > min(256, 8 * E):
-            # beyond the few-row kernels a copy is float16 times a power of two: off by half a step, 2^-11 of its value,
-            # or half of float16's smallest step, 2^-25, times that power, which is at most 2^-14 of the bound it is
-            # taken from (256 * 448^2 * sum of the blocks' scale products); 1.01 for the bound on what is rounded
+            # beyond the few-row kernels a copy is float16 times a power of two p: off by half a step, 2^-11 of its
+            # value, or by half of float16's smallest step, 2^-25 p. With size the sum of the blocks' scale products,
+            # 2^x <= size and 2^y <= |tw| the powers next below, p = 2^(x + y + 2 + 26 - 15) <= 2^13 size |tw|.
+            # 1.01 for the roundings of what is rounded and of size.
             size = np.repeat(1.01 * hs @ s2[e].astype(np.float64).T, 128, axis=1)[:, :H] * np.abs(w)
-            np.add.at(err, t, 2.0 ** -11 * (np.abs(y * w) + off @ np.abs(w2).T * np.abs(w)) * 1.01 + 2.0 ** -39 * 256 * 448.0 ** 2 * size)
+            np.add.at(err, t, 2.0 ** -11 * (np.abs(y * w) + off @ np.abs(w2).T * np.abs(w)) * 1.01 + 2.0 ** (13 - 25) * size)
     return out[tokens], (err + (k + 3) * U32 * 1.01 * mag)[tokens]
 
 

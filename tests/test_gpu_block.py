@@ -211,6 +211,21 @@ def test_experts_quantised_output(T, H):
     assert torch.equal(out, _moe_run(d))
 
 
+@pytest.mark.parametrize("T", [2, 7, 40, 200, 1300])
+def test_experts_scaled_by_powers_of_two(T):
+    """Scales and router weights times powers of two move the output by their product and not a bit besides, up to
+    where the bound on a copy's values is beyond float32 though the values are not; negated scales negate."""
+    d = _moe(T, 272, 256, 6, 2, 31 + T)
+    base = _moe_run(d)
+    q13, s13, q2, s2 = d["w"]
+    for a, b in ((100, 0), (60, 45), (-40, 20), (-60, -20), (20, -90)):
+        e = dict(d, w=(q13, s13, q2, np.ldexp(s2, a).astype(np.float32)), tw=np.ldexp(d["tw"], b).astype(np.float32))
+        want = torch.ldexp(base.double(), torch.tensor(a + b)).float().bfloat16()
+        assert bool(want.isfinite().all())
+        assert torch.equal(_moe_run(e), want)
+    assert torch.equal(_moe_run(dict(d, w=(q13, s13, q2, -s2))), -base)
+
+
 @pytest.mark.parametrize("T", [3, 260])
 def test_two_passes(T):
     """moe_block_ffn is the chain of its calls; each pass is checked on the codes that the one before it left."""

@@ -836,7 +836,7 @@ __device__ inline v8i frag_at(const uint8_t* st, int lane_off, int row0) {
 //           read once by the combine, were 536 MB of a pass of 4096 tokens, top-8, H
 //           2048. The power comes from a bound on the row's sums, |h| <= 448 hs and
 //           |w| <= 448 sw, so that no value can overflow and no maximum has to be
-//           found: what is 2^-29 of the bound and more keeps all 11 bits.
+//           found: what is 2^-27 of the bound and more keeps all 11 bits.
 // NS: stages. With one, half the LDS lets more workgroups run on a CU, and they
 // fill each other's waits: every tile of the larger sizes has one.
 template <int BM, int BN, int WGM, int WGN, int MODE, int OCC, int NS, bool WIDE>
@@ -985,7 +985,7 @@ void block_tiled(const BlockArgs p) {
     if constexpr (MODE == kDown) {
       static_assert(MODE != kDown || kBlocks == 1, "a wave's columns lie in one block");
 #pragma unroll
-      for (int j = 0; j < C::SM; ++j) size[j] = __builtin_fmaf(sx[j], sw[0], size[j]);
+      for (int j = 0; j < C::SM; ++j) size[j] = __builtin_fmaf(fabsf(sx[j]), fabsf(sw[0]), size[j]);
     }
     if constexpr (WIDE)
       wide_mfmas<C::SN, C::SM, kBlocks>(acc, wf, xf, sx, sw);
@@ -1066,11 +1066,12 @@ void block_tiled(const BlockArgs p) {
     for (int j = 0; j < C::SM; ++j) {
       const int ml = wm * C::WM + j * 16 + r16;
       const float w = row_w[ml];
-      // the exponent of the bound, twice as large for the roundings of the sums and of itself
-      const float bound = size[j] * fabsf(w) * (2.0f * 128.0f * 448.0f * 448.0f);
-      const int e = (int)((__float_as_uint(bound) >> 23) & 0xFF) - 126;  // bound < 2^e
-      // 2^(15 - e) and back; infinite and NaN bounds make nothing smaller, nor do zeros
-      const int up = bound > 0.f && e < 129 ? min(15 - e, 126) : 0;
+      // size < 2^(bs - 126), |w| < 2^(bw - 126): the row's values stay below 2^e, with a factor
+      // of two for the roundings of the sums, whatever of the product might overflow
+      const int bs = (int)(__float_as_uint(size[j]) >> 23), bw = (int)(__float_as_uint(w) >> 23) & 0xFF;
+      const int e = bs + bw - 252 + 26;  // 2 * 128 * 448^2 < 2^26
+      // 2^(15 - e) and back, which neither take w out of range; infinite and NaN scales keep 1
+      const int up = bs == 255 || bw == 255 ? 0 : max(-113, min(15 - e, min(126, 253 - bw)));
       const float to = __uint_as_float((uint32_t)(127 + up) << 23), from = __uint_as_float((uint32_t)(127 - up) << 23);
       const int col = n0 + wn * C::WN;
       if (g == 0 && (col & 127) == 0 && ml < rows && col < N) p.ys[(int64_t)(col >> 7) * p.a_rows + row0 + ml] = from;
