@@ -118,8 +118,11 @@ def balance_loss(logits, ids, coef, sequences=1, score="softmax"):
                 v = np.exp(l - np.where(np.isneginf(top), 0.0, top))
                 slope = np.ones_like(v)
             else:
-                v = 1.0 / (1.0 + np.exp(-l))
-                slope = 1.0 - v
+                # over their largest: sigmoids themselves end at e^-745
+                v = -np.logaddexp(0.0, -l)
+                slope = -np.expm1(v)
+                top = v.max(1, keepdims=True)
+                v = np.exp(v - np.where(np.isneginf(top), 0.0, top))
         z = v.sum(1, keepdims=True)
         q = np.divide(v, z, out=np.zeros_like(v), where=z > 0)
         f = E * counts[s] / (k * n)

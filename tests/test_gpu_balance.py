@@ -86,9 +86,17 @@ def test_barred_experts(score):
     t = torch.from_numpy(l).cuda()
     _, _, grad = _check(t, l, ids, S, score)
     assert not grad[:, 7].any() and not grad[:, 11].any() and not grad[5].any()
-    if score == "softmax":  # all alike, however low: an even choice
-        l[8] = np.finfo(np.float32).min
-        _check(torch.from_numpy(l).cuda(), l, ids, S, score)
+    l[8] = np.finfo(np.float32).min  # all alike, however low: an even choice
+    _check(torch.from_numpy(l).cuda(), l, ids, S, score)
+
+
+@pytest.mark.parametrize("E,k", [(40, 3), (128, 4), (300, 5)])
+def test_sigmoids_below_float32(E, k):
+    """Logits whose sigmoids float32 does not hold still choose between experts; beside tokens of ordinary logits."""
+    t, l, ids = _inputs(2, 50, E, k, E, pad=0.1)
+    for row, shift in ((3, -60.0), (4, -100.0), (50, -200.0), (51, -1.0e4), (99, -3.0e38)):
+        l[row] = l[row] + np.float32(shift)
+    _check(torch.from_numpy(l).cuda(), l, ids, 2, "sigmoid")
 
 
 def test_gradient_against_differences():

@@ -137,7 +137,7 @@ struct Tokens {
     const int l = lane % LANES;
     const uint64_t group = LANES == 64 ? ~0ull : ((1ull << (LANES & 63)) - 1) << (lane - l);
     float x[UT][NC][4], inv[UT], dot[UT];
-    bool here[UT];
+    bool here[UT], low[UT];
 #pragma unroll
     for (int u = 0; u < UT; ++u) {
       here[u] = (__ballot(id[u] >= 0 && id[u] < p.E) & group) != 0 && t0 + (int64_t)u * step < p.L;
@@ -162,6 +162,26 @@ struct Tokens {
           z += x[u][i][r];
         }
       z = group_sum<LANES>(z);
+      // sigmoids too small for float32, where sigmoid(v) is e^v: the same p from a softmax
+      low[u] = sigmoid && z < 0x1p-60f;
+      if (low[u]) {
+        m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) m = fmaxf(m, value(u, i, r, 4 * (l + LANES * i), p.E));
+        m = group_max<LANES>(m);
+        m = m == -INFINITY ? 0.f : m;
+        z = 0.f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            x[u][i][r] = __expf(value(u, i, r, 4 * (l + LANES * i), p.E) - m);
+            z += x[u][i][r];
+          }
+        z = group_sum<LANES>(z);
+      }
       inv[u] = z > 0.f ? 1.0f / z : 0.f;
       float d = 0.f;
 #pragma unroll
@@ -183,7 +203,7 @@ struct Tokens {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           // d p_j / d l_j = p_j (1 - sigmoid(l_j)) for sigmoids divided by their sum
-          const float v = x[u][i][r], slope = sigmoid ? 1.0f - v : 1.0f;
+          const float v = x[u][i][r], slope = sigmoid && !low[u] ? 1.0f - v : 1.0f;
           d[r] = here[u] ? v * inv[u] * slope * (w[i][r] - dot[u]) : 0.f;
         }
         TL* dst = grad + (row0 + t) * p.E + e;
