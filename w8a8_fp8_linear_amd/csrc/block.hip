@@ -424,28 +424,31 @@ struct BlockFewArgs {
 };
 
 // The expert of group `grp` and, in LDS, its slots in order; the number of slots
-// (0: nothing to do). Every wave writes the same list; a barrier follows.
+// (0: nothing to do). Every wave writes the same list; a barrier follows. All ids
+// are loaded at once, the group's own among them: one latency before the weights.
 __device__ inline int few_group(const BlockFewArgs& p, int grp, int lane, int* list, int& e) {
-  e = p.by_slot ? __builtin_amdgcn_readfirstlane(p.ids[grp]) : grp;
+  constexpr int kPer = kFewSlots / 64;
+  int id[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (64 * i < p.n) id[i] = p.ids[64 * i + lane < p.n ? 64 * i + lane : 0];
+  e = grp;
+  if (p.by_slot) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (grp >> 6 == i) e = __builtin_amdgcn_readlane(id[i], grp & 63);
+  }
+  if (e < 0 || e >= p.E) return 0;
   int n = 0;
-  if (e >= 0 && e < p.E) {
-    for (int base = 0; base < p.n; base += 256) {
-      int id[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int s = base + 64 * i + lane;
-        id[i] = p.ids[s < p.n ? s : 0];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int s = base + 64 * i + lane;
-        const bool mine = s < p.n && id[i] == e;
-        const uint64_t m = __ballot(mine);
-        if (mine) list[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u))] = s;
-        if (p.by_slot && n == 0 && m != 0 && base + 64 * i + __builtin_ctzll(m) != grp) return 0;  // not the first
-        n += __builtin_popcountll(m);
-      }
-    }
+  for (int i = 0; i < kPer; ++i) {
+    if (64 * i >= p.n) break;
+    const int s = 64 * i + lane;
+    const bool mine = s < p.n && id[i] == e;
+    const uint64_t m = __ballot(mine);
+    if (mine) list[n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u))] = s;
+    if (p.by_slot && n == 0 && m != 0 && 64 * i + __builtin_ctzll(m) != grp) return 0;  // not the first
+    n += __builtin_popcountll(m);
   }
   return n;
 }
