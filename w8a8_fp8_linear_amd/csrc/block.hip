@@ -563,18 +563,25 @@ __global__ __launch_bounds__(256) void block_few_down(const BlockFewArgs p) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < I; k0 += kCols) {
+      const int c = k0 + 8 * lane, step = lane >> 4, piece = (lane & 15) >> 1;
+      v4i ha, hb;
+      auto load_h = [&](int r) {  // zeros past the row's end
+        const int slot = __builtin_amdgcn_readfirstlane(list[r0 + min(r, rows - 1)]);
+        const auto rH = make_rsrc(p.h + (int64_t)slot * I, (int64_t)I * 4);
+        ha = buffer_load16(rH, (uint32_t)c * 4u);
+        hb = buffer_load16(rH, (uint32_t)c * 4u + 16u);
+      };
+      // the first rows, then the weights: loads return in order, and the rows are needed first
+      load_h(wave);
       v8i wf[1][NT];
       float sw[1][1];
       skinny_weights(rW, 16, sWrow, k0 >> 7, nk, I, wave, r16, g, wf, sw);
+      __builtin_amdgcn_sched_barrier(0);
       if (r0 || k0) lds_barrier();  // the codes or sums before have been read
-      const int c = k0 + 8 * lane, step = lane >> 4, piece = (lane & 15) >> 1;
       for (int r = wave; r < rows; r += 4) {
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (c < I) {
-          const float* src = p.h + (int64_t)list[r0 + r] * I + c;
-          const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
-          v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        }
+        if (r != wave) load_h(r);
+        const float v[8] = {__int_as_float(ha.x), __int_as_float(ha.y), __int_as_float(ha.z), __int_as_float(ha.w),
+                            __int_as_float(hb.x), __int_as_float(hb.y), __int_as_float(hb.z), __int_as_float(hb.w)};
         uint32_t am = 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
