@@ -735,7 +735,7 @@ struct BlockArgs {
   float* hs;               // gate/up: their scales [N / 256, T topk]
   uint16_t* y16;           // down: weighted rows in sorted order [T topk, N], float16 times ys
   float* ys;               // down: [blocks of N, T topk]
-  int topk, N, K, tiles_m, tiles_n;
+  int topk, N, K, tiles_m, tiles_n;  // topk: gate/up
 };
 
 template <int BM, int BN, int WGM, int WGN, int MODE, int NS>
@@ -948,11 +948,12 @@ void block_tiled(const BlockArgs p) {
   const int a_base = (BN + wm * C::WM) * 128, b_base = wn * C::WN * 128, s_base = C::kCodes + (wm * C::WM + r16) * 4;
   // weight blocks of the wave's column tiles (gate/up: even tiles are gate columns, odd ones up columns)
   const float* sBe = p.sB + (int64_t)e * nb * nk;
-  constexpr int kBlocks = MODE == kGateUp ? 2 : 128 % C::WN == 0 ? 1 : C::SN;
+  constexpr int kBlocks = MODE == kGateUp ? 2 : 1;
+  static_assert(MODE == kGateUp || 128 % C::WN == 0, "a wave's columns lie in one block");
   ScalarPtr sBp[kBlocks];
 #pragma unroll
   for (int i = 0; i < kBlocks; ++i) {
-    const int b = MODE == kGateUp ? nt + i * (nb >> 1) : min((n0 + wn * C::WN + i * 16) >> 7, nb - 1);
+    const int b = MODE == kGateUp ? nt + i * (nb >> 1) : min((n0 + wn * C::WN) >> 7, nb - 1);
     sBp[i] = (ScalarPtr)(sBe + (int64_t)b * nk);
   }
   v4f acc[C::SN][C::SM];
@@ -993,7 +994,6 @@ void block_tiled(const BlockArgs p) {
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (MODE == kDown) {
-      static_assert(MODE != kDown || kBlocks == 1, "a wave's columns lie in one block");
 #pragma unroll
       for (int j = 0; j < C::SM; ++j) size[j] = __builtin_fmaf(fabsf(sx[j]), fabsf(sw[0]), size[j]);
     }
@@ -1424,7 +1424,6 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
   p.B = w;
   p.sB = sw;
   p.y = y;
-  p.topk = 1;
   p.N = (int)N;
   p.K = (int)K;
   // By the number of tiles. One workgroup a CU, waves splitting K, while 32 x 32 or
@@ -1639,7 +1638,6 @@ hipError_t launch_block_moe(const uint8_t* xq, const float* xs, const int32_t* i
   d.tw = r.w;
   d.y16 = y;
   d.ys = ys;
-  d.topk = (int)topk;
   d.N = (int)H;
   d.K = (int)I;
   tiles = max_tiles(n, E, r.bm[1]);
