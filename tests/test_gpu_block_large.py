@@ -139,3 +139,22 @@ def test_captured_passes(T, E):
         torch.ones(1 << 18, device="cuda").sum()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(oq, wq) and torch.equal(osc, wsc), i
+
+
+@pytest.mark.parametrize("E1,E2", [(2, 8), (7, 20), (100, 700)])
+def test_one_expert_takes_all(E1, E2):
+    """Every copy goes to one expert: the same bits whichever it is and however many others get nothing (sizes on
+    which both calls run the same kernels; 700 experts take the order of three launches)."""
+    T, H, I = 3000, 272, 256
+    g = _gen(90 + E2)
+    one = _experts(1, H, I, g)
+    q, s = w8.quantize_blocks(_normal((T, H), g))
+    tw = torch.rand(T, 1, device="cuda", generator=g)
+    outs = []
+    for E, e in ((E1, E1 - 1), (E2, 0), (E2, E2 - 1)):
+        w = [torch.full((E, *t.shape[1:]), 0x7F if t.dtype is torch.uint8 else float("nan"), dtype=t.dtype, device="cuda") for t in one]
+        for big, t in zip(w, one):
+            big[e] = t[0]
+        outs.append(w8.moe_w8a8_block_grouped(q, s, torch.full((T, 1), e, dtype=torch.int32, device="cuda"), tw, *w))
+    assert bool(outs[0].isfinite().all()) and bool(outs[0].any())
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])

@@ -1501,7 +1501,6 @@ static hipError_t launch_block_few(const BlockFewArgs& a, uint16_t* small, hipSt
   return hipGetLastError();
 }
 
-// counts | offsets | perm | route scratch | codes of h | their scales | slot -> row | y | its scales
 // Rows of the gate/up and the down tiles. One stage, three workgroups a CU. Groups of
 // up to 48 rows on average wait for their weights more than for the matrix unit: 32
 // rows a tile, and the exact sums of the widened codes; larger ones 64 rows on FP8
