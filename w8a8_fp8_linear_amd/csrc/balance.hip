@@ -136,12 +136,12 @@ struct Tokens {
     TL* grad = static_cast<TL*>(p.grad);
     const int l = lane % LANES;
     const uint64_t group = LANES == 64 ? ~0ull : ((1ull << (LANES & 63)) - 1) << (lane - l);
-    float x[UT][NC][4], inv[UT], dot[UT];
-    bool here[UT], low[UT];
+    float x[UT][NC][4], inv[UT], dot[UT];  // x inv: p_j times its slope
+    bool here[UT];
 #pragma unroll
     for (int u = 0; u < UT; ++u) {
       here[u] = (__ballot(id[u] >= 0 && id[u] < p.E) & group) != 0 && t0 + (int64_t)u * step < p.L;
-      float m = sigmoid ? 0.f : -INFINITY, z = 0.f;
+      float m = sigmoid ? 0.f : -INFINITY, z = 0.f, d = 0.f;
 #pragma unroll
       for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -158,13 +158,22 @@ struct Tokens {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float v = x[u][i][r];
-          x[u][i][r] = sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : __expf(v - m);
-          z += x[u][i][r];
+          if (sigmoid) {
+            // d p_j / d l_j is p_j (1 - sigmoid(l_j)) for sigmoids divided by their sum; from one
+            // half on 1 - sigmoid(l) is e^-l sigmoid(l), which a subtraction would lose
+            const float t = __expf(-v), y = __builtin_amdgcn_rcpf(1.0f + t);
+            z += y;
+            d = __builtin_fmaf(w[i][r], y, d);
+            x[u][i][r] = y * (y < 0.5f ? 1.0f - y : t * y);
+          } else {
+            x[u][i][r] = __expf(v - m);
+            z += x[u][i][r];
+            d = __builtin_fmaf(w[i][r], x[u][i][r], d);
+          }
         }
       z = group_sum<LANES>(z);
       // sigmoids too small for float32, where sigmoid(v) is e^v: the same p from a softmax
-      low[u] = sigmoid && z < 0x1p-60f;
-      if (low[u]) {
+      if (sigmoid && z < 0x1p-60f) {
         m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
@@ -172,22 +181,18 @@ struct Tokens {
           for (int r = 0; r < 4; ++r) m = fmaxf(m, value(u, i, r, 4 * (l + LANES * i), p.E));
         m = group_max<LANES>(m);
         m = m == -INFINITY ? 0.f : m;
-        z = 0.f;
+        z = d = 0.f;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             x[u][i][r] = __expf(value(u, i, r, 4 * (l + LANES * i), p.E) - m);
             z += x[u][i][r];
+            d = __builtin_fmaf(w[i][r], x[u][i][r], d);
           }
         z = group_sum<LANES>(z);
       }
       inv[u] = z > 0.f ? 1.0f / z : 0.f;
-      float d = 0.f;
-#pragma unroll
-      for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) d = __builtin_fmaf(w[i][r], x[u][i][r], d);
       dot[u] = group_sum<LANES>(d) * inv[u];
       if (here[u]) sum += (double)dot[u] + (z > 0.f ? (double)base : 0.0);
     }
@@ -201,11 +206,7 @@ struct Tokens {
         const int e = 4 * (l + LANES * i);
         float d[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          // d p_j / d l_j = p_j (1 - sigmoid(l_j)) for sigmoids divided by their sum
-          const float v = x[u][i][r], slope = sigmoid && !low[u] ? 1.0f - v : 1.0f;
-          d[r] = here[u] ? v * inv[u] * slope * (w[i][r] - dot[u]) : 0.f;
-        }
+        for (int r = 0; r < 4; ++r) d[r] = here[u] ? x[u][i][r] * inv[u] * (w[i][r] - dot[u]) : 0.f;
         TL* dst = grad + (row0 + t) * p.E + e;
         if constexpr (VEC && sizeof(TL) == 4) {
           if (e < p.E) *reinterpret_cast<float4*>(dst) = make_float4(d[0], d[1], d[2], d[3]);
