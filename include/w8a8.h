@@ -804,8 +804,8 @@ int w8a8_block_linear(const uint16_t* x_bf16, const uint8_t* w_q, const float* w
  *             the next pass's input
  *   workspace  moe_w8a8_block_workspace_bytes bytes; calls that may overlap
  *              need one each
- *   Limits as moe_w8a8_grouped (H a multiple of 16, I of 128), and fewer than
- *   2^21 tiles of 64 copies x 128 columns.
+ *   Limits as moe_w8a8_grouped (H a multiple of 16, I of 128), I < 2^24, and
+ *   fewer than 2^21 tiles of 64 copies x 128 columns.
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, WORKSPACE, DEVICE,
  *         LAUNCH.
  */

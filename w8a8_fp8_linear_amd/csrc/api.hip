@@ -813,6 +813,7 @@ int check_block_moe(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk) {
   const int c = check_moe_shape(T, H, I, E, topk);
   if (c != W8A8_OK) return c;
   if (I % kFusedIMultiple != 0) return W8A8_ERR_UNSUPPORTED;
+  if (I >= int64_t(1) << 24) return W8A8_ERR_UNSUPPORTED;  // offsets inside 128 rows of h fit 31 bits
   if (!mul_ok(T * topk, H) || !mul_ok(T * topk * H, 4)) return W8A8_ERR_BAD_SHAPE;
   // a grid holds fewer than 2^32 threads: at most 8 workgroups of 256 for 64 copies and 128 columns
   if ((T * topk / 64 + E + 1) * (blocks128(H) + blocks128(I)) >= int64_t(1) << 21 || T * blocks128(H) >= int64_t(1) << 27)
