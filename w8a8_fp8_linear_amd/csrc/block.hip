@@ -1076,12 +1076,13 @@ void block_tiled(const BlockArgs p) {
     for (int j = 0; j < C::SM; ++j) {
       const int ml = wm * C::WM + j * 16 + r16;
       const float w = row_w[ml];
-      // size < 2^(bs - 126), |w| < 2^(bw - 126): the row's values stay below 2^e, with a factor
-      // of two for the roundings of the sums, whatever of the product might overflow
-      const int bs = (int)(__float_as_uint(size[j]) >> 23), bw = (int)(__float_as_uint(w) >> 23) & 0xFF;
-      const int e = bs + bw - 252 + 26;  // 2 * 128 * 448^2 < 2^26
-      // 2^(15 - e) and back, which neither take w out of range; infinite and NaN scales keep 1
-      const int up = bs == 255 || bw == 255 ? 0 : max(-113, min(15 - e, min(126, 253 - bw)));
+      // size < 2^(bs - 126), 2 * 128 * 448^2 < 2^26 with a factor of two for the roundings of the sums, and
+      // a float32 is below 2^128: |a| < 2^ea. |w| < 2^(bw - 126): the row's values stay below 2^e.
+      const int bs = (int)(__float_as_uint(size[j]) >> 23) & 0xFF, bw = (int)(__float_as_uint(w) >> 23) & 0xFF;
+      const int ea = min(bs - 126 + 26, 128), e = ea + bw - 126;
+      // 2^(15 - e) and back, which neither take w out of range: w 2^up is about 2^(14 - ea), a normal float32,
+      // also where the sum of the scales is infinite and the values are not
+      const int up = max(-113, min(15 - e, min(126, 253 - bw)));
       const float to = __uint_as_float((uint32_t)(127 + up) << 23), from = __uint_as_float((uint32_t)(127 - up) << 23);
       const int col = n0 + wn * C::WN;
       if (g == 0 && (col & 127) == 0 && ml < rows && col < N) p.ys[(int64_t)(col >> 7) * p.a_rows + row0 + ml] = from;
