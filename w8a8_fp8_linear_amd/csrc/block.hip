@@ -228,9 +228,12 @@ __global__ __launch_bounds__(256) void block_skinny(const uint8_t* __restrict__ 
         }
       }
     }
+    // XL: the wait below counts on the weights' loads, 2 U NT of them, to be the last that were issued
+    if constexpr (XL) __builtin_amdgcn_sched_barrier(0);
     skinny_weights(rW, 16, sWrow, kb0, nk, K, wave, r16, g, wf, sw);
     if constexpr (XL) {
-      // the rows have landed once only the weight loads are outstanding
+      // the loads return in order: the rows have landed once only the weights' are outstanding
+      __builtin_amdgcn_sched_barrier(0);
       wait_vmcnt<2 * U * NT>();
 #pragma unroll
       for (int u = 0; u < U; ++u)
