@@ -273,6 +273,8 @@ __global__ __launch_bounds__(256) void gemm_skinny(const uint8_t* __restrict__ A
         }
       }
     }
+    // XL: the wait below counts on the weights' loads, 2 U NT of them, to be the last that were issued
+    if constexpr (XL) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k0 = (kt + 4 * u) << 7;
@@ -301,7 +303,8 @@ __global__ __launch_bounds__(256) void gemm_skinny(const uint8_t* __restrict__ A
       }
     }
     if constexpr (XL) {
-      // the input pieces have landed once only the weight loads are outstanding
+      // the loads return in order: the input pieces have landed once only the weights' are outstanding
+      __builtin_amdgcn_sched_barrier(0);
       wait_vmcnt<2 * U * NT>();
 #pragma unroll
       for (int u = 0; u < U; ++u)
