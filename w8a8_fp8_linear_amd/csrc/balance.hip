@@ -306,9 +306,9 @@ __global__ __launch_bounds__(kThreads) void balance_main(const BalanceArgs p, in
   const int n = hist[p.E];
   const float base = n > 0 ? p.coef / ((float)p.S * (float)n) : 0.f;
   for (int e = tid; e < p.E; e += kThreads) {
-    // (f - 1) * base, f - 1 = (c E - k n) / (k n), the difference from whole numbers
+    // (f - 1) * base, f - 1 = (c E - k n) / (k n) from whole numbers, rounded to float32 once
     const double kn = (double)p.k * (double)n;
-    up[e] = n > 0 ? base * ((float)((double)hist[e] * (double)p.E - kn) / (float)kn) : 0.f;
+    up[e] = n > 0 ? base * (float)(((double)hist[e] * (double)p.E - kn) / kn) : 0.f;
     if (gi == 0) p.counts[(int64_t)s * p.E + e] = hist[e];
   }
   __syncthreads();
