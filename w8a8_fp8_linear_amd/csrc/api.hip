@@ -786,7 +786,7 @@ int64_t blocks128(int64_t n) { return (n + 127) / 128; }
 
 int check_quant_blocks(int64_t M, int64_t K) {
   if (M < 0 || K < 0 || !mul_ok(M, K) || !mul_ok(M * K, 2)) return W8A8_ERR_BAD_SHAPE;
-  // 16 rows x 4 blocks a workgroup; the grid's second extent is 16 bits wide
+  // 16 rows x 4 blocks a workgroup of 256 threads, fewer than 2^32 threads
   if (K == 0 || K % 16 != 0 || K > (int64_t(1) << 24) || M > (int64_t(1) << 26)) return W8A8_ERR_UNSUPPORTED;
   if (((M + 15) / 16) * ((blocks128(K) + 3) / 4) >= int64_t(1) << 24) return W8A8_ERR_UNSUPPORTED;
   return W8A8_OK;

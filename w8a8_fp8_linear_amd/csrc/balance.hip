@@ -380,7 +380,9 @@ int tokens_at_once(int64_t E) {
   return kThreads / lanes * (E <= 256 ? 4 : 1);
 }
 
-// One workgroup for a single sequence of at most two rounds of its tokens.
+// One workgroup for a single sequence of at most two rounds of its tokens (in a graph, one launch of
+// one workgroup and two launches: 64 experts, one round 7.7 and 11.7 us, two 11.1 and 12.3, three 15.3
+// and 12.4; 512 experts 5.8 and 9.9, 7.8 and 10.6, 9.8 and 10.6).
 bool balance_one(int64_t L, int64_t S, int64_t E) { return S == 1 && L <= 2 * tokens_at_once(E); }
 
 template <typename TL, int LANES, int NC, bool VEC>

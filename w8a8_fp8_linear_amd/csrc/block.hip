@@ -1108,9 +1108,10 @@ void block_tiled(const BlockArgs p) {
         const uint4 v = *reinterpret_cast<const uint4*>(smem + row * C::kEpiStride + col * 2);
         uint4* const to = reinterpret_cast<uint4*>(p.y16 + (int64_t)(row0 + row) * N + n0 + col);
         // Rows that the caches may keep for the combine, unless a group's rows outweigh its
-        // weights (tiles of 128 rows) and would drive these out (whole passes, kept and
-        // streamed: 4096 tokens, top-4 of 192, H 1024 120 and 125 us; top-8 of 64, H 2048
-        // 217 and 202).
+        // weights (tiles of 128 rows) and would drive these out (whole passes in a graph, kept
+        // and streamed. Tiles of 64 rows: top-8 of 64, H 2048, 2048 tokens 130 and 136 us; top-4
+        // of 192, H 1024, 4096 tokens 110 and 113. Tiles of 128 rows: top-8 of 64, 4096 tokens
+        // 215 and 217, 8192 tokens 377 and 372).
         if constexpr (BM >= 128)
           store16_nt(to, v);
         else
@@ -1354,8 +1355,9 @@ __global__ __launch_bounds__(kRouteThreads) void block_route_rest(const RouteArg
 }
 
 // One launch up to here, where LDS holds the counters, and three beyond, two of them
-// the other formats' (whole passes, H 256, I 128, one launch and two: 8192 slots,
-// 64 experts 24.8 and 28.5 us, 65536 slots 48.8 and 53.1, of 8 experts 59.7 and 62.1).
+// the other formats' (whole passes in a graph, H 256, I 128, one launch and three: 8192 slots,
+// 64 experts 25.1 and 30.2 us, 65536 slots 61.8 and 68.8, of 8 experts 60.8 and 66.1, of
+// 512 experts 65.6 and 76.9).
 constexpr int64_t kRouteOneSlots = 65536, kRouteOneExperts = 512;
 
 bool route_one(int64_t n, int64_t E) { return n <= kRouteOneSlots && E <= kRouteOneExperts; }
@@ -1418,6 +1420,11 @@ hipError_t launch_quantize_weight_blocks(const uint16_t* w, int64_t E, int64_t N
 
 hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, uint16_t* y,
                              int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  // One tile of 16 weight rows a workgroup up to 4 rows, two up to 32. A second tile pays from
+  // some 6,000 weight rows on, and the more rows the more, because the two share the rows'
+  // fragments; fewer weight rows leave CUs idle (in a graph, one tile and two. 4 rows: 2048 x
+  // 2048 3.5 and 4.3 us, 8192 x 2048 5.2 and 5.1; 12 rows: 2048 x 2048 3.8 and 4.6, 8192 x 2048
+  // 5.6 and 5.3, 6144 x 4096 9.4 and 8.5, 16384 x 2048 8.6 and 7.5).
   if (M <= 4) return run_skinny<1, 1, false>(a, sa, w, sw, y, M, N, K, stream);
   if (M <= 16) return run_skinny<1, 2, false>(a, sa, w, sw, y, M, N, K, stream);
   if (M <= 32) return run_skinny<2, 2, true>(a, sa, w, sw, y, M, N, K, stream);
@@ -1430,16 +1437,17 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
   p.y = y;
   p.N = (int)N;
   p.K = (int)K;
-  // By the number of tiles. One workgroup a CU, waves splitting K, while 32 x 32 or
-  // 64 x 32 tiles are no more than the CUs (301 x 1040 x 1056: 5.9 us against 7.1
-  // for 64 x 64 tiles and 10.3 for 128 x 128); 64 x 64 tiles with two stages up to two
-  // a CU (512 x 2048 x 2048: 10.5; K split 14.6; one stage 11.5), with one up to three
-  // (512 x 6144 x 2048: 13.1; two stages 19.0); 64 x 128 up to three (1024 x 6144 x
-  // 2048: 18.9; 64 x 64 24.0; 128 x 128 19.3). Beyond, rounds of the GPU: 768 tiles of
-  // 128 x 128 or 512 of 128 x 256, whose round takes about 1.45 times as long (4096 x
-  // 6144 x 2048, 2 rounds each: 53.2 against 59.2 us; 8192 x 2048 x 6144, 2 against 1:
-  // 104.8 against 93.9 us). Two groups of waves in turns on 256 x 192 tiles, as the
-  // product with row scales has them, took 54.8 us and 129.9 us.
+  // By the number of tiles (times of the product alone in a graph). One workgroup a CU, waves
+  // splitting K, while 32 x 32 or 64 x 32 tiles are no more than the CUs (64 x 1024 x 2048:
+  // 6.8 us in 32 x 32 against 7.9 in 64 x 64 of two stages and 7.4 of one; 301 x 1040 x 1056: 5.4
+  // in 64 x 32 against 6.1 and 5.8, 128 x 128 10.0; 256 x 2048 x 2048, the last of these: 8.7
+  // against 8.2 and 7.8); 64 x 64 tiles with two stages up to two a CU (512 x 2048 x 2048: 9.8; K
+  // split 14.1; one stage 10.7), with one up to three (512 x 6144 x 2048: 12.5; two stages 18.4);
+  // 64 x 128 up to three (1024 x 6144 x 2048: 18.4; 64 x 64 23.8; 128 x 128 18.6). Beyond,
+  // rounds of the GPU: 768 tiles of 128 x 128 or 512 of 128 x 256, whose round takes about 1.3
+  // to 1.45 times as long (4096 x 6144 x 2048, 2 rounds each: 54 against 68 us; 8192 x 2048 x
+  // 6144, 2 against 1: 107 against 98 to 103). Two groups of waves in turns on 256 x 192 tiles,
+  // as the product with row scales has them, were 3 % slower in the one and 38 % in the other.
   const auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
   if (tiles(32, 32) <= 256) return run_ksplit<2, 2, 3>(a, sa, w, sw, y, M, N, K, stream);
   if (tiles(64, 32) <= 256) return run_ksplit<4, 2, 1>(a, sa, w, sw, y, M, N, K, stream);
@@ -1451,14 +1459,18 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
   return run_tiled<128, 128, 2, 2, kDense, 3, 1>(p, (M + 127) / 128, stream);
 }
 
-// Rows that are quantised inside the product, by every workgroup for itself:
-// up to 8, or 16 of at most one round of columns (one launch, 9.5 us, against
-// 9.3 us in two for 12 rows of 8192 x 2048; 17.9 against 13.2 us for 6144 x 4096,
-// 24 rows of 6160 x 2048 14.6 against 9.1 us).
+// Rows that are quantised inside the product, by every workgroup for itself: up to 8, or 16 of at
+// most one round of columns. In a graph, one launch and two: 8 rows of 8192 x 2048 6.4 us either
+// way; 12 rows 8.9 and 8.3, where the one call takes the host 3 to 4 us less; 12 rows of 6144 x 4096 17.0 and 11.5;
+// 24 rows of 6160 x 2048 14.6 and 8.5.
 static bool block_fused(int64_t M, int64_t K) { return M <= 8 || (M <= 16 && K <= kSkinnyCols); }
 
 hipError_t launch_block_linear(const uint16_t* x, const uint8_t* w, const float* sw, uint16_t* y, int64_t M, int64_t N,
                                int64_t K, void* ws, hipStream_t stream) {
+  // One tile of 16 weight rows a workgroup up to 4 rows, two beyond, which halve the quantiser's
+  // work (in a graph, one tile and two. 4 rows: 2048 x 2048 4.4 and 4.5 us, 8192 x 2048 5.4 and
+  // 5.2; 8 rows: 2048 x 2048 5.2 and 5.8, 8192 x 2048 7.4 and 6.4, 6144 x 4096 12.5 and 11.1; 16
+  // rows: 2048 x 2048 7.4 and 8.4, 8192 x 2048 11.3 and 9.2).
   if (M == 1) return run_skinny_bf16<1, 1>(x, w, sw, y, M, N, K, stream);
   if (M <= 4) return run_skinny_bf16<4, 1>(x, w, sw, y, M, N, K, stream);
   if (M <= 8) return run_skinny_bf16<8, 2>(x, w, sw, y, M, N, K, stream);
@@ -1475,16 +1487,19 @@ size_t block_linear_workspace_bytes(int64_t M, int64_t K) {
   return (size_t)(align256(M * K) + align256((K + 127) / 128 * M * 4));
 }
 
-// Whether the pass takes the kernels for groups of few rows: up to 8 on average,
-// and few ids for every workgroup to look through (whole passes in tiles and here, I
-// 512: top-8 of 64, H 2048, 16 tokens 49.4 and 43.3 us, 32 tokens 52.4 and 50.7, 48
-// tokens 53.2 and 57.0; top-4 of 192, H 1024, 37 tokens 44.4 and 42.7, 64 tokens 49.0
-// and 50.7, 96 tokens 53.4 and 63.0; top-2 of 8, H 1024, 32 tokens 27.6 and 17.2).
+// Whether the pass takes the kernels for groups of few rows: up to 8 on average, and few ids for
+// every workgroup to look through (whole passes in a graph, these kernels and tiles. I 512: top-8 of
+// 64, H 2048, 16 tokens 43 and 49 us, 32 tokens 51 and 52, 48 tokens 57 and 53; H 4096, 32 tokens 96
+// and 104; top-4 of 192, H 1024, 37 tokens 43 and 44, 64 tokens 51 and 49; top-2 of 8, H 1024, 32
+// tokens 17 and 28. I 1024: top-8 of 64, H 2048, 16 tokens 80 and 84, 32 tokens 90 and 88. I 1536,
+// top-4 of 16, H 4096: 32 tokens 75 and 83, 48 tokens 85 and 84, 64 tokens 104 and 84).
 static bool block_few(int64_t T, int64_t E, int64_t topk) { return T * topk <= kFewSlots && T * topk <= 8 * E; }
 
-// And of those, the ones whose down projection makes the sum too (H 1024, I 512,
-// top-4 of 128: 1 token 10.9 us against 13.4 us, 3 tokens 14.7 against 15.2, 6 tokens
-// 20.6 against 18.1; with a launch less the host takes 3 us less).
+// And of those, the ones whose down projection makes the sum too, a launch less, which takes the
+// host 3 us less (whole passes in a graph, two kernels and three. I 512, H 1024, top-4 of 128: 1 token
+// 9.1 and 10.5 us, 2 tokens 10.3 and 11.2, 4 tokens 15.0 and 14.0; top-8 of 64, H 2048: 1 token 13.3
+// and 14.5, 2 tokens 18.5 and 18.3; I 1536, top-4 of 16, H 4096: 1 token 22.4 and 24.6, 2 tokens
+// 33.7 and 34.9).
 static bool block_small(int64_t T, int64_t I, int64_t topk) {
   return T * topk <= kSmallSlots && T * topk * I <= kSmallCodes;
 }
@@ -1493,6 +1508,10 @@ static bool block_small(int64_t T, int64_t I, int64_t topk) {
 static hipError_t launch_block_few(const BlockFewArgs& a, uint16_t* small, hipStream_t stream) {
   const int groups = a.by_slot ? a.n : a.E;
   const dim3 gate((unsigned)(groups * (a.I / 16)));
+  // steps of 128 columns a wave has in flight: two rounds of them are 1024 columns, which four would
+  // take in one half empty (whole passes in a graph, two and four: 37 tokens, top-4 of 192, H 1024
+  // 46.8 and 53.7 us, 1 token, top-4 of 128, H 1024 9.0 and 9.5, H 1536 10.1 and 9.9; 1 token, top-8
+  // of 64, H 2048 13.7 and 13.3, H 4096 17.2 and 16.9; 16 tokens, H 4096 82.0 and 83.8)
   if (a.H <= 1024)
     hipLaunchKernelGGL(block_few_gate_up<2>, gate, dim3(256), 0, stream, a);
   else
@@ -1505,17 +1524,23 @@ static hipError_t launch_block_few(const BlockFewArgs& a, uint16_t* small, hipSt
   return hipGetLastError();
 }
 
-// Rows of the gate/up and the down tiles. One stage, three workgroups a CU. Groups of
-// up to 48 rows on average wait for their weights more than for the matrix unit: 32
-// rows a tile, and the exact sums of the widened codes; larger ones 64 rows on FP8
-// (whole passes, I 512, 32 rows and 64: top-8 of 64, H 2048, 384 tokens 56.7 and 58.8
-// us, 512 tokens 65.4 and 60.6, 1024 tokens 90.7 and 74.4; top-4 of 192, H 1024, 1024
-// tokens 71.2 and 71.3, 2048 tokens 86.1 and 83.4, 3000 tokens 101 and 92).
+// Rows of the gate/up and the down tiles. One stage, three workgroups a CU. Groups of up to 48 rows
+// on average take 32 rows a tile and the near-exact sums of the widened codes; larger ones 64 rows on
+// FP8. The narrow tiles are the faster for up to some 20 rows, where the weights are the bound, and
+// at most 13 % slower up to 48, where their sums are what they are kept for: a pass is off by 0.0017
+// of its norm instead of 0.0020 to 0.0025. (Whole passes in a graph, 32 rows and 64, for 16, 32, 48 and 64 rows a
+// group: top-8 of 64, H 2048, I 512 57 and 60, 63 and 62, 72 and 72, 77 and 72 us; I 1024 92 and 94, 99
+// and 97, 113 and 112, 125 and 116; top-4 of 192, H 1024, I 512 74 and 75, 84 and 79, 91 and 88, 103 and
+// 96; top-4 of 16, H 4096, I 1536 88 and 89, 101 and 91, 97 and 93, 103 and 108.) Widened sums in the
+// 64-row tiles cost more: 4096 tokens, top-8 of 64 take 269 us against 211 (two workgroups a CU; at
+// three the registers spill, 608).
 static bool block_narrow(int64_t T, int64_t E, int64_t topk) { return T * topk <= 48 * E; }
 static int gate_rows(int64_t T, int64_t E, int64_t topk) { return block_narrow(T, E, topk) ? 32 : 64; }
-// 64 x 128 and 128 x 128 tiles: top-8 of 64, 2048 tokens 116.9 and 115.7 us, 3000
-// tokens 158.8 and 148.8, 4096 tokens 209 and 188; top-4 of 192, 16384 tokens 240 and
-// 246 (the larger stream their rows out).
+// 64 x 128 and 128 x 128 tiles, for 128, 256, 350, 512 and 1024 rows a group (whole passes in a graph):
+// top-8 of 64, H 2048, I 512 90 and 96, 130 and 134, 150 and 155, 209 and 208, 369 and 356 us; I 1024 143 and
+// 148, 208 and 206, 255 and 246, 349 and 336, 633 and 599; top-4 of 192, H 1024, I 512 126 and 129, 190
+// and 192, 250 and 245, 346 and 334, 646 and 615; top-4 of 16, H 4096, I 1536 124 and 118, 178 and 172,
+// 209 and 197, 283 and 262, 510 and 456.
 static int down_rows(int64_t T, int64_t E, int64_t topk) {
   return block_narrow(T, E, topk) ? 32 : T * topk / E < 350 ? 64 : 128;
 }
