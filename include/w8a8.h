@@ -792,11 +792,11 @@ int w8a8_block_linear(const uint16_t* x_bf16, const uint8_t* w_q, const float* w
  * and u on the BF16 matrix unit (codes are exact in BF16), near float32; the
  * others, as w8a8_block_gemm, on the FP8 unit, where some 4 in 10,000 of the
  * codes of h come out as the neighbouring one: a pass is then off by 0.0020 to
- * 0.0025 of its norm instead of the 0.0017 of the last rounding. With more than 256 or 8 E routed copies the
- * copies topk_w * (W2[e] . h) are kept in 16 bits before they are added, float16
- * times a power of two for each 128 columns of a copy: off by at most 2^-11 of
- * the value, or 2^-12 of topk_w times the sum over h's blocks of the products of
- * their scales where that is more.
+ * 0.0025 of its norm instead of the 0.0017 of the last rounding. With more than
+ * 256 or 8 E routed copies the copies topk_w * (W2[e] . h) are kept in 16 bits
+ * before they are added, float16 times a power of two for each 128 columns of a
+ * copy: off by at most 2^-11 of the value, or 2^-12 of topk_w times the sum over
+ * h's blocks of the products of their scales where that is more.
  *   x_q [T, H]  x_scale [ceil(H/128), T]
  *   w13_q [E, 2I, H] (rows 0..I-1 gate, I..2I-1 up)  w13_scale [E, 2I/128, ceil(H/128)]
  *   w2_q [E, H, I]  w2_scale [E, ceil(H/128), I/128]

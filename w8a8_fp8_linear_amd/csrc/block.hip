@@ -1460,9 +1460,9 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
 }
 
 // Rows that are quantised inside the product, by every workgroup for itself: up to 8, or 16 of at
-// most one round of columns. In a graph, one launch and two: 8 rows of 8192 x 2048 6.4 us either
-// way; 12 rows 8.9 and 8.3, where the one call takes the host 3 to 4 us less; 12 rows of 6144 x 4096 17.0 and 11.5;
-// 24 rows of 6160 x 2048 14.6 and 8.5.
+// most one round of columns. In a graph, one launch and two: 12 rows of 8192 x 2048 8.9 and 8.3 us,
+// where the one launch takes the host 3 to 4 us less; 12 rows of 6144 x 4096 17.0 and 11.5; 24 rows of
+// 6160 x 2048 14.6 and 8.5.
 static bool block_fused(int64_t M, int64_t K) { return M <= 8 || (M <= 16 && K <= kSkinnyCols); }
 
 hipError_t launch_block_linear(const uint16_t* x, const uint8_t* w, const float* sw, uint16_t* y, int64_t M, int64_t N,
@@ -1508,8 +1508,8 @@ static bool block_small(int64_t T, int64_t I, int64_t topk) {
 static hipError_t launch_block_few(const BlockFewArgs& a, uint16_t* small, hipStream_t stream) {
   const int groups = a.by_slot ? a.n : a.E;
   const dim3 gate((unsigned)(groups * (a.I / 16)));
-  // steps of 128 columns a wave has in flight: two rounds of them are 1024 columns, which four would
-  // take in one half empty (whole passes in a graph, two and four: 37 tokens, top-4 of 192, H 1024
+  // Steps of 128 columns that a wave has in flight: a round of the four waves is 1024 columns with two
+  // and 2048 with four, half of it empty up to 1024 (whole passes in a graph, two and four: 37 tokens, top-4 of 192, H 1024
   // 46.8 and 53.7 us, 1 token, top-4 of 128, H 1024 9.0 and 9.5, H 1536 10.1 and 9.9; 1 token, top-8
   // of 64, H 2048 13.7 and 13.3, H 4096 17.2 and 16.9; 16 tokens, H 4096 82.0 and 83.8)
   if (a.H <= 1024)
